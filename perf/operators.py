@@ -107,7 +107,7 @@ def draw(rng):
         batch = _log(rng, 1, 16)
         high = _log(rng, 1, 120000 // batch)
         c = {"op": "read", "hkv": hkv, "d": d, "ctx": "%dx%d-%d" % (batch, _log(rng, 1, high), high),
-             "skip": rng.randrange(0, 100)}
+             "skip": rng.randrange(0, min(100, high))}
     c.pop("name", None)
     return c
 
