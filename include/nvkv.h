@@ -385,6 +385,124 @@ nvkv_status nvkv_pages_restore_k8v4(const nvkv_cache *cache, const int32_t *page
                                     const int32_t *slot_ids, int32_t n, const void *arena,
                                     int64_t num_slots, int32_t *err_word, nvkv_stream_t stream);
 
+/* Masked and modified scores.  Attention layers that cap their scores, bias
+ * them by distance or see only part of the cache use the *_mod calls: the
+ * same attention over the same caches, with the scores of query i (position
+ * p, query head hq) and key j
+ *     x = sm_scale * q_i . k_j
+ *     x = softcap * tanh(x / softcap)                      if softcap > 0
+ *     x = x - alibi_slopes[hq] * |p - j|                   if alibi_slopes
+ * and the keys lo <= j < hi visible to it, where
+ *     lo = max(0, s, p - window + 1)        (s = the query's key_starts entry;
+ *                                            the window term if window > 0)
+ *     hi = p + 1                            the causal bound, or, when p lies
+ *                                           inside the sequence's prefix P =
+ *                                           prefix_lens[b] (p < P),
+ *     hi = P, at most p + window            queries of the prefix see all of
+ *                                           it, in both directions
+ * and hi <= kv_len always.  The interval may be empty (a document that starts
+ * after p): the row's output is then 0.  Keys outside the interval are not
+ * looked at: their pages may be absent from the page table (-1, freed, or
+ * reused by another sequence) as long as no query of the call sees a key of
+ * the page, and no bad page id is reported for them.
+ *   softcap:      > 0 and finite, or 0 for none.
+ *   window:       > 0: that many keys up to the query's own; 0: none.
+ *   alibi_slopes: device float [Hq], or NULL.
+ *   prefix_lens:  device int32 [batch], or NULL (values <= 0: no prefix).
+ *   key_starts:   device int32, first key that may be seen, or NULL: one per
+ *                 sequence [batch] in the decode calls (the T newest queries
+ *                 share it), one per query row [total_q] in the prefill calls
+ *                 (packed documents: the position where the row's document
+ *                 starts).  Values <= 0 leave the row unbounded. */
+typedef struct nvkv_score_mod {
+    float softcap;
+    int32_t window;
+    const float *alibi_slopes;
+    const int32_t *prefix_lens;
+    const int32_t *key_starts;
+} nvkv_score_mod;
+
+/* nvkv_decode_attn followed by nvkv_combine (same arguments, layouts,
+ * workspace and checks), with the scores of `mod`.  The split plan covers
+ * only the 128-token units that a query of the sequence can see, so a window
+ * or a document start bounds what is read.  softcap, window and the pointers
+ * are read when the call is made; the arrays by the kernels.
+ *
+ * nvkv_decode_attn_mod_k8v4: the same over a K8V4 cache. */
+nvkv_status nvkv_decode_attn_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
+                                 int32_t T, int32_t num_q_heads, float sm_scale,
+                                 const nvkv_score_mod *mod, int32_t num_splits, void *workspace,
+                                 size_t workspace_bytes, void *out, nvkv_stream_t stream);
+nvkv_status nvkv_decode_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs *seqs,
+                                      const void *q, int32_t T, int32_t num_q_heads,
+                                      float sm_scale, const nvkv_score_mod *mod,
+                                      int32_t num_splits, void *workspace,
+                                      size_t workspace_bytes, void *out, nvkv_stream_t stream);
+
+/* nvkv_prefill_attn_split (same arguments, layouts, workspace and checks),
+ * with the scores of `mod`.  A prefix is seen in both directions as far as
+ * it is cached: put it into one chunk.
+ *
+ * nvkv_prefill_attn_mod_k8v4: the same over a K8V4 cache. */
+nvkv_status nvkv_prefill_attn_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
+                                  const int32_t *cu_q, int32_t total_q, int32_t max_q,
+                                  int32_t num_q_heads, float sm_scale, const nvkv_score_mod *mod,
+                                  int32_t num_splits, void *workspace, size_t workspace_bytes,
+                                  void *out, nvkv_stream_t stream);
+nvkv_status nvkv_prefill_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs *seqs,
+                                       const void *q, const int32_t *cu_q, int32_t total_q,
+                                       int32_t max_q, int32_t num_q_heads, float sm_scale,
+                                       const nvkv_score_mod *mod, int32_t num_splits,
+                                       void *workspace, size_t workspace_bytes, void *out,
+                                       nvkv_stream_t stream);
+
+/* nvkv_append_rope with rotary positions on several axes, as image and video
+ * tokens have them (time, height, width), and the queries' rotation in the
+ * same launch.
+ *   rope_cs, max_pos, rotary_dim: the table of nvkv_rope_table.
+ *   positions:    device int32 [num_axes][total_new]: the position of every
+ *                 new row on every axis, 0 <= position < max_pos.  (Where the
+ *                 row goes in the cache is kv_lens and cu_new's matter alone.)
+ *   num_axes:     1 .. 4.
+ *   axis_of_pair: HOST array of rotary_dim/2 bytes, each < num_axes, read
+ *                 before the call returns: pair i (elements i and i +
+ *                 rotary_dim/2) turns by table row
+ *                 positions[axis_of_pair[i]][row].  Sections in a row and
+ *                 interleaved axes are both just such a list.
+ *   q:            device bf16 [total_new][Hq][D], rotated into q_out (same
+ *                 shape; q_out = q is allowed) and rounded once to bf16, or
+ *                 NULL (then q_out and num_q_heads are not used).
+ * The rotation is that of nvkv_append_rope.  A row with a position outside
+ * the table on any axis sets NVKV_DEVERR_LENGTH and is left out: none of its
+ * K, V and q_out is written.  A row on a bad page sets NVKV_DEVERR_PAGE_ID;
+ * its K and V are left out, its query is rotated all the same. */
+nvkv_status nvkv_append_rope_axes(const nvkv_cache *cache, const nvkv_seqs *seqs,
+                                  const void *k_new, const void *v_new, const int32_t *cu_new,
+                                  int32_t total_new, int32_t max_new, const float *rope_cs,
+                                  int32_t max_pos, int32_t rotary_dim, const int32_t *positions,
+                                  int32_t num_axes, const uint8_t *axis_of_pair, const void *q,
+                                  int32_t num_q_heads, void *q_out, nvkv_stream_t stream);
+
+/* Read cached rows back as bf16: rows cu_rows[b] .. cu_rows[b+1]-1 of k_out
+ * and v_out (device bf16 [total_rows][Hkv][D]) get the K and V rows of
+ * positions starts[b] .. starts[b]+n_b-1 of sequence b, n_b = cu_rows[b+1] -
+ * cu_rows[b].  NVFP4 values are bf16 numbers: the read is exact and appending
+ * the rows again gives the same bytes wherever the group's largest code is
+ * 6.  A K8V4 K value is rounded once to bf16.
+ *   starts:     device int32 [batch].
+ *   cu_rows:    device int32 [batch+1], cu_rows[0] = 0, non-decreasing.
+ *   total_rows: cu_rows[batch] (host copy); max_rows >= every n_b (host bound).
+ * A sequence whose rows are not all cached (starts[b] < 0 or starts[b] + n_b
+ * > kv_lens[b]) sets NVKV_DEVERR_LENGTH, a bad page NVKV_DEVERR_PAGE_ID; the
+ * rows concerned are left as they were.
+ * nvkv_read_rows_k8v4: the same from a K8V4 cache. */
+nvkv_status nvkv_read_rows(const nvkv_cache *cache, const nvkv_seqs *seqs, const int32_t *starts,
+                           const int32_t *cu_rows, int32_t total_rows, int32_t max_rows,
+                           void *k_out, void *v_out, nvkv_stream_t stream);
+nvkv_status nvkv_read_rows_k8v4(const nvkv_cache *cache, const nvkv_seqs *seqs,
+                                const int32_t *starts, const int32_t *cu_rows, int32_t total_rows,
+                                int32_t max_rows, void *k_out, void *v_out, nvkv_stream_t stream);
+
 /* Static description of a status code. */
 const char *nvkv_status_string(nvkv_status status);
 

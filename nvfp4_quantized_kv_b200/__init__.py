@@ -26,7 +26,8 @@ __all__ = [
     "nvkv_pages_spill", "nvkv_pages_restore", "nvkv_k8v4_page_bytes", "nvkv_append_k8v4",
     "nvkv_decode_attn_k8v4", "nvkv_prefill_attn_k8v4", "nvkv_pages_spill_k8v4",
     "nvkv_pages_restore_k8v4", "nvkv_prefill_attn_split", "nvkv_prefill_workspace_bytes",
-    "nvkv_prefill_num_splits",
+    "nvkv_prefill_num_splits", "ScoreMod", "nvkv_decode_attn_mod", "nvkv_prefill_attn_mod",
+    "nvkv_append_rope_axes", "nvkv_read_rows",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -53,6 +54,12 @@ class _SeqsC(ctypes.Structure):
                 ("max_kv_len", ctypes.c_int32), ("err_word", ctypes.c_void_p)]
 
 
+class _ScoreModC(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("key_starts", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -67,6 +74,10 @@ def library():
         L = ctypes.CDLL(library_path)
         vp, i32, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
         cp, sp = ctypes.POINTER(_CacheC), ctypes.POINTER(_SeqsC)
+        mp = ctypes.POINTER(_ScoreModC)
+        decode_mod = [cp, sp, vp, i32, i32, f32, mp, i32, vp, sz, vp, vp]
+        prefill_mod = [cp, sp, vp, vp, i32, i32, i32, f32, mp, i32, vp, sz, vp, vp]
+        read_rows = [cp, sp, vp, vp, i32, i32, vp, vp, vp]
         sig = {
             "nvkv_page_bytes": (sz, [i32, i32]),
             "nvkv_default_num_splits": (i32, []),
@@ -95,6 +106,14 @@ def library():
             "nvkv_append_k8v4": (ctypes.c_int, [cp, sp, vp, vp, vp, i32, i32, vp]),
             "nvkv_decode_attn_k8v4": (ctypes.c_int, [cp, sp, vp, i32, i32, f32, i32, vp, sz, vp]),
             "nvkv_prefill_attn_k8v4": (ctypes.c_int, [cp, sp, vp, vp, i32, i32, i32, f32, vp, vp]),
+            "nvkv_decode_attn_mod": (ctypes.c_int, decode_mod),
+            "nvkv_decode_attn_mod_k8v4": (ctypes.c_int, decode_mod),
+            "nvkv_prefill_attn_mod": (ctypes.c_int, prefill_mod),
+            "nvkv_prefill_attn_mod_k8v4": (ctypes.c_int, prefill_mod),
+            "nvkv_append_rope_axes": (ctypes.c_int, [cp, sp, vp, vp, vp, i32, i32, vp, i32, i32, vp,
+                                                     i32, ctypes.c_char_p, vp, i32, vp, vp]),
+            "nvkv_read_rows": (ctypes.c_int, read_rows),
+            "nvkv_read_rows_k8v4": (ctypes.c_int, read_rows),
             "nvkv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         }
         for name, (res, args) in sig.items():
@@ -414,3 +433,167 @@ def nvkv_prefill_attn_k8v4(cache: Cache, seqs: Seqs, q: torch.Tensor, cu_q: torc
         ctypes.byref(cache._c), ctypes.byref(seqs._c), _dev(q, torch.bfloat16, "q"),
         _dev(cu_q, torch.int32, "cu_q"), int(total_q), int(max_q), int(num_q_heads),
         float(sm_scale), _dev(out, torch.bfloat16, "out"), _stream(stream)), "nvkv_prefill_attn_k8v4")
+
+
+# ---- masked attention, several-axis rotary append, reading rows back -------
+# These calls also check that their tensors are on one device and as large as
+# the call makes them, and run on that device whatever the current one is.
+
+def _same_device(device: torch.device, *named) -> None:
+    for t, name in named:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+
+
+def _at_least(t: torch.Tensor, n: int, name: str) -> None:
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
+
+
+def _call(device: torch.device, fn, what: str, stream, *args) -> None:
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(stream))
+    _check(status, what)
+
+
+class ScoreMod:
+    """How a masked attention call changes its scores and which keys a query
+    sees (nvkv_score_mod in include/nvkv.h): scores capped at softcap by a
+    tanh, a bias -alibi_slopes[head] * |distance| (float32 [Hq]), a sliding
+    window of that many keys, a prefix of prefix_lens[b] tokens (int32
+    [batch]) whose queries see all of it, and the first visible key key_starts
+    (int32, [batch] for decode, [total_q] for prefill).  The tensors are kept
+    and read by every call, so their contents may change between calls."""
+
+    def __init__(self, softcap: float = 0.0, window: int = 0,
+                 alibi_slopes: torch.Tensor | None = None, prefix_lens: torch.Tensor | None = None,
+                 key_starts: torch.Tensor | None = None):
+        self.softcap, self.window = float(softcap), int(window)
+        self.alibi_slopes, self.prefix_lens, self.key_starts = alibi_slopes, prefix_lens, key_starts
+        self._c = _ScoreModC(
+            self.softcap, self.window,
+            _dev(alibi_slopes, torch.float32, "alibi_slopes") if alibi_slopes is not None else None,
+            _dev(prefix_lens, torch.int32, "prefix_lens") if prefix_lens is not None else None,
+            _dev(key_starts, torch.int32, "key_starts") if key_starts is not None else None)
+
+    def _check(self, device: torch.device, num_q_heads: int, batch: int, starts: int) -> None:
+        for t, n, name in ((self.alibi_slopes, num_q_heads, "alibi_slopes"),
+                           (self.prefix_lens, batch, "prefix_lens"),
+                           (self.key_starts, starts, "key_starts")):
+            if t is not None:
+                if t.device != device:
+                    raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+                _at_least(t, n, name)
+
+
+def nvkv_decode_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, T: int, num_q_heads: int,
+                         sm_scale: float, mod: ScoreMod, num_splits: int,
+                         workspace: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """Decode attention of T queries per sequence with the scores and masks of
+    mod, merged into out (bf16 [batch*T][Hq][D]); workspace as for
+    nvkv_decode_attn.  For caches of either format."""
+    device = cache.pool.device
+    _same_device(device, (seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens"), (q, "q"),
+                 (workspace, "workspace"), (out, "out"))
+    mod._check(device, num_q_heads, seqs.batch, seqs.batch)
+    n = seqs.batch * T * num_q_heads * cache.head_dim
+    _at_least(q, n, "q")
+    _at_least(out, n, "out")
+    L = library()
+    _call(device, L.nvkv_decode_attn_mod_k8v4 if cache.kv_format == "k8v4" else L.nvkv_decode_attn_mod,
+          "nvkv_decode_attn_mod", stream, ctypes.byref(cache._c), ctypes.byref(seqs._c),
+          _dev(q, torch.bfloat16, "q"), int(T), int(num_q_heads), float(sm_scale),
+          ctypes.byref(mod._c), int(num_splits), _dev(workspace, torch.uint8, "workspace"),
+          workspace.numel(), _dev(out, torch.bfloat16, "out"))
+
+
+def nvkv_prefill_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, cu_q: torch.Tensor,
+                          total_q: int, max_q: int, num_q_heads: int, sm_scale: float,
+                          mod: ScoreMod, num_splits: int, workspace: "torch.Tensor | None",
+                          out: torch.Tensor, stream=None) -> None:
+    """Chunked prefill with the scores and masks of mod; num_splits and
+    workspace as for nvkv_prefill_attn_split.  For caches of either format."""
+    device = cache.pool.device
+    _same_device(device, (seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens"), (q, "q"),
+                 (cu_q, "cu_q"), (workspace, "workspace"), (out, "out"))
+    mod._check(device, num_q_heads, seqs.batch, total_q)
+    n = total_q * num_q_heads * cache.head_dim
+    _at_least(q, n, "q")
+    _at_least(out, n, "out")
+    _at_least(cu_q, seqs.batch + 1, "cu_q")
+    ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
+    L = library()
+    _call(device,
+          L.nvkv_prefill_attn_mod_k8v4 if cache.kv_format == "k8v4" else L.nvkv_prefill_attn_mod,
+          "nvkv_prefill_attn_mod", stream, ctypes.byref(cache._c), ctypes.byref(seqs._c),
+          _dev(q, torch.bfloat16, "q"), _dev(cu_q, torch.int32, "cu_q"), int(total_q), int(max_q),
+          int(num_q_heads), float(sm_scale), ctypes.byref(mod._c), int(num_splits), ws,
+          workspace.numel() if workspace is not None else 0, _dev(out, torch.bfloat16, "out"))
+
+
+def nvkv_append_rope_axes(cache: Cache, seqs: Seqs, k_new: torch.Tensor, v_new: torch.Tensor,
+                          cu_new: torch.Tensor, total_new: int, max_new: int,
+                          rope_cs: torch.Tensor, rotary_dim: int, positions: torch.Tensor,
+                          axis_of_pair, q: torch.Tensor | None = None,
+                          q_out: torch.Tensor | None = None, stream=None) -> None:
+    """nvkv_append_rope with the positions of every row on several axes:
+    positions int32 [num_axes][total_new], axis_of_pair the axis (a whole
+    number) of each of the rotary_dim/2 pairs.  q (bf16 [total_new][Hq][D]) is
+    rotated into q_out in the same launch."""
+    _fmt(cache, "nvfp4", "nvkv_append_rope_axes")
+    device = cache.pool.device
+    _same_device(device, (seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens"),
+                 (k_new, "k_new"), (v_new, "v_new"), (cu_new, "cu_new"), (rope_cs, "rope_cs"),
+                 (positions, "positions"), (q, "q"), (q_out, "q_out"))
+    if positions.dim() != 2 or positions.shape[1] != total_new:
+        raise ValueError("positions must be [num_axes][total_new]")
+    if rope_cs.dim() != 3 or rope_cs.shape[1] * 2 != rotary_dim or rope_cs.shape[2] != 2:
+        raise ValueError("rope_cs must be [max_pos][rotary_dim/2][2]")
+    if len(axis_of_pair) * 2 != rotary_dim:
+        raise ValueError("axis_of_pair must have rotary_dim/2 entries")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    n = total_new * cache.num_kv_heads * cache.head_dim
+    _at_least(k_new, n, "k_new")
+    _at_least(v_new, n, "v_new")
+    _at_least(cu_new, seqs.batch + 1, "cu_new")
+    hq = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != total_new or q.shape[2] != cache.head_dim:
+            raise ValueError("q must be [total_new][Hq][D]")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        hq = q.shape[1]
+    _call(device, library().nvkv_append_rope_axes, "nvkv_append_rope_axes", stream,
+          ctypes.byref(cache._c), ctypes.byref(seqs._c), _dev(k_new, torch.bfloat16, "k_new"),
+          _dev(v_new, torch.bfloat16, "v_new"), _dev(cu_new, torch.int32, "cu_new"),
+          int(total_new), int(max_new), _dev(rope_cs, torch.float32, "rope_cs"),
+          int(rope_cs.shape[0]), int(rotary_dim), _dev(positions, torch.int32, "positions"),
+          int(positions.shape[0]), bytes(axis_of_pair),
+          _dev(q, torch.bfloat16, "q") if q is not None else None, int(hq),
+          _dev(q_out, torch.bfloat16, "q_out") if q_out is not None else None)
+
+
+def nvkv_read_rows(cache: Cache, seqs: Seqs, starts: torch.Tensor, cu_rows: torch.Tensor,
+                   total_rows: int, max_rows: int, k_out: torch.Tensor, v_out: torch.Tensor,
+                   stream=None) -> None:
+    """The cached K and V rows of positions starts[b] .. of every sequence as
+    bf16, rows cu_rows[b] .. cu_rows[b+1]-1 of k_out and v_out
+    ([total_rows][Hkv][D]).  For caches of either format."""
+    device = cache.pool.device
+    _same_device(device, (seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens"),
+                 (starts, "starts"), (cu_rows, "cu_rows"), (k_out, "k_out"), (v_out, "v_out"))
+    n = total_rows * cache.num_kv_heads * cache.head_dim
+    _at_least(k_out, n, "k_out")
+    _at_least(v_out, n, "v_out")
+    _at_least(starts, seqs.batch, "starts")
+    _at_least(cu_rows, seqs.batch + 1, "cu_rows")
+    L = library()
+    _call(device, L.nvkv_read_rows_k8v4 if cache.kv_format == "k8v4" else L.nvkv_read_rows,
+          "nvkv_read_rows", stream, ctypes.byref(cache._c), ctypes.byref(seqs._c),
+          _dev(starts, torch.int32, "starts"), _dev(cu_rows, torch.int32, "cu_rows"),
+          int(total_rows), int(max_rows), _dev(k_out, torch.bfloat16, "k_out"),
+          _dev(v_out, torch.bfloat16, "v_out"))

@@ -6,7 +6,7 @@
 #include <cstdlib>
 #include <cstring>
 
-#include "nvkv_common.cuh"
+#include "score_mod.cuh"
 
 namespace nvkv {
 cudaError_t launch_append(const nvkv_cache &, const nvkv_seqs &, const void *, const void *,
@@ -15,7 +15,8 @@ cudaError_t launch_rope_table(float *, int, int, double, double, cudaStream_t);
 cudaError_t launch_append_k8v4(const nvkv_cache &, const nvkv_seqs &, const void *, const void *,
                                const int32_t *, int, int, cudaStream_t);
 cudaError_t launch_decode_simt(const nvkv_cache &, const nvkv_seqs &, const void *, int, int,
-                               float, int, float *, float *, cudaStream_t, bool);
+                               float, int, float *, float *, cudaStream_t, bool,
+                               const ScoreMod *);
 bool decode_tc_supported(const nvkv_cache &, int, int);
 bool decode_qk4_supported(const nvkv_cache &, int, int);
 cudaError_t launch_decode_qk4(const nvkv_cache &, const nvkv_seqs &, const void *, int, int, float,
@@ -31,11 +32,21 @@ int prefill_max_splits();
 int prefill_auto_splits(int64_t, int);
 int prefill_tc_items(const nvkv_cache &, const nvkv_seqs &, int, int);
 cudaError_t launch_combine(const nvkv_seqs &, const void *, const void *, int, int, int, int, int,
-                           void *, cudaStream_t);
+                           void *, cudaStream_t, const ScoreMod *);
 cudaError_t launch_prefill_simt(const nvkv_cache &, const nvkv_seqs &, const void *,
-                                const int32_t *, int, int, float, void *, cudaStream_t, bool);
+                                const int32_t *, int, int, float, void *, cudaStream_t, bool,
+                                const ScoreMod *);
 cudaError_t launch_page_copy(const uint8_t *, int64_t, uint8_t *, int64_t, const int32_t *,
                              const int32_t *, int, int64_t, int32_t *, cudaStream_t);
+int64_t read_rows_blocks(const nvkv_cache &, int);
+cudaError_t launch_read_rows(const nvkv_cache &, const nvkv_seqs &, const int32_t *,
+                             const int32_t *, int, int, void *, void *, cudaStream_t, bool);
+bool append_axes_fits(const nvkv_cache &, int, int, bool);
+int append_axes_max_axes();
+cudaError_t launch_append_axes(const nvkv_cache &, const nvkv_seqs &, const void *, const void *,
+                               const int32_t *, int, int, const float *, int, int,
+                               const int32_t *, int, const uint8_t *, const void *, int, void *,
+                               cudaStream_t);
 }  // namespace nvkv
 
 using namespace nvkv;
@@ -186,6 +197,20 @@ PrefillLayout prefill_layout(int64_t total_q, int Hq, int D, int S) {
   return {lse_off, lse_off + align256(rows * sizeof(float))};
 }
 
+// The kernels' form of a score modification (scores are in base-2 units).
+nvkv_status check_mod(const nvkv_score_mod *mod, ScoreMod &m) {
+  if (!mod || !std::isfinite(mod->softcap) || mod->softcap < 0.f || mod->window < 0)
+    return NVKV_ERR_INVALID_ARG;
+  m.cap2 = mod->softcap * kLog2e;
+  m.cap_in = mod->softcap > 0.f ? 2.f * kLog2e / m.cap2 : 0.f;
+  if (!std::isfinite(m.cap2) || !std::isfinite(m.cap_in)) return NVKV_ERR_INVALID_ARG;
+  m.window = mod->window;
+  m.slopes = mod->alibi_slopes;
+  m.prefix = mod->prefix_lens;
+  m.starts = mod->key_starts;
+  return NVKV_OK;
+}
+
 // NVKV_DECODE_KERNEL=simt forces the CUDA-core decode and prefill kernels;
 // NVKV_DECODE_KERNEL=tc forces the decode kernel that dequantises K for
 // the f16 tensor-core scores (where it takes the shape).  The tests use
@@ -195,6 +220,56 @@ bool force_kernel(const char *name) {
   return v && std::strcmp(v, name) == 0;
 }
 bool force_simt() { return force_kernel("simt"); }
+
+nvkv_status decode_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q, int32_t T,
+                       int32_t num_q_heads, float sm_scale, const nvkv_score_mod *mod,
+                       int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
+                       nvkv_stream_t stream, bool k8) {
+  DecodeArgs a;
+  nvkv_status st = check_decode(cache, seqs, q, T, num_q_heads, sm_scale, num_splits, workspace,
+                                workspace_bytes, a);
+  if (st != NVKV_OK) return st;
+  ScoreMod m;
+  if ((st = check_mod(mod, m)) != NVKV_OK) return st;
+  if (!out || !aligned16(out)) return NVKV_ERR_INVALID_ARG;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_decode_simt(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o,
+                                           a.ws_lse, s, k8, &m);
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(launch_combine(*seqs, a.ws_o, a.ws_lse, T, num_q_heads, cache->num_kv_heads,
+                                    cache->head_dim, a.S, out, s, &m));
+}
+
+nvkv_status prefill_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
+                        const int32_t *cu_q, int32_t total_q, int32_t max_q, int32_t num_q_heads,
+                        float sm_scale, const nvkv_score_mod *mod, int32_t num_splits,
+                        void *workspace, size_t workspace_bytes, void *out, nvkv_stream_t stream,
+                        bool k8) {
+  nvkv_status st = check_prefill(cache, seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale, out);
+  if (st != NVKV_OK) return st;
+  ScoreMod m;
+  if ((st = check_mod(mod, m)) != NVKV_OK) return st;
+  if (num_splits < 0 || num_splits > prefill_max_splits()) return NVKV_ERR_INVALID_ARG;
+  if (total_q == 0) return NVKV_OK;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
+                                         out, s, k8, &m));
+}
+
+nvkv_status read_rows(const nvkv_cache *cache, const nvkv_seqs *seqs, const int32_t *starts,
+                      const int32_t *cu_rows, int32_t total_rows, int32_t max_rows, void *k_out,
+                      void *v_out, nvkv_stream_t stream, bool k8) {
+  nvkv_status st = check_cache(cache);
+  if (st != NVKV_OK) return st;
+  if ((st = check_seqs(seqs)) != NVKV_OK) return st;
+  if (total_rows < 0 || max_rows < 0) return NVKV_ERR_INVALID_ARG;
+  if (total_rows == 0 || max_rows == 0) return NVKV_OK;
+  if (!starts || !cu_rows || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+    return NVKV_ERR_INVALID_ARG;
+  if (read_rows_blocks(*cache, max_rows) > INT32_MAX) return NVKV_ERR_UNSUPPORTED;
+  return cuda_status(launch_read_rows(*cache, *seqs, starts, cu_rows, total_rows, max_rows, k_out,
+                                      v_out, reinterpret_cast<cudaStream_t>(stream), k8));
+}
 
 }  // namespace
 
@@ -321,7 +396,7 @@ nvkv_status nvkv_decode_attn(const nvkv_cache *cache, const nvkv_seqs *seqs, con
     return cuda_status(
         launch_decode_tc(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o, a.ws_lse, st_));
   return cuda_status(launch_decode_simt(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o,
-                                        a.ws_lse, st_, false));
+                                        a.ws_lse, st_, false, nullptr));
 }
 
 nvkv_status nvkv_combine(const nvkv_seqs *seqs, const void *workspace, int32_t T,
@@ -336,7 +411,7 @@ nvkv_status nvkv_combine(const nvkv_seqs *seqs, const void *workspace, int32_t T
   const WorkspaceLayout w = layout(seqs->batch, T, num_q_heads, num_kv_heads, head_dim, S);
   const void *ws_lse = static_cast<const char *>(workspace) + w.lse_off;
   return cuda_status(launch_combine(*seqs, workspace, ws_lse, T, num_q_heads, num_kv_heads,
-                                    head_dim, S, out, reinterpret_cast<cudaStream_t>(stream)));
+                                    head_dim, S, out, reinterpret_cast<cudaStream_t>(stream), nullptr));
 }
 
 nvkv_status nvkv_prefill_attn(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
@@ -351,7 +426,7 @@ nvkv_status nvkv_prefill_attn(const nvkv_cache *cache, const nvkv_seqs *seqs, co
     return cuda_status(launch_prefill_tc(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads,
                                          sm_scale, out, 1, nullptr, nullptr, st_));
   return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
-                                         out, st_, false));
+                                         out, st_, false, nullptr));
 }
 
 size_t nvkv_prefill_workspace_bytes(int32_t total_q, int32_t num_q_heads, int32_t head_dim,
@@ -388,7 +463,7 @@ nvkv_status nvkv_prefill_attn_split(const nvkv_cache *cache, const nvkv_seqs *se
   cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
   if (force_simt() || !prefill_tc_supported(*cache))
     return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
-                                           out, st_, false));
+                                           out, st_, false, nullptr));
   const int S = num_splits > 0 ? num_splits
                                : prefill_auto_splits(
                                      prefill_tc_items(*cache, *seqs, max_q, num_q_heads),
@@ -438,7 +513,7 @@ nvkv_status nvkv_decode_attn_k8v4(const nvkv_cache *cache, const nvkv_seqs *seqs
     return cuda_status(launch_decode_qk4_k8v4(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S,
                                               a.ws_o, a.ws_lse, st_));
   return cuda_status(launch_decode_simt(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o,
-                                        a.ws_lse, st_, true));
+                                        a.ws_lse, st_, true, nullptr));
 }
 
 const char *nvkv_decode_kernel_name_k8v4(const nvkv_cache *cache, int32_t T,
@@ -458,7 +533,84 @@ nvkv_status nvkv_prefill_attn_k8v4(const nvkv_cache *cache, const nvkv_seqs *seq
       check_prefill(cache, seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale, out);
   if (st != NVKV_OK || total_q == 0) return st;
   return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
-                                         out, reinterpret_cast<cudaStream_t>(stream), true));
+                                         out, reinterpret_cast<cudaStream_t>(stream), true, nullptr));
+}
+
+nvkv_status nvkv_decode_attn_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
+                                 int32_t T, int32_t num_q_heads, float sm_scale,
+                                 const nvkv_score_mod *mod, int32_t num_splits, void *workspace,
+                                 size_t workspace_bytes, void *out, nvkv_stream_t stream) {
+  return decode_mod(cache, seqs, q, T, num_q_heads, sm_scale, mod, num_splits, workspace,
+                    workspace_bytes, out, stream, false);
+}
+
+nvkv_status nvkv_decode_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs *seqs,
+                                      const void *q, int32_t T, int32_t num_q_heads,
+                                      float sm_scale, const nvkv_score_mod *mod,
+                                      int32_t num_splits, void *workspace,
+                                      size_t workspace_bytes, void *out, nvkv_stream_t stream) {
+  return decode_mod(cache, seqs, q, T, num_q_heads, sm_scale, mod, num_splits, workspace,
+                    workspace_bytes, out, stream, true);
+}
+
+nvkv_status nvkv_prefill_attn_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
+                                  const int32_t *cu_q, int32_t total_q, int32_t max_q,
+                                  int32_t num_q_heads, float sm_scale, const nvkv_score_mod *mod,
+                                  int32_t num_splits, void *workspace, size_t workspace_bytes,
+                                  void *out, nvkv_stream_t stream) {
+  return prefill_mod(cache, seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale, mod, num_splits,
+                     workspace, workspace_bytes, out, stream, false);
+}
+
+nvkv_status nvkv_prefill_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs *seqs,
+                                       const void *q, const int32_t *cu_q, int32_t total_q,
+                                       int32_t max_q, int32_t num_q_heads, float sm_scale,
+                                       const nvkv_score_mod *mod, int32_t num_splits,
+                                       void *workspace, size_t workspace_bytes, void *out,
+                                       nvkv_stream_t stream) {
+  return prefill_mod(cache, seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale, mod, num_splits,
+                     workspace, workspace_bytes, out, stream, true);
+}
+
+nvkv_status nvkv_append_rope_axes(const nvkv_cache *cache, const nvkv_seqs *seqs,
+                                  const void *k_new, const void *v_new, const int32_t *cu_new,
+                                  int32_t total_new, int32_t max_new, const float *rope_cs,
+                                  int32_t max_pos, int32_t rotary_dim, const int32_t *positions,
+                                  int32_t num_axes, const uint8_t *axis_of_pair, const void *q,
+                                  int32_t num_q_heads, void *q_out, nvkv_stream_t stream) {
+  nvkv_status st = check_cache(cache);
+  if (st != NVKV_OK) return st;
+  if ((st = check_seqs(seqs)) != NVKV_OK) return st;
+  if (total_new < 0 || max_new < 0) return NVKV_ERR_INVALID_ARG;
+  if (!rope_cs || (reinterpret_cast<uintptr_t>(rope_cs) & 7u) || max_pos <= 0 ||
+      rotary_dim <= 0 || rotary_dim % 32 != 0 || rotary_dim > cache->head_dim)
+    return NVKV_ERR_INVALID_ARG;
+  if (num_axes < 1 || !axis_of_pair) return NVKV_ERR_INVALID_ARG;
+  if (num_axes > append_axes_max_axes()) return NVKV_ERR_UNSUPPORTED;
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (axis_of_pair[i] >= num_axes) return NVKV_ERR_INVALID_ARG;
+  if (total_new == 0 || max_new == 0) return NVKV_OK;
+  if (!k_new || !v_new || !cu_new || !positions || !aligned16(k_new) || !aligned16(v_new))
+    return NVKV_ERR_INVALID_ARG;
+  if (q && (!q_out || !aligned16(q) || !aligned16(q_out) || num_q_heads <= 0))
+    return NVKV_ERR_INVALID_ARG;
+  if (!append_axes_fits(*cache, max_new, num_q_heads, q != nullptr)) return NVKV_ERR_UNSUPPORTED;
+  return cuda_status(launch_append_axes(*cache, *seqs, k_new, v_new, cu_new, total_new, max_new,
+                                        rope_cs, max_pos, rotary_dim, positions, num_axes,
+                                        axis_of_pair, q, num_q_heads, q_out,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvkv_status nvkv_read_rows(const nvkv_cache *cache, const nvkv_seqs *seqs, const int32_t *starts,
+                           const int32_t *cu_rows, int32_t total_rows, int32_t max_rows,
+                           void *k_out, void *v_out, nvkv_stream_t stream) {
+  return read_rows(cache, seqs, starts, cu_rows, total_rows, max_rows, k_out, v_out, stream, false);
+}
+
+nvkv_status nvkv_read_rows_k8v4(const nvkv_cache *cache, const nvkv_seqs *seqs,
+                                const int32_t *starts, const int32_t *cu_rows, int32_t total_rows,
+                                int32_t max_rows, void *k_out, void *v_out, nvkv_stream_t stream) {
+  return read_rows(cache, seqs, starts, cu_rows, total_rows, max_rows, k_out, v_out, stream, true);
 }
 
 nvkv_status nvkv_pages_spill(const nvkv_cache *cache, const int32_t *page_ids,

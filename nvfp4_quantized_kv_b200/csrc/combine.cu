@@ -7,14 +7,15 @@
 //     L = max_s lse2_s,  w_s = 2^(lse2_s - L),  out = sum_s w_s o_s / sum_s w_s,
 // rounded once to bf16.  One warp per query row; each lane owns D/32
 // channels.
-#include "nvkv_common.cuh"
+#include "score_mod.cuh"
 
 namespace nvkv {
 
+template <class Mod>
 __global__ void __launch_bounds__(256)
 combine_kernel(const int32_t *__restrict__ kv_lens, int B, int Hkv, int T, int Hq, int D, int S,
                const float *__restrict__ ws_o, const float *__restrict__ ws_lse,
-               __nv_bfloat16 *__restrict__ out) {
+               __nv_bfloat16 *__restrict__ out, Mod mod) {
   const int G = Hq / Hkv;
   const int R = T * G;
   const long wid = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -29,7 +30,7 @@ combine_kernel(const int32_t *__restrict__ kv_lens, int B, int Hkv, int T, int H
   int64_t U = 0, pair_start = 0;
   int units = 0;
   for (int bb = 0; bb < B; ++bb) {
-    const int ub = units_of_len(kv_lens[bb]);
+    const int ub = mod.units(kv_lens, bb, T);
     if (bb == b) {
       pair_start = U + (int64_t)h * ub;
       units = ub;
@@ -81,14 +82,21 @@ combine_kernel(const int32_t *__restrict__ kv_lens, int B, int Hkv, int T, int H
 }
 
 cudaError_t launch_combine(const nvkv_seqs &s, const void *ws_o, const void *ws_lse, int T,
-                           int Hq, int Hkv, int D, int S, void *out, cudaStream_t stream) {
+                           int Hq, int Hkv, int D, int S, void *out, cudaStream_t stream,
+                           const ScoreMod *mod) {
   const int R = T * (Hq / Hkv);
   const long warps = (long)s.batch * Hkv * R;
   const int threads = 256;
   const long blocks = (warps * 32 + threads - 1) / threads;
-  combine_kernel<<<(unsigned)blocks, threads, 0, stream>>>(
-      s.kv_lens, s.batch, Hkv, T, Hq, D, S, static_cast<const float *>(ws_o),
-      static_cast<const float *>(ws_lse), static_cast<__nv_bfloat16 *>(out));
+  auto run = [&](auto m) {
+    combine_kernel<<<(unsigned)blocks, threads, 0, stream>>>(
+        s.kv_lens, s.batch, Hkv, T, Hq, D, S, static_cast<const float *>(ws_o),
+        static_cast<const float *>(ws_lse), static_cast<__nv_bfloat16 *>(out), m);
+  };
+  if (mod)
+    run(*mod);
+  else
+    run(NoMod{});
   return cudaGetLastError();
 }
 

@@ -20,7 +20,7 @@
 // among its KV storage formats): K rows of one E4M3 byte per element with
 // one float scale per row, V as in the NVFP4 cache.  Only the K score and
 // the block offsets differ; the softmax and the value sums are shared.
-#include "nvkv_common.cuh"
+#include "score_mod.cuh"
 
 namespace nvkv {
 
@@ -83,23 +83,28 @@ __device__ __forceinline__ float k_half_score(K8v4Layout, const uint8_t *blk, in
 }
 
 // Online softmax of one query row (qr: fp32, pre-scaled to base-2 scores)
-// over keys [jb, je) of one sequence / kv-head, jb a multiple of 16, in a
-// pool of layout L.  The calling warp returns the running max m, the sum l
-// of 2^(s - m) and, per lane, the unnormalised value sums of channels
-// [lane*D/32, (lane+1)*D/32).
-template <class L>
+// over keys [jb, je) of one sequence / kv-head, in a pool of layout L (jb a
+// multiple of 16 unless Mod is on).  The calling warp returns the running
+// max m, the sum l of 2^(s - m) and, per lane, the unnormalised value sums of
+// channels [lane*D/32, (lane+1)*D/32).  With a ScoreMod the scores are capped
+// and biased by slope2 * |pos - key|; keys outside the interval are left out
+// whatever their bytes hold (weight and scale are replaced, not multiplied).
+template <class L, class Mod>
 __device__ __forceinline__ void attend_rows_simt(const uint8_t *__restrict__ pool, int num_pages,
                                                  int Hkv, int D, int h,
                                                  const int32_t *__restrict__ pt, int jb, int je,
                                                  const float *qr, float &m, float &l, float acc[8],
-                                                 int32_t *err) {
+                                                 int32_t *err, const Mod &mod, int pos,
+                                                 float slope2) {
   const int lane = threadIdx.x & 31;
   const int dpl = D / 32;
   m = -INFINITY;
   l = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  for (int p0 = jb; p0 < je; p0 += kPageTokens) {
+  // pages from the one that holds jb; none for an empty interval
+  const int jp = !Mod::kOn ? jb : jb < je ? jb / kPageTokens * kPageTokens : je;
+  for (int p0 = jp; p0 < je; p0 += kPageTokens) {
     const int page = pt[p0 / kPageTokens];
     if (page < 0 || page >= num_pages) {
       if (lane == 0) report(err, NVKV_DEVERR_PAGE_ID);
@@ -108,9 +113,13 @@ __device__ __forceinline__ void attend_rows_simt(const uint8_t *__restrict__ poo
     const uint8_t *blk = pool + (size_t)page * Hkv * L::head(D) + (size_t)h * L::head(D);
     // ---- scores: lane -> (slot, half of head_dim) ----
     const int slot = lane & 15, half = lane >> 4;
-    const bool valid = (p0 + slot) < je;
+    const bool valid = (p0 + slot) < je && (!Mod::kOn || p0 + slot >= jb);
     float s = k_half_score(L{}, blk, D, slot, half, qr);
     s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if constexpr (Mod::kOn) {
+      if (mod.cap2 > 0.f) s = mod.cap(s);
+      s = fmaf(-slope2, fabsf((float)(pos - (p0 + slot))), s);
+    }
     const float s_eff = valid ? s : -INFINITY;
     const float m_new = fmaxf(m, warp_max(s_eff));
     const float alpha = exp2f(m - m_new);  // m = -inf on the first page -> 0
@@ -127,7 +136,8 @@ __device__ __forceinline__ void attend_rows_simt(const uint8_t *__restrict__ poo
     for (int j = 0; j < 16; ++j) {
       const float pj = __shfl_sync(0xffffffffu, p, j);
       const uint8_t sb = (sc[j >> 2] >> (8 * (j & 3))) & 0xffu;
-      wgt[j] = (p0 + j < je) ? pj * e4m3_to_float(sb) : 0.f;
+      const bool in = p0 + j < je && (!Mod::kOn || p0 + j >= jb);
+      wgt[j] = in ? pj * e4m3_to_float(sb) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -147,32 +157,38 @@ __device__ __forceinline__ void attend_rows_simt(const uint8_t *__restrict__ poo
   }
 }
 
-template <class L>
+template <class L, class Mod>
 __global__ void __launch_bounds__(kSimtWarps * 32)
 decode_simt_kernel(const uint8_t *__restrict__ pool, int num_pages, int Hkv, int D,
                    const int32_t *__restrict__ page_table, int max_pages,
                    const int32_t *__restrict__ kv_lens, int B, int max_kv_len,
                    const __nv_bfloat16 *__restrict__ q, int T, int Hq, float qscale,
-                   int S, float *__restrict__ ws_o, float *__restrict__ ws_lse, int32_t *err) {
+                   int S, float *__restrict__ ws_o, float *__restrict__ ws_lse, int32_t *err,
+                   Mod mod) {
   extern __shared__ float qs[];  // [R][D] query rows of the current pair, pre-scaled
   const int G = Hq / Hkv;
   const int R = T * G;
   const int c = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  int64_t U = 0;
-  for (int b = 0; b < B; ++b) U += (int64_t)units_of_len(kv_lens[b]) * Hkv;
+  const int64_t U = total_units(mod, kv_lens, B, Hkv, T);
   if (U == 0) return;
   const int64_t u0 = range_begin(c, U, S), u1 = range_begin(c + 1, U, S);
   int64_t u = u0;
   while (u < u1) {
     int b, h, units;
     int64_t pair_start;
-    locate_pair(kv_lens, B, Hkv, u, b, h, pair_start, units);
+    locate_pair_mod(mod, kv_lens, B, Hkv, T, u, b, h, pair_start, units);
     const int64_t seg_end = min(u1, pair_start + units);
     const int kv_len = kv_lens[b];
-    const int tok_begin = (int)(u - pair_start) * kUnitTokens;
-    const int tok_end = min((int)(seg_end - pair_start) * kUnitTokens, kv_len);
+    int tok_begin = (int)(u - pair_start) * kUnitTokens;
+    int tok_end = min((int)(seg_end - pair_start) * kUnitTokens, kv_len);
+    if constexpr (Mod::kOn) {  // the segment's units, newest first
+      int lo, first, n;
+      visible_units(kv_len, T, mod.start(b), mod.window, lo, first, n);
+      tok_begin = unit_token<Mod>(first, n, pair_start, seg_end - 1);
+      tok_end = min(unit_token<Mod>(first, n, pair_start, u) + kUnitTokens, kv_len);
+    }
     const size_t slot = (size_t)c + (size_t)b * Hkv + h;
     const bool bad_len = kv_len > max_kv_len || kv_len > max_pages * kPageTokens;
     if (bad_len && threadIdx.x == 0) report(err, NVKV_DEVERR_LENGTH);
@@ -190,11 +206,20 @@ decode_simt_kernel(const uint8_t *__restrict__ pool, int num_pages, int Hkv, int
     const int dpl = D / 32;  // output channels per lane
     for (int r = warp; r < R; r += kSimtWarps) {
       const int t = r / G;
+      [[maybe_unused]] const int g = r % G;
       const int n_vis = kv_len - T + t + 1;  // keys 0 .. n_vis-1 are visible
-      const int jb = tok_begin, je = bad_len ? jb : min(tok_end, n_vis);
+      int jb = tok_begin, je = bad_len ? jb : min(tok_end, n_vis);
+      float slope2 = 0.f;
+      if constexpr (Mod::kOn) {
+        int lo, hi;
+        key_range(n_vis - 1, kv_len, mod.start(b), mod.window, mod.prefix_of(b), lo, hi);
+        jb = max(tok_begin, lo);
+        je = bad_len ? jb : min(tok_end, hi);
+        slope2 = mod.slope2(h * G + g);
+      }
       float m, l, acc[8];
       attend_rows_simt<L>(pool, num_pages, Hkv, D, h, pt, jb, je, qs + (size_t)r * D, m, l, acc,
-                          err);
+                          err, mod, n_vis - 1, slope2);
       // ---- partial result of this split for row r ----
       float *o = ws_o + (slot * R + r) * (size_t)D;
       const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -206,12 +231,14 @@ decode_simt_kernel(const uint8_t *__restrict__ pool, int num_pages, int Hkv, int
 }
 
 // k8: the pool is in the K8V4 layout (else NVFP4).
-cudaError_t launch_decode_simt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
-                               int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
-                               cudaStream_t stream, bool k8) {
+template <class Mod>
+cudaError_t launch_decode_simt_mod(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
+                                   int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
+                                   cudaStream_t stream, bool k8, const Mod &mod) {
   const int R = T * (Hq / c.num_kv_heads);
   const size_t smem = (size_t)R * c.head_dim * sizeof(float);
-  auto kernel = k8 ? decode_simt_kernel<K8v4Layout> : decode_simt_kernel<Nvfp4Layout>;
+  auto kernel =
+      k8 ? decode_simt_kernel<K8v4Layout, Mod> : decode_simt_kernel<Nvfp4Layout, Mod>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -219,21 +246,29 @@ cudaError_t launch_decode_simt(const nvkv_cache &c, const nvkv_seqs &s, const vo
   kernel<<<S, kSimtWarps * 32, smem, stream>>>(
       c.pool, c.num_pages, c.num_kv_heads, c.head_dim, s.page_table, s.max_pages_per_seq,
       s.kv_lens, s.batch, s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), T, Hq, qscale, S,
-      ws_o, ws_lse, s.err_word);
+      ws_o, ws_lse, s.err_word, mod);
   return cudaGetLastError();
+}
+
+cudaError_t launch_decode_simt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
+                               int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
+                               cudaStream_t stream, bool k8, const ScoreMod *mod) {
+  return mod ? launch_decode_simt_mod(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, k8, *mod)
+             : launch_decode_simt_mod(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, k8,
+                                      NoMod{});
 }
 
 // Chunked prefill on CUDA cores: one warp per (chunk row, query head), over
 // the row's whole visible prefix (keys 0 .. its position).  Used for chunks
 // the tensor-core prefill kernel does not take.
-template <class L>
+template <class L, class Mod>
 __global__ void __launch_bounds__(kSimtWarps * 32)
 prefill_simt_kernel(const uint8_t *__restrict__ pool, int num_pages, int Hkv, int D,
                     const int32_t *__restrict__ page_table, int max_pages,
                     const int32_t *__restrict__ kv_lens, int B, int max_kv_len,
                     const __nv_bfloat16 *__restrict__ q, const int32_t *__restrict__ cu_q,
                     int total_q, int Hq, float qscale, __nv_bfloat16 *__restrict__ out,
-                    int32_t *err) {
+                    int32_t *err, Mod mod) {
   extern __shared__ float qs[];  // [kSimtWarps][D]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long w = (long)blockIdx.x * kSimtWarps + warp;
@@ -248,34 +283,49 @@ prefill_simt_kernel(const uint8_t *__restrict__ pool, int num_pages, int Hkv, in
   float *qr = qs + warp * D;
   for (int d = lane; d < D; d += 32) qr[d] = __bfloat162float(q[((size_t)row * Hq + hq) * D + d]) * qscale;
   __syncwarp();
-  int je = pos + 1;
+  int jb = 0, je = pos + 1;
+  float slope2 = 0.f;
+  if constexpr (Mod::kOn) {
+    key_range(pos, kv_len, mod.start(row), mod.window, mod.prefix_of(b), jb, je);
+    slope2 = mod.slope2(hq);
+  }
   if (row - cu_q[b] >= n_b || pos < 0 || kv_len > max_kv_len ||
       kv_len > max_pages * kPageTokens) {
     if (lane == 0) report(err, NVKV_DEVERR_LENGTH);
-    je = 0;
+    jb = je = 0;
   }
   float m, l, acc[8];
-  attend_rows_simt<L>(pool, num_pages, Hkv, D, h, page_table + (size_t)b * max_pages, 0, je, qr,
-                      m, l, acc, err);
+  attend_rows_simt<L>(pool, num_pages, Hkv, D, h, page_table + (size_t)b * max_pages, jb, je, qr,
+                      m, l, acc, err, mod, pos, slope2);
   const int dpl = D / 32;
   const float inv = l > 0.f ? 1.f / l : 0.f;
   __nv_bfloat16 *dst = out + ((size_t)row * Hq + hq) * D + lane * dpl;
   for (int i = 0; i < dpl; ++i) dst[i] = __float2bfloat16_rn(acc[i] * inv);
 }
 
-cudaError_t launch_prefill_simt(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
-                                const int32_t *cu_q, int total_q, int Hq, float sm_scale,
-                                void *out, cudaStream_t stream, bool k8) {
+template <class Mod>
+cudaError_t launch_prefill_simt_mod(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
+                                    const int32_t *cu_q, int total_q, int Hq, float sm_scale,
+                                    void *out, cudaStream_t stream, bool k8, const Mod &mod) {
   const long warps = (long)total_q * Hq;
   const long blocks = (warps + kSimtWarps - 1) / kSimtWarps;
   const size_t smem = (size_t)kSimtWarps * c.head_dim * sizeof(float);
   const float qscale = sm_scale * 1.4426950408889634f;
-  auto kernel = k8 ? prefill_simt_kernel<K8v4Layout> : prefill_simt_kernel<Nvfp4Layout>;
+  auto kernel =
+      k8 ? prefill_simt_kernel<K8v4Layout, Mod> : prefill_simt_kernel<Nvfp4Layout, Mod>;
   kernel<<<(unsigned)blocks, kSimtWarps * 32, smem, stream>>>(
       c.pool, c.num_pages, c.num_kv_heads, c.head_dim, s.page_table, s.max_pages_per_seq,
       s.kv_lens, s.batch, s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), cu_q, total_q, Hq,
-      qscale, static_cast<__nv_bfloat16 *>(out), s.err_word);
+      qscale, static_cast<__nv_bfloat16 *>(out), s.err_word, mod);
   return cudaGetLastError();
+}
+
+cudaError_t launch_prefill_simt(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
+                                const int32_t *cu_q, int total_q, int Hq, float sm_scale,
+                                void *out, cudaStream_t stream, bool k8, const ScoreMod *mod) {
+  return mod ? launch_prefill_simt_mod(c, s, q, cu_q, total_q, Hq, sm_scale, out, stream, k8, *mod)
+             : launch_prefill_simt_mod(c, s, q, cu_q, total_q, Hq, sm_scale, out, stream, k8,
+                                       NoMod{});
 }
 
 }  // namespace nvkv

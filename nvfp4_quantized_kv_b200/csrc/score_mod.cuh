@@ -1,0 +1,131 @@
+// score_mod.cuh -- the score modifications of the masked attention
+// (nvkv_score_mod in include/nvkv.h): a tanh cap, a bias that falls with the
+// distance, and the visible key interval of a query.
+//
+// The attention kernels are templates over a Mod type: NoMod is the plain
+// causal attention (every member folds away), ScoreMod the masked one.
+#pragma once
+
+#include "nvkv_common.cuh"
+
+namespace nvkv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Visible keys [lo, hi) of a query at position p of a sequence of kv_len
+// tokens: lo = max(0, start, p - W + 1), hi = p + 1, or p + min(P - p, W)
+// when p lies inside the prefix P; at most kv_len.  W <= 0: no window.
+// Always an interval; empty (hi <= lo) when start > p, or p < 0.
+__host__ __device__ inline void key_range(int p, int kv_len, int start, int window, int prefix,
+                                          int &lo, int &hi) {
+  lo = start > 0 ? start : 0;
+  hi = lo;
+  if (p < 0) return;
+  hi = p + 1;
+  if (window > 0 && p - window + 1 > lo) lo = p - window + 1;
+  if (prefix > p) {
+    const int ahead = prefix - p;
+    hi = (window > 0 && window < ahead) ? p + window : prefix;
+  }
+  if (hi > kv_len) hi = kv_len;
+}
+
+// First key that any of the T newest queries of a sequence can see, and the
+// 128-token units that hold the keys from there on (the split plan's units).
+__host__ __device__ inline void visible_units(int kv_len, int T, int start, int window, int &lo,
+                                              int &first_unit, int &units) {
+  lo = start > 0 ? start : 0;
+  const int p0 = kv_len > T ? kv_len - T : 0;  // position of the first query
+  if (window > 0 && p0 - window + 1 > lo) lo = p0 - window + 1;
+  if (kv_len <= 0 || lo >= kv_len) {
+    first_unit = units = 0;
+    return;
+  }
+  first_unit = lo / kUnitTokens;
+  units = (kv_len - 1) / kUnitTokens - first_unit + 1;
+}
+
+// Plain causal attention.
+struct NoMod {
+  static constexpr bool kOn = false;
+  __device__ __forceinline__ int units(const int32_t *kv_lens, int b, int) const {
+    return units_of_len(kv_lens[b]);
+  }
+};
+
+// Kernel arguments of the masked attention.  Scores are in base-2 units
+// (x = q.k * sm_scale * log2 e), and so are the cap and the slopes.
+struct ScoreMod {
+  static constexpr bool kOn = true;
+  float cap2;             // cap * log2 e; 0 = no cap
+  float cap_in;           // 2 log2 e / cap2: the exponent of exp(2 x / cap2), base 2
+  int window;             // 0 = none
+  const float *slopes;    // [Hq] or null
+  const int32_t *prefix;  // [batch] or null
+  const int32_t *starts;  // decode: [batch], prefill: [total_q]; or null
+
+  __device__ __forceinline__ int start(int i) const { return starts ? starts[i] : 0; }
+  __device__ __forceinline__ int prefix_of(int b) const { return prefix ? prefix[b] : 0; }
+  __device__ __forceinline__ float slope2(int hq) const { return slopes ? slopes[hq] * kLog2e : 0.f; }
+  __device__ __forceinline__ int units(const int32_t *kv_lens, int b, int T) const {
+    int lo, first, n;
+    visible_units(kv_lens[b], T, start(b), window, lo, first, n);
+    return n;
+  }
+  // cap2 * tanh(x / cap2) = cap2 - 2 cap2 / (2^(x * cap_in) + 1): one base-2
+  // exponential and one reciprocal.  Each approximation is good to a few
+  // 2^-23, so the result is off by at most about 2^-20 * cap2 whatever x
+  // (tanh.approx would be off by 2^-11 * cap2, several per cent of a softmax
+  // weight at a cap of 50).  The exponential's overflow to infinity gives
+  // +cap2, its underflow -cap2.
+  __device__ __forceinline__ float cap(float x) const {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * cap_in));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
+    return fmaf(-2.f * cap2, r, cap2);
+  }
+};
+
+// locate_pair over the units that a Mod's queries can see (T: queries per
+// sequence of the whole step).
+template <class Mod>
+__device__ __forceinline__ void locate_pair_mod(const Mod &mod, const int32_t *kv_lens, int B,
+                                                int Hkv, int T, int64_t u, int &b, int &h,
+                                                int64_t &pair_start, int &units) {
+  int64_t acc = 0;
+  for (b = 0; b < B; ++b) {
+    const int ub = mod.units(kv_lens, b, T);
+    const int64_t span = (int64_t)ub * Hkv;
+    if (u < acc + span) {
+      h = (int)((u - acc) / ub);
+      pair_start = acc + (int64_t)h * ub;
+      units = ub;
+      return;
+    }
+    acc += span;
+  }
+  h = 0;
+  pair_start = acc;
+  units = 0;
+}
+
+template <class Mod>
+__device__ __forceinline__ int64_t total_units(const Mod &mod, const int32_t *kv_lens, int B,
+                                               int Hkv, int T) {
+  int64_t U = 0;
+  for (int b = 0; b < B; ++b) U += (int64_t)mod.units(kv_lens, b, T) * Hkv;
+  return U;
+}
+
+// First token of unit u of a pair that owns units [pair_start, pair_start +
+// units).  The masked attention takes a pair's units from the newest to the
+// oldest: with a distance bias the largest scores come first, so the running
+// maximum is found once instead of being raised in every tile.
+template <class Mod>
+__device__ __forceinline__ int unit_token(int first_unit, int units, int64_t pair_start,
+                                          int64_t u) {
+  const int i = (int)(u - pair_start);
+  return (Mod::kOn ? first_unit + units - 1 - i : i) * kUnitTokens;
+}
+
+}  // namespace nvkv
