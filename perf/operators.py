@@ -106,8 +106,9 @@ def draw(rng):
     else:
         batch = _log(rng, 1, 16)
         high = _log(rng, 1, 120000 // batch)
-        c = {"op": "read", "hkv": hkv, "d": d, "ctx": "%dx%d-%d" % (batch, _log(rng, 1, high), high),
-             "skip": rng.randrange(0, min(100, high))}
+        low = _log(rng, 1, high)
+        c = {"op": "read", "hkv": hkv, "d": d, "ctx": "%dx%d-%d" % (batch, low, high),
+             "skip": rng.randrange(0, min(100, low))}
     c.pop("name", None)
     return c
 
