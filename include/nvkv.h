@@ -404,7 +404,8 @@ nvkv_status nvkv_pages_restore_k8v4(const nvkv_cache *cache, const int32_t *page
  * after p): the row's output is then 0.  Keys outside the interval are not
  * looked at: their pages may be absent from the page table (-1, freed, or
  * reused by another sequence) as long as no query of the call sees a key of
- * the page, and no bad page id is reported for them.
+ * the page, and no bad page id is reported for them.  The keys of a bad page
+ * that a query does see are left out (and reported).
  *   softcap:      > 0 and finite, or 0 for none.
  *   window:       > 0: that many keys up to the query's own; 0: none.
  *   alibi_slopes: device float [Hq], or NULL.

@@ -20,14 +20,15 @@ cudaError_t launch_decode_simt(const nvkv_cache &, const nvkv_seqs &, const void
 bool decode_tc_supported(const nvkv_cache &, int, int);
 bool decode_qk4_supported(const nvkv_cache &, int, int);
 cudaError_t launch_decode_qk4(const nvkv_cache &, const nvkv_seqs &, const void *, int, int, float,
-                              int, float *, float *, cudaStream_t);
+                              int, float *, float *, cudaStream_t, const ScoreMod *);
 cudaError_t launch_decode_qk4_k8v4(const nvkv_cache &, const nvkv_seqs &, const void *, int, int,
-                                   float, int, float *, float *, cudaStream_t);
+                                   float, int, float *, float *, cudaStream_t, const ScoreMod *);
 cudaError_t launch_decode_tc(const nvkv_cache &, const nvkv_seqs &, const void *, int, int, float,
-                             int, float *, float *, cudaStream_t);
+                             int, float *, float *, cudaStream_t, const ScoreMod *);
 bool prefill_tc_supported(const nvkv_cache &);
 cudaError_t launch_prefill_tc(const nvkv_cache &, const nvkv_seqs &, const void *, const int32_t *,
-                              int, int, int, float, void *, int, float *, float *, cudaStream_t);
+                              int, int, int, float, void *, int, float *, float *, cudaStream_t,
+                              const ScoreMod *);
 int prefill_max_splits();
 int prefill_auto_splits(int64_t, int);
 int prefill_tc_items(const nvkv_cache &, const nvkv_seqs &, int, int);
@@ -221,6 +222,51 @@ bool force_kernel(const char *name) {
 }
 bool force_simt() { return force_kernel("simt"); }
 
+// The decode kernel of the step's shape (nvkv_decode_kernel_name); mod: null
+// for plain causal attention.
+cudaError_t run_decode(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T, int Hq,
+                       float sm_scale, const DecodeArgs &a, cudaStream_t stream,
+                       const ScoreMod *mod) {
+  if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(c, T, Hq))
+    return launch_decode_qk4(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, mod);
+  if (!force_simt() && decode_tc_supported(c, T, Hq))
+    return launch_decode_tc(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, mod);
+  return launch_decode_simt(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, false, mod);
+}
+
+// The same over a K8V4 cache (nvkv_decode_kernel_name_k8v4).
+cudaError_t run_decode_k8v4(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T, int Hq,
+                            float sm_scale, const DecodeArgs &a, cudaStream_t stream,
+                            const ScoreMod *mod) {
+  if (!force_simt() && decode_qk4_supported(c, T, Hq))
+    return launch_decode_qk4_k8v4(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, mod);
+  return launch_decode_simt(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, true, mod);
+}
+
+// The key-split tensor-core prefill, else the CUDA-core one (arguments
+// checked); mod: null for plain causal attention.
+nvkv_status run_prefill_split(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
+                              const int32_t *cu_q, int total_q, int max_q, int Hq, float sm_scale,
+                              int num_splits, void *workspace, size_t workspace_bytes, void *out,
+                              cudaStream_t stream, const ScoreMod *mod) {
+  if (force_simt() || !prefill_tc_supported(c))
+    return cuda_status(
+        launch_prefill_simt(c, s, q, cu_q, total_q, Hq, sm_scale, out, stream, false, mod));
+  const int S = num_splits > 0 ? num_splits
+                               : prefill_auto_splits(prefill_tc_items(c, s, max_q, Hq),
+                                                     nvkv_default_num_splits());
+  float *ws_o = nullptr, *ws_lse = nullptr;
+  if (S > 1) {
+    const PrefillLayout w = prefill_layout(total_q, Hq, c.head_dim, S);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < w.total)
+      return NVKV_ERR_WORKSPACE;
+    ws_o = static_cast<float *>(workspace);
+    ws_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.lse_off);
+  }
+  return cuda_status(launch_prefill_tc(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out, S, ws_o,
+                                       ws_lse, stream, mod));
+}
+
 nvkv_status decode_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q, int32_t T,
                        int32_t num_q_heads, float sm_scale, const nvkv_score_mod *mod,
                        int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
@@ -233,8 +279,9 @@ nvkv_status decode_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const voi
   if ((st = check_mod(mod, m)) != NVKV_OK) return st;
   if (!out || !aligned16(out)) return NVKV_ERR_INVALID_ARG;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_decode_simt(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o,
-                                           a.ws_lse, s, k8, &m);
+  const cudaError_t e =
+      k8 ? run_decode_k8v4(*cache, *seqs, q, T, num_q_heads, sm_scale, a, s, &m)
+         : run_decode(*cache, *seqs, q, T, num_q_heads, sm_scale, a, s, &m);
   if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_combine(*seqs, a.ws_o, a.ws_lse, T, num_q_heads, cache->num_kv_heads,
                                     cache->head_dim, a.S, out, s, &m));
@@ -252,8 +299,11 @@ nvkv_status prefill_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const vo
   if (num_splits < 0 || num_splits > prefill_max_splits()) return NVKV_ERR_INVALID_ARG;
   if (total_q == 0) return NVKV_OK;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
-                                         out, s, k8, &m));
+  if (k8)
+    return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
+                                           out, s, true, &m));
+  return run_prefill_split(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale,
+                           num_splits, workspace, workspace_bytes, out, s, &m);
 }
 
 nvkv_status read_rows(const nvkv_cache *cache, const nvkv_seqs *seqs, const int32_t *starts,
@@ -388,15 +438,8 @@ nvkv_status nvkv_decode_attn(const nvkv_cache *cache, const nvkv_seqs *seqs, con
   const nvkv_status st = check_decode(cache, seqs, q, T, num_q_heads, sm_scale, num_splits,
                                       workspace, workspace_bytes, a);
   if (st != NVKV_OK) return st;
-  cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-  if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(*cache, T, num_q_heads))
-    return cuda_status(
-        launch_decode_qk4(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o, a.ws_lse, st_));
-  if (!force_simt() && decode_tc_supported(*cache, T, num_q_heads))
-    return cuda_status(
-        launch_decode_tc(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o, a.ws_lse, st_));
-  return cuda_status(launch_decode_simt(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o,
-                                        a.ws_lse, st_, false, nullptr));
+  return cuda_status(run_decode(*cache, *seqs, q, T, num_q_heads, sm_scale, a,
+                                reinterpret_cast<cudaStream_t>(stream), nullptr));
 }
 
 nvkv_status nvkv_combine(const nvkv_seqs *seqs, const void *workspace, int32_t T,
@@ -424,7 +467,7 @@ nvkv_status nvkv_prefill_attn(const nvkv_cache *cache, const nvkv_seqs *seqs, co
   cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
   if (!force_simt() && prefill_tc_supported(*cache))
     return cuda_status(launch_prefill_tc(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads,
-                                         sm_scale, out, 1, nullptr, nullptr, st_));
+                                         sm_scale, out, 1, nullptr, nullptr, st_, nullptr));
   return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
                                          out, st_, false, nullptr));
 }
@@ -460,24 +503,9 @@ nvkv_status nvkv_prefill_attn_split(const nvkv_cache *cache, const nvkv_seqs *se
   if (st != NVKV_OK) return st;
   if (num_splits < 0 || num_splits > prefill_max_splits()) return NVKV_ERR_INVALID_ARG;
   if (total_q == 0) return NVKV_OK;
-  cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-  if (force_simt() || !prefill_tc_supported(*cache))
-    return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
-                                           out, st_, false, nullptr));
-  const int S = num_splits > 0 ? num_splits
-                               : prefill_auto_splits(
-                                     prefill_tc_items(*cache, *seqs, max_q, num_q_heads),
-                                     nvkv_default_num_splits());
-  float *ws_o = nullptr, *ws_lse = nullptr;
-  if (S > 1) {
-    const PrefillLayout w = prefill_layout(total_q, num_q_heads, cache->head_dim, S);
-    if (!workspace || !aligned16(workspace) || workspace_bytes < w.total)
-      return NVKV_ERR_WORKSPACE;
-    ws_o = static_cast<float *>(workspace);
-    ws_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.lse_off);
-  }
-  return cuda_status(launch_prefill_tc(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads,
-                                       sm_scale, out, S, ws_o, ws_lse, st_));
+  return run_prefill_split(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale,
+                           num_splits, workspace, workspace_bytes, out,
+                           reinterpret_cast<cudaStream_t>(stream), nullptr);
 }
 
 size_t nvkv_k8v4_page_bytes(int32_t num_kv_heads, int32_t head_dim) {
@@ -508,12 +536,8 @@ nvkv_status nvkv_decode_attn_k8v4(const nvkv_cache *cache, const nvkv_seqs *seqs
   const nvkv_status st = check_decode(cache, seqs, q, T, num_q_heads, sm_scale, num_splits,
                                       workspace, workspace_bytes, a);
   if (st != NVKV_OK) return st;
-  cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-  if (!force_simt() && decode_qk4_supported(*cache, T, num_q_heads))
-    return cuda_status(launch_decode_qk4_k8v4(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S,
-                                              a.ws_o, a.ws_lse, st_));
-  return cuda_status(launch_decode_simt(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o,
-                                        a.ws_lse, st_, true, nullptr));
+  return cuda_status(run_decode_k8v4(*cache, *seqs, q, T, num_q_heads, sm_scale, a,
+                                     reinterpret_cast<cudaStream_t>(stream), nullptr));
 }
 
 const char *nvkv_decode_kernel_name_k8v4(const nvkv_cache *cache, int32_t T,

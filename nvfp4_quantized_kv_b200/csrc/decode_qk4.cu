@@ -72,7 +72,7 @@
 //    waits into no-ops and lets the kernel drain and free its Tensor Memory.
 #include <cfloat>
 
-#include "nvkv_common.cuh"
+#include "score_mod.cuh"
 #include "sm100.cuh"
 
 namespace nvkv {
@@ -153,7 +153,8 @@ struct Fmt {
   static constexpr int kOffM = kOffRed + 4 * kNP * 4;              // float [kNP]
   static constexpr int kOffAlpha = kOffM + kNP * 4;
   static constexpr int kOffNvis = kOffAlpha + kNP * 4;
-  static constexpr int kOffFlags = kOffNvis + kNP * 4;             // int[4]: abort at [2]
+  static constexpr int kOffRow = kOffNvis + kNP * 4;               // int4 [8] (ScoreMod only)
+  static constexpr int kOffFlags = kOffRow + 8 * 16;               // int[4]: abort at [2]
   static constexpr int kOffPages = kOffFlags + 16;                 // int[stages][8]
   static constexpr int kOffKsv = kOffPages + kStages * kUnitPages * 4;  // u32 [ks slot]: pages present
   static constexpr int kOffBars = kOffKsv + ((kKsSlots > 0 ? kKsSlots : 1) * 4 + 7) / 8 * 8;
@@ -168,7 +169,7 @@ struct Fmt {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(kOffQ % 1024 == 0 && kOffP % 128 == 0 && kOffKs % 128 == 0 &&
                     kOffVsc % 16 == 0 && kOffSfb % 16 == 0 && kOffPages % 16 == 0 &&
-                    kOffBars % 8 == 0,
+                    kOffRow % 16 == 0 && kOffBars % 8 == 0,
                 "alignment");
 };
 
@@ -177,6 +178,7 @@ struct Shared {
   uint32_t *vsc;
   float *fac, *red, *m_s, *alpha_s;
   int32_t *nvis_s, *pages;
+  int4 *row_s;     // ScoreMod: (first visible key, one past the last, position, slope bits) of a row
   uint32_t *ksv;  // [ks slot]: bit p set when page p of the unit is present (NVFP4)
   volatile int *flags;
   // A barrier of a ring slot completes once per unit that uses the slot.  A
@@ -200,27 +202,44 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
   return guarded_wait(bar, parity, flags + 2, err, kWaitBudget);  // flags[2]: abort
 }
 
-// Segment of the CTA's range: units [u, seg_end) of pair (b, h).
+// Segment of the CTA's range: units [u, seg_end) of pair (b, h).  With a
+// ScoreMod the pair's units start at first_unit of the sequence and no key
+// below lo is visible.
 struct Seg {
   int b, h, kv_len;
+  int lo, first_unit, units;
   int64_t pair_start, seg_end;
   bool bad;
 };
 
-__device__ __forceinline__ Seg segment_at(int64_t u, int64_t u1, const int32_t *kv_lens, int B,
-                                          int Hkv, int max_kv_len, int max_pages) {
+template <class Mod>
+__device__ __forceinline__ Seg segment_at(const Mod &mod, int T, int64_t u, int64_t u1,
+                                          const int32_t *kv_lens, int B, int Hkv, int max_kv_len,
+                                          int max_pages) {
   Seg s;
-  int units;
-  locate_pair(kv_lens, B, Hkv, u, s.b, s.h, s.pair_start, units);
-  s.seg_end = min(u1, s.pair_start + units);
+  locate_pair_mod(mod, kv_lens, B, Hkv, T, u, s.b, s.h, s.pair_start, s.units);
+  s.seg_end = min(u1, s.pair_start + s.units);
+  s.lo = s.first_unit = 0;
+  if (s.b >= B) {  // past the last unit
+    s.kv_len = 0;
+    s.bad = false;
+    return s;
+  }
   s.kv_len = kv_lens[s.b];
+  if constexpr (Mod::kOn) {
+    int n;
+    visible_units(s.kv_len, T, mod.start(s.b), mod.window, s.lo, s.first_unit, n);
+  }
   s.bad = s.kv_len > max_kv_len || s.kv_len > max_pages * kPageTokens;
   if (s.bad) s.kv_len = 0;  // nothing of a bad sequence is read
   return s;
 }
 
-__device__ __forceinline__ int page_of(const int32_t *pt_row, int tok, int kv_len, int num_pages) {
-  if (tok >= kv_len) return -1;
+// Page of the 16 tokens from `tok` on; -1 when it is absent or when none of
+// them is in [lo, kv_len).
+__device__ __forceinline__ int page_of(const int32_t *pt_row, int tok, int lo, int kv_len,
+                                       int num_pages) {
+  if (tok >= kv_len || tok + kPageTokens <= lo) return -1;
   const int p = pt_row[tok / kPageTokens];
   return (p >= 0 && p < num_pages) ? p : -1;
 }
@@ -259,7 +278,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 // and scales, all over 128-byte rows of the pool), true = K8V4 (tmap_k: 3-D
 // [block][token][256 B], 128-byte SW128 boxes of 16 tokens, one per head_dim
 // half; tmap_ks: [block][64 B] row scales; tmap_v: [block][18][128 B]).
-template <int RM, bool K8>
+template <int RM, bool K8, class Mod>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_ks,
@@ -267,7 +286,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const int32_t *__restrict__ page_table, int max_pages,
                   const int32_t *__restrict__ kv_lens, int B, int max_kv_len,
                   const __nv_bfloat16 *__restrict__ q, int T, int Hq, float qscale, int S,
-                  float *__restrict__ ws_o, float *__restrict__ ws_lse, int32_t *err) {
+                  float *__restrict__ ws_o, float *__restrict__ ws_lse, int32_t *err, Mod mod) {
   // RM: query rows per pair rounded up to an even count (padding rows are
   // zero); the score MMA has N = RM * kTerms columns.
   static_assert(RM % 2 == 0 && RM >= 2 && RM <= kRowsCap, "rows");
@@ -279,7 +298,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 kOffSfb = F::kOffSfb, kOffFac = F::kOffFac, kOffRed = F::kOffRed,
                 kOffM = F::kOffM, kOffAlpha = F::kOffAlpha,
                 kOffNvis = F::kOffNvis, kOffFlags = F::kOffFlags, kOffPages = F::kOffPages,
-                kOffKsv = F::kOffKsv,
+                kOffKsv = F::kOffKsv, kOffRow = F::kOffRow,
                 kOffBars = F::kOffBars, kOffTmem = F::kOffTmem;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -296,6 +315,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
   sh.m_s = reinterpret_cast<float *>(smem + kOffM);
   sh.alpha_s = reinterpret_cast<float *>(smem + kOffAlpha);
   sh.nvis_s = reinterpret_cast<int32_t *>(smem + kOffNvis);
+  sh.row_s = reinterpret_cast<int4 *>(smem + kOffRow);
   sh.flags = reinterpret_cast<volatile int *>(smem + kOffFlags);
   sh.pages = reinterpret_cast<int32_t *>(smem + kOffPages);
   sh.ksv = reinterpret_cast<uint32_t *>(smem + kOffKsv);
@@ -365,8 +385,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
   tc_fence_after();
   const uint32_t tmem = *sh.tmem_slot;
 
-  int64_t U = 0;
-  for (int b = 0; b < B; ++b) U += (int64_t)units_of_len(kv_lens[b]) * Hkv;
+  const int64_t U = total_units(mod, kv_lens, B, Hkv, T);
   const int c = blockIdx.x;
   const int64_t u0 = U > 0 ? range_begin(c, U, S) : 0;
   const int64_t u1 = U > 0 ? range_begin(c + 1, U, S) : 0;
@@ -393,12 +412,14 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     const int p = lane & 7;
     int64_t u = u0;
-    Seg sg = segment_at(u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+    Seg sg = segment_at(mod, T, u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
     auto page_for = [&](const Seg &g, int64_t uu) -> int {
-      const int tok = (int)(uu - g.pair_start) * kUnitTokens + p * kPageTokens;
+      const int tok =
+          unit_token<Mod>(g.first_unit, g.units, g.pair_start, uu) + p * kPageTokens;
       const int32_t *pt = page_table + (size_t)g.b * max_pages;
-      const int pg = page_of(pt, tok, g.kv_len, num_pages);
-      if (big && lane < kUnitPages && tok < g.kv_len && pg < 0) report(err, NVKV_DEVERR_PAGE_ID);
+      const int pg = page_of(pt, tok, g.lo, g.kv_len, num_pages);
+      if (big && lane < kUnitPages && tok < g.kv_len && tok + kPageTokens > g.lo && pg < 0)
+        report(err, NVKV_DEVERR_PAGE_ID);
       return pg;
     };
     int cur = u < u1 ? page_for(sg, u) : -1;
@@ -408,7 +429,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
       int nxt = -1;
       Seg nsg = sg;
       if (u + 1 < u1) {
-        if (u + 1 >= sg.seg_end) nsg = segment_at(u + 1, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+        if (u + 1 >= sg.seg_end) nsg = segment_at(mod, T, u + 1, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
         nxt = page_for(nsg, u + 1);
       }
       if (uc >= (uint32_t)ring) {
@@ -467,7 +488,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // value MMAs of each unit once its V^T and P are ready.  Each commits
     // its own MMAs; the tensor pipe runs both streams.
     if (lane == 0) {
-      int64_t seg_end = segment_at(u0, u1, kv_lens, B, Hkv, max_kv_len, max_pages).seg_end;
+      int64_t seg_end = segment_at(mod, T, u0, u1, kv_lens, B, Hkv, max_kv_len, max_pages).seg_end;
       bool issued = false;
       if (warp == kMmaWarp) {
         // NVFP4: E2M1 x E2M1 block-scaled; K8V4: E4M3 x E4M3 (kind::f8f6f4,
@@ -480,7 +501,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           const int64_t uu = u0 + qk;
           const bool opens = qk == 0 || uu >= seg_end;
           if (uu >= seg_end) {
-            seg_end = segment_at(uu, u1, kv_lens, B, Hkv, max_kv_len, max_pages).seg_end;
+            seg_end = segment_at(mod, T, uu, u1, kv_lens, B, Hkv, max_kv_len, max_pages).seg_end;
             ++seg_idx;
           }
           if (opens) wait_bar(sh.qready, seg_idx & 1, sh.flags, err);
@@ -526,7 +547,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           const int64_t uu = u0 + pv;
           const bool first = pv == 0 || uu >= seg_end;  // O^T starts from zero
           if (uu >= seg_end)
-            seg_end = segment_at(uu, u1, kv_lens, B, Hkv, max_kv_len, max_pages).seg_end;
+            seg_end = segment_at(mod, T, uu, u1, kv_lens, B, Hkv, max_kv_len, max_pages).seg_end;
           const int ps = pv % kPSlots;
           wait_bar(&sh.pready[ps], (pv / kPSlots) & 1, sh.flags, err);
           const uint32_t pslot = pb + ps * kPSlotBytes;
@@ -745,7 +766,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint32_t uc = 0;
     uint32_t seg_idx = 0;
     for (int64_t u = u0; u < u1; ++seg_idx) {
-      const Seg sg = segment_at(u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+      const Seg sg = segment_at(mod, T, u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
       if (sg.bad && threadIdx.x == 0) report(err, NVKV_DEVERR_LENGTH);
       const int64_t seg_start = u;
       const size_t slot = (size_t)c + (size_t)sg.b * Hkv + sg.h;
@@ -769,6 +790,19 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           sh.nvis_s[stid] = stid < R ? sg.kv_len - T + stid / G + 1 : 0;
           sh.m_s[stid] = -FLT_MAX;
         }
+        if constexpr (Mod::kOn) {
+          if (stid < RM) {
+            int4 row = make_int4(0, 0, 0, 0);
+            if (stid < R) {
+              const int pos = sg.kv_len - T + stid / G;
+              key_range(pos, sg.kv_len, mod.start(sg.b), mod.window, mod.prefix_of(sg.b), row.x,
+                        row.y);
+              row.z = pos;
+              row.w = __float_as_int(mod.slope2(sg.h * G + stid % G));
+            }
+            sh.row_s[stid] = row;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < RM; ++i) l_part[i] = 0.f, mr[i] = -FLT_MAX;
         wait_bar(sh.qready, seg_idx & 1, sh.flags, err);
@@ -783,7 +817,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const bool first = (u == seg_start);
         const int stage = uc % kStages;
         const uint8_t *vb = sh.stages + stage * kStageBytes + kKTileBytes;
-        const int tok0 = (int)(u - sg.pair_start) * kUnitTokens;
+        const int tok0 = unit_token<Mod>(sg.first_unit, sg.units, sg.pair_start, u);
         if (!smx) {
           wait_bar(&sh.full[stage], (uc / kStages) & 1, sh.flags, err);
           // ---- scale pairs of this warp's two groups (head_dim rows
@@ -804,6 +838,13 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (nval < 8) {
               w0 = nval >= 4 ? w0 : nval <= 0 ? 0u : w0 & ((1u << (8 * nval)) - 1u);
               w1 = nval <= 4 ? 0u : w1 & ((1u << (8 * (nval - 4))) - 1u);
+            }
+            if constexpr (Mod::kOn) {  // tokens before every query's interval
+              const int nlow = sg.lo - (tok0 + 16 * pp + 8 * h8);
+              if (nlow > 0) {
+                w0 = nlow >= 4 ? 0u : w0 & (0xffffffffu << (8 * nlow));
+                w1 = nlow >= 8 ? 0u : nlow <= 4 ? w1 : w1 & (0xffffffffu << (8 * (nlow - 4)));
+              }
             }
             const uint4 t4 = make_uint4(e4m3x2_to_f16x2(__byte_perm(w0, w1, 0x40)),
                                         e4m3x2_to_f16x2(__byte_perm(w0, w1, 0x51)),
@@ -885,7 +926,12 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
             } else {
               present = (pm_cur >> ((32 * lq + lane) >> 4)) & 1u;
             }
-            const bool vis_all = tok0 + kUnitTokens <= sg.kv_len - T + 1 && present;
+            // every key of the unit is visible to every query (the first
+            // query's interval ends first, the last one's starts last)
+            bool vis_all = tok0 + kUnitTokens <= sg.kv_len - T + 1 && present;
+            if constexpr (Mod::kOn)
+              vis_all = vis_all && tok0 >= sg.lo &&
+                        (mod.window <= 0 || tok0 >= sg.kv_len - mod.window);
 #pragma unroll
             for (int j = 0; j < RM; ++j) {
               const uint32_t *c8 = rr + j * kTerms;
@@ -906,8 +952,22 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const float2 a2 = add_f32x2(a0, a1);
                 sc = (a2.x + a2.y) * facr[j];
               }
-              const int nv = vis_all ? (j < R ? 0x7fffffff : 0) : sh.nvis_s[j];
-              x[j] = pos < nv && present ? sc : -INFINITY;
+              if constexpr (Mod::kOn) {
+                if (mod.cap2 > 0.f) sc = mod.cap(sc);
+                if (mod.slopes) {
+                  const int4 row = sh.row_s[j];
+                  sc = fmaf(-__int_as_float(row.w), fabsf((float)(row.z - pos)), sc);
+                }
+                bool in = j < R;
+                if (!vis_all) {
+                  const int4 row = sh.row_s[j];
+                  in = pos >= row.x && pos < row.y && present;
+                }
+                x[j] = in ? sc : -INFINITY;
+              } else {
+                const int nv = vis_all ? (j < R ? 0x7fffffff : 0) : sh.nvis_s[j];
+                x[j] = pos < nv && present ? sc : -INFINITY;
+              }
             }
           }
           // Weights: p = 2^(score - running max) in fp32 (2^-inf = 0), as
@@ -1133,9 +1193,10 @@ bool make_k8_maps(const nvkv_cache &c, CUtensorMap *mk, CUtensorMap *mks, CUtens
              CUDA_SUCCESS;
 }
 
-template <bool K8>
+template <bool K8, class Mod>
 cudaError_t launch_fmt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T, int Hq,
-                       float sm_scale, int S, float *ws_o, float *ws_lse, cudaStream_t stream) {
+                       float sm_scale, int S, float *ws_o, float *ws_lse, cudaStream_t stream,
+                       const Mod &mod) {
   CUtensorMap map_k, map_ks, map_v;
   const bool ok = K8 ? make_k8_maps(c, &map_k, &map_ks, &map_v)
                      : make_map(c, kKRows, CU_TENSOR_MAP_SWIZZLE_128B, &map_k) &&
@@ -1144,15 +1205,16 @@ cudaError_t launch_fmt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, i
   if (!ok) return cudaErrorNotSupported;
   const float qscale = sm_scale * 1.4426950408889634f;
   const int R = T * (Hq / c.num_kv_heads);
-  auto kernel = R <= 2 ? decode_qk4_kernel<2, K8> : R <= 4 ? decode_qk4_kernel<4, K8>
-                                                             : decode_qk4_kernel<6, K8>;
+  auto kernel = R <= 2   ? decode_qk4_kernel<2, K8, Mod>
+                : R <= 4 ? decode_qk4_kernel<4, K8, Mod>
+                         : decode_qk4_kernel<6, K8, Mod>;
   const int smem = Fmt<K8>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<S, kThreads, smem, stream>>>(
       map_k, map_ks, map_v, c.num_pages, c.num_kv_heads, s.page_table, s.max_pages_per_seq,
       s.kv_lens, s.batch, s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), T, Hq, qscale, S,
-      ws_o, ws_lse, s.err_word);
+      ws_o, ws_lse, s.err_word, mod);
   return cudaGetLastError();
 }
 
@@ -1166,18 +1228,21 @@ bool decode_qk4_supported(const nvkv_cache &c, int T, int Hq) {
   return c.head_dim == kD && R >= 1 && R <= kRowsCap && encode_fn() != nullptr;
 }
 
+// mod: null for plain causal attention.
 cudaError_t launch_decode_qk4(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
                               int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
-                              cudaStream_t stream) {
-  return launch_fmt<false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream);
+                              cudaStream_t stream, const ScoreMod *mod) {
+  return mod ? launch_fmt<false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod)
+             : launch_fmt<false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, NoMod{});
 }
 
 // The same kernel over a K8V4 cache (E4M3 K rows with an fp32 row scale,
 // NVFP4 V): the scores on kind::f8f6f4 from the cached E4M3 bytes.
 cudaError_t launch_decode_qk4_k8v4(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
                                    int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
-                                   cudaStream_t stream) {
-  return launch_fmt<true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream);
+                                   cudaStream_t stream, const ScoreMod *mod) {
+  return mod ? launch_fmt<true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod)
+             : launch_fmt<true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, NoMod{});
 }
 
 }  // namespace nvkv

@@ -25,7 +25,7 @@
 //    running max (raised lazily, only when it grows by more than 2^8, then O
 //    is rescaled), the denominator of the f16 weights, and the final O / l.
 //  * One thread issues the MMAs, event-driven; every wait is bounded.
-#include "nvkv_common.cuh"
+#include "score_mod.cuh"
 #include "sm100.cuh"
 
 namespace nvkv {
@@ -71,7 +71,8 @@ constexpr int kOffV = kOffK + 2 * kKTileBytes;
 constexpr int kVscBytes = kTilePages * 16 * 8 * 4;            // V scales of a tile as f16 pairs
 constexpr int kOffVsc = kOffV + 2 * kVTileBytes;              // 2 tables (tile parity)
 constexpr int kOffPages = kOffVsc + 2 * kVscBytes;            // int[stages][4]
-constexpr int kOffFlags = kOffPages + kStages * kTilePages * 4;
+constexpr int kOffPres = kOffPages + kStages * kTilePages * 4;  // u32[4] (ScoreMod only)
+constexpr int kOffFlags = kOffPres + 16;
 constexpr int kOffBars = kOffFlags + 16;
 constexpr int kNumBars = 2 * kStages + 2 * 5 + 2;  // full, empty; kready, vready, sready, pready, pvdone; qready, final
 constexpr int kOffTmem = kOffBars + kNumBars * 8;
@@ -88,6 +89,7 @@ __device__ __forceinline__ uint32_t dup_scale(uint32_t byte) {
   return e4m3x2_to_f16x2(byte | (byte << 8));
 }
 
+template <class Mod>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hkv,
                   const int32_t *__restrict__ page_table, int max_pages,
@@ -95,7 +97,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
                   const __nv_bfloat16 *__restrict__ q, const int32_t *__restrict__ cu_q,
                   int total_q, int Hq, float qscale, __nv_bfloat16 *__restrict__ out,
                   int num_splits, float *__restrict__ ws_o, float *__restrict__ ws_lse,
-                  int32_t *err) {
+                  int32_t *err, Mod mod) {
   // blockIdx.x = m-tile * num_splits + split: split s of an m-tile takes the
   // s-th of num_splits equal runs of its key tiles and, when num_splits > 1,
   // leaves O / l and log2(l) + m of its rows in the workspace for the merge.
@@ -111,12 +113,40 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
                    kv_len > max_kv_len || kv_len > max_pages * kPageTokens;
   const int i_first = (128 * mt) / G;
   const int i_last = min(n_b - 1, (128 * mt + 127) / G);
-  const int pos_last = kv_len - n_b + i_last;     // keys 0 .. pos_last are needed
-  const int ntiles_all = bad ? 0 : pos_last / kTileTokens + 1;
+  int pos_last = kv_len - n_b + i_last;     // keys 0 .. pos_last are needed
+  int key_lo = 0;                           // (ScoreMod: keys key_lo .. pos_last)
+  if constexpr (Mod::kOn) {
+    // The union of the rows' intervals: every warp scans all rows.
+    int lo = 0x7fffffff, hi = 0;
+    if (!bad) {
+      const int prefix = mod.prefix_of(b);
+      for (int i = i_first + (threadIdx.x & 31); i <= i_last; i += 32) {
+        int l, h2;
+        key_range(kv_len - n_b + i, kv_len, mod.start(q0 + i), mod.window, prefix, l, h2);
+        if (l < h2) lo = min(lo, l), hi = max(hi, h2);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    key_lo = min(lo, hi);  // (hi = 0: nothing is seen)
+    pos_last = hi - 1;
+  }
+  const int tile_lo = key_lo / kTileTokens;
+  const int ntiles_all =
+      bad || pos_last < key_lo ? 0 : pos_last / kTileTokens + 1 - tile_lo;
   // This CTA's key tiles j0 .. j0 + ntiles - 1; every ring and barrier below
   // counts from its first tile.
   const int j0 = (int)((int64_t)split * ntiles_all / num_splits);
   const int ntiles = (int)((int64_t)(split + 1) * ntiles_all / num_splits) - j0;
+  // First key of the CTA's j-th tile.  The masked attention goes from the
+  // newest tile to the oldest: with a distance bias the largest scores come
+  // first and the running maximum is not raised again in every tile.
+  auto tile_key = [&](int j) {
+    return (Mod::kOn ? tile_lo + ntiles_all - 1 - (j0 + j) : j0 + j) * kTileTokens;
+  };
   // Output rows exist only when the chunk lies inside the total_q rows.
   const bool rows_ok = n_b >= 0 && q0 >= 0 && q0 + n_b <= total_q;
 
@@ -128,6 +158,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
   uint8_t *vtiles = smem + kOffV;
   uint32_t *vsc = reinterpret_cast<uint32_t *>(smem + kOffVsc);  // [2][page][group][8]
   int32_t *spages = reinterpret_cast<int32_t *>(smem + kOffPages);
+  // ScoreMod: bit p of entry (tile & 3) is set when page p of the tile is
+  // present, so the softmax leaves the keys of an absent page out.  Written
+  // with the tile's K; the K of tile j + 4 is written after the scores of
+  // tile j + 2, which wait for the value MMAs of tile j.
+  volatile uint32_t *present = reinterpret_cast<volatile uint32_t *>(smem + kOffPres);
   volatile int *flags = reinterpret_cast<volatile int *>(smem + kOffFlags);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBars);
   uint64_t *full = bars, *empty = bars + kStages;
@@ -170,8 +205,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
     prefetch_tmap(&tmap);
     const int p = lane & 3;
     auto page_for = [&](int j) -> int {
-      const int tok = j * kTileTokens + p * kPageTokens;
+      const int tok = tile_key(j) + p * kPageTokens;
       if (tok > pos_last) return -1;  // keys past the last query are never needed
+      if (Mod::kOn && tok + kPageTokens <= key_lo) return -1;
       const int pg = pt[tok / kPageTokens];
       if (pg < 0 || pg >= num_pages) {
         if (lane < kTilePages) report(err, NVKV_DEVERR_PAGE_ID);
@@ -179,10 +215,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
       }
       return pg;
     };
-    int cur = ntiles > 0 ? page_for(j0) : -1;
+    int cur = ntiles > 0 ? page_for(0) : -1;
     for (int j = 0; j < ntiles; ++j) {
       const int stage = j % kStages;
-      const int nxt = j + 1 < ntiles ? page_for(j0 + j + 1) : -1;
+      const int nxt = j + 1 < ntiles ? page_for(j + 1) : -1;
       if (j >= kStages) {
         if (lane == 0) wait_bar(&empty[stage], ((j / kStages) + 1) & 1, flags, err);
         __syncwarp();
@@ -271,7 +307,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
       wait_bar(&full[stage], (j / kStages) & 1, flags, err);
       const int4 pg4 = *reinterpret_cast<const int4 *>(spages + stage * kTilePages);
       const int pgs[4] = {pg4.x, pg4.y, pg4.z, pg4.w};
-      const int tok0 = (j0 + j) * kTileTokens;
+      const int tok0 = tile_key(j);
       {
         // This tile's V scales, converted once: thread t takes 4 consecutive
         // tokens of one (page, group); the 16 V^T rows of a group share them.
@@ -290,11 +326,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
         wait_bar(&sready[slot], ((j >> 1) + 1) & 1, flags, err);
         tc_fence_after();
       }
+      if (Mod::kOn && t == 0)
+        present[j & 3] = (pgs[0] >= 0 ? 1u : 0u) | (pgs[1] >= 0 ? 2u : 0u) |
+                         (pgs[2] >= 0 ? 4u : 0u) | (pgs[3] >= 0 ? 8u : 0u);
       {
         // thread = token n (32 consecutive per warp), two 32-d chunks
         const int n = t & 63, cp = t >> 6;
         const int p = n >> 4, s = n & 15;
-        const bool ok = pgs[p] >= 0 && tok0 + n <= pos_last;
+        const bool ok = pgs[p] >= 0 && tok0 + n <= pos_last && (!Mod::kOn || tok0 + n >= key_lo);
         const uint8_t *pg = stg + p * kPagePitch;
         uint32_t sc = 0;  // scale bytes of groups 4cp .. 4cp+3
         if (ok)
@@ -372,6 +411,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
                 else if (t0 + 1 > pos_last) o8[i] &= 0xffffu;
               }
             }
+            if (Mod::kOn && ptok < key_lo) {  // and those before the first visible key
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int t0 = ptok + 2 * i;
+                if (t0 + 1 < key_lo) o8[i] = 0u;
+                else if (t0 < key_lo) o8[i] &= 0xffff0000u;
+              }
+            }
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) o8[i] = 0u;
@@ -398,6 +445,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
     const bool valid = gr < rows && !bad;
     const int i = gr / G, g = gr % G;
     const int pos = kv_len - n_b + i;        // keys 0 .. pos are visible
+    int row_lo = 0, row_hi = 0;              // (ScoreMod: keys row_lo .. row_hi - 1)
+    float slope2 = 0.f;
+    if constexpr (Mod::kOn) {
+      if (valid) {
+        key_range(pos, kv_len, mod.start(q0 + i), mod.window, mod.prefix_of(b), row_lo, row_hi);
+        slope2 = mod.slope2(h * G + g);
+      }
+    }
     // Q row -> Tensor Memory (A operand), f16, pre-scaled to base-2 scores.
     {
       const __nv_bfloat16 *qr = q + ((size_t)(q0 + i) * Hq + h * G + g) * kD;
@@ -447,9 +502,33 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
           x[48 + e] = __uint_as_float(r3[e]);
         }
       }
-      const int key0 = (j0 + j) * kTileTokens;
+      const int key0 = tile_key(j);
       float tmax = -INFINITY;
-      if (valid && key0 + kTileTokens - 1 <= pos) {
+      if constexpr (Mod::kOn) {
+        if (mod.cap2 > 0.f) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) x[e] = mod.cap(x[e]);
+        }
+        if (mod.slopes) {
+          // (distances are exact; with a prefix a key may lie ahead)
+          const float d0 = (float)(pos - key0);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), x[e]);
+        }
+        if (key0 < row_lo || key0 + kTileTokens > row_hi) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (key0 + e < row_lo || key0 + e >= row_hi) x[e] = -INFINITY;
+        }
+        const uint32_t here = present[j & 3];
+        if (here != 15u) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (!((here >> (e / kPageTokens)) & 1u)) x[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 64; ++e) tmax = fmaxf(tmax, x[e]);
+      } else if (valid && key0 + kTileTokens - 1 <= pos) {
 #pragma unroll
         for (int e = 0; e < 64; ++e) tmax = fmaxf(tmax, x[e]);
       } else {
@@ -637,25 +716,26 @@ int prefill_tc_items(const nvkv_cache &c, const nvkv_seqs &s, int max_q, int Hq)
   return (int)(((int64_t)max_q * G + 127) / 128) * c.num_kv_heads * s.batch;
 }
 
-cudaError_t launch_prefill_tc(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
-                              const int32_t *cu_q, int total_q, int max_q, int Hq,
-                              float sm_scale, void *out, int num_splits, float *ws_o,
-                              float *ws_lse, cudaStream_t stream) {
+template <class Mod>
+static cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
+                                      const int32_t *cu_q, int total_q, int max_q, int Hq,
+                                      float sm_scale, void *out, int num_splits, float *ws_o,
+                                      float *ws_lse, cudaStream_t stream, const Mod &mod) {
   CUtensorMap map;
   if (!make_pool_tmap(c, &map)) return cudaErrorNotSupported;
   if (num_splits < 1 || num_splits > kMaxSplits || (num_splits > 1 && (!ws_o || !ws_lse)))
     return cudaErrorInvalidValue;
   const int G = Hq / c.num_kv_heads;
   const int mtiles = (max_q * G + 127) / 128;
-  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel,
+  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<Mod>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)(mtiles * num_splits), (unsigned)c.num_kv_heads, (unsigned)s.batch);
-  prefill_tc_kernel<<<grid, kThreads, kSmemBytes, stream>>>(
+  prefill_tc_kernel<Mod><<<grid, kThreads, kSmemBytes, stream>>>(
       map, c.num_pages, c.num_kv_heads, s.page_table, s.max_pages_per_seq, s.kv_lens,
       s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), cu_q, total_q, Hq,
       sm_scale * 1.4426950408889634f, static_cast<__nv_bfloat16 *>(out), num_splits,
-      num_splits > 1 ? ws_o : nullptr, ws_lse, s.err_word);
+      num_splits > 1 ? ws_o : nullptr, ws_lse, s.err_word, mod);
   if ((e = cudaGetLastError()) != cudaSuccess || num_splits == 1) return e;
   const dim3 mgrid((unsigned)(((int64_t)max_q * Hq + kMergeWarps - 1) / kMergeWarps),
                    (unsigned)s.batch);
@@ -663,6 +743,17 @@ cudaError_t launch_prefill_tc(const nvkv_cache &c, const nvkv_seqs &s, const voi
       ws_o, ws_lse, num_splits, cu_q, total_q, Hq, G, 128 * mtiles,
       static_cast<__nv_bfloat16 *>(out));
   return cudaGetLastError();
+}
+
+// mod: null for plain causal attention.
+cudaError_t launch_prefill_tc(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
+                              const int32_t *cu_q, int total_q, int max_q, int Hq,
+                              float sm_scale, void *out, int num_splits, float *ws_o,
+                              float *ws_lse, cudaStream_t stream, const ScoreMod *mod) {
+  return mod ? launch_prefill_mod(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out, num_splits,
+                                  ws_o, ws_lse, stream, *mod)
+             : launch_prefill_mod(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out, num_splits,
+                                  ws_o, ws_lse, stream, NoMod{});
 }
 
 }  // namespace nvkv
