@@ -441,8 +441,11 @@ nvkv_status nvkv_decode_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs *
                                       size_t workspace_bytes, void *out, nvkv_stream_t stream);
 
 /* nvkv_prefill_attn_split (same arguments, layouts, workspace and checks),
- * with the scores of `mod`.  A prefix is seen in both directions as far as
- * it is cached: put it into one chunk.
+ * with the scores of `mod`, on the tensor cores for both head_dims.
+ * num_splits = 0 takes the automatic count that the workspace has room for
+ * (1 for a NULL one; nvkv_prefill_workspace_bytes(..., 0) is enough for any).
+ * A prefix is seen in both directions as far as it is cached: put it into one
+ * chunk.
  *
  * nvkv_prefill_attn_mod_k8v4: the same over a K8V4 cache. */
 nvkv_status nvkv_prefill_attn_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,

@@ -25,7 +25,7 @@ cudaError_t launch_decode_qk4_k8v4(const nvkv_cache &, const nvkv_seqs &, const 
                                    float, int, float *, float *, cudaStream_t, const ScoreMod *);
 cudaError_t launch_decode_tc(const nvkv_cache &, const nvkv_seqs &, const void *, int, int, float,
                              int, float *, float *, cudaStream_t, const ScoreMod *);
-bool prefill_tc_supported(const nvkv_cache &);
+bool prefill_tc_supported(const nvkv_cache &, bool mod);
 cudaError_t launch_prefill_tc(const nvkv_cache &, const nvkv_seqs &, const void *, const int32_t *,
                               int, int, int, float, void *, int, float *, float *, cudaStream_t,
                               const ScoreMod *);
@@ -249,12 +249,17 @@ nvkv_status run_prefill_split(const nvkv_cache &c, const nvkv_seqs &s, const voi
                               const int32_t *cu_q, int total_q, int max_q, int Hq, float sm_scale,
                               int num_splits, void *workspace, size_t workspace_bytes, void *out,
                               cudaStream_t stream, const ScoreMod *mod) {
-  if (force_simt() || !prefill_tc_supported(c))
+  if (force_simt() || !prefill_tc_supported(c, mod != nullptr))
     return cuda_status(
         launch_prefill_simt(c, s, q, cu_q, total_q, Hq, sm_scale, out, stream, false, mod));
-  const int S = num_splits > 0 ? num_splits
-                               : prefill_auto_splits(prefill_tc_items(c, s, max_q, Hq),
-                                                     nvkv_default_num_splits());
+  int S = num_splits > 0 ? num_splits
+                         : prefill_auto_splits(prefill_tc_items(c, s, max_q, Hq),
+                                               nvkv_default_num_splits());
+  if (mod && num_splits == 0) {  // as many as the workspace has room for
+    const bool usable = workspace && aligned16(workspace);
+    while (S > 1 && (!usable || workspace_bytes < prefill_layout(total_q, Hq, c.head_dim, S).total))
+      --S;
+  }
   float *ws_o = nullptr, *ws_lse = nullptr;
   if (S > 1) {
     const PrefillLayout w = prefill_layout(total_q, Hq, c.head_dim, S);
@@ -465,7 +470,7 @@ nvkv_status nvkv_prefill_attn(const nvkv_cache *cache, const nvkv_seqs *seqs, co
       check_prefill(cache, seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale, out);
   if (st != NVKV_OK || total_q == 0) return st;
   cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-  if (!force_simt() && prefill_tc_supported(*cache))
+  if (!force_simt() && prefill_tc_supported(*cache, false))
     return cuda_status(launch_prefill_tc(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads,
                                          sm_scale, out, 1, nullptr, nullptr, st_, nullptr));
   return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
@@ -486,7 +491,7 @@ int32_t nvkv_prefill_num_splits(const nvkv_cache *cache, int32_t batch, int32_t 
   if (check_cache(cache) != NVKV_OK || batch <= 0 || max_q < 0 || num_q_heads <= 0 ||
       num_q_heads % cache->num_kv_heads != 0)
     return 0;
-  if (force_simt() || !prefill_tc_supported(*cache)) return 1;
+  if (force_simt() || !prefill_tc_supported(*cache, false)) return 1;
   nvkv_seqs s{};
   s.batch = batch;
   return prefill_auto_splits(prefill_tc_items(*cache, s, max_q, num_q_heads),

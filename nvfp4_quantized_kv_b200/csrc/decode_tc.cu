@@ -928,15 +928,17 @@ bool decode_tc_supported(const nvkv_cache &c, int T, int Hq) {
   return c.head_dim == kD && T >= 1 && G >= 1 && G <= 48 && encode_fn() != nullptr;
 }
 
-// The pool as a 2-D byte tensor of 128-byte rows; one 36-row box is one
-// page's kv-head block (head_dim 256).  Shared with the prefill kernel.
+// The pool as a 2-D byte tensor of 128-byte rows; one box of 18*D/128 rows (36
+// at head_dim 256) is one page's kv-head block.  Shared with the prefill
+// kernel.
 bool make_pool_tmap(const nvkv_cache &c, CUtensorMap *map) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  const cuuint64_t rows = (cuuint64_t)c.num_pages * c.num_kv_heads * kRowsPerHead;
+  const cuuint32_t per_head = (cuuint32_t)head_bytes(c.head_dim) / 128;
+  const cuuint64_t rows = (cuuint64_t)c.num_pages * c.num_kv_heads * per_head;
   const cuuint64_t dims[2] = {128, rows};
   const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, kRowsPerHead};
+  const cuuint32_t box[2] = {128, per_head};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.pool, dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

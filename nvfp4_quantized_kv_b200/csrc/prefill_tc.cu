@@ -1,5 +1,6 @@
 // prefill_tc.cu -- chunked-prefill attention over the NVFP4 paged pool on the
-// 5th-generation tensor cores (tcgen05), head_dim 256.
+// 5th-generation tensor cores (tcgen05): head_dim 256, and 128 with a
+// ScoreMod (the comments' sizes are those of head_dim 256).
 //
 // Computes the chunked prefill of the "knoopx/ninfer" README, "Capabilities
 // and limits": the n_b newest positions of a sequence (their K/V rows already
@@ -36,16 +37,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kD = 256;
-constexpr int kRowsPerHead = 36;
-constexpr int kHeadBytes = 18 * kD;
-constexpr int kPagePitch = 5120;
 constexpr int kTileTokens = 64;
 constexpr int kTilePages = 4;
 constexpr int kStages = 4;
-constexpr int kStageBytes = kTilePages * kPagePitch;   // 20 KB
-constexpr int kKTileBytes = kTileTokens * kD * 2;      // 32 KB
-constexpr int kVTileBytes = kD * kTileTokens * 2;      // 32 KB
 constexpr int kDeqWarps = 8;                           // warps 0..7
 constexpr int kSmxWarp0 = 8;                           // warps 8..11
 constexpr int kSmxWarps = 4;
@@ -65,20 +59,37 @@ constexpr uint32_t kColQ = 0;     // 128: Q (row lanes, d pairs)
 constexpr uint32_t kColS = 128;   // 2 x 64: S slots (P overwrites the first 32 columns)
 constexpr uint32_t kColO = 256;   // 256: O (row lanes, fp32 d)
 
-// Shared memory.
-constexpr int kOffK = kStages * kStageBytes;
-constexpr int kOffV = kOffK + 2 * kKTileBytes;
-constexpr int kVscBytes = kTilePages * 16 * 8 * 4;            // V scales of a tile as f16 pairs
-constexpr int kOffVsc = kOffV + 2 * kVTileBytes;              // 2 tables (tile parity)
-constexpr int kOffPages = kOffVsc + 2 * kVscBytes;            // int[stages][4]
-constexpr int kOffPres = kOffPages + kStages * kTilePages * 4;  // u32[4] (ScoreMod only)
-constexpr int kOffFlags = kOffPres + 16;
-constexpr int kOffBars = kOffFlags + 16;
-constexpr int kNumBars = 2 * kStages + 2 * 5 + 2;  // full, empty; kready, vready, sready, pready, pvdone; qready, final
-constexpr int kOffTmem = kOffBars + kNumBars * 8;
-constexpr int kSmemBytes = kOffTmem + 16 + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-static_assert(kOffK % 1024 == 0 && kOffPages % 16 == 0 && kOffBars % 8 == 0, "alignment");
+// Sizes and shared memory by head_dim.  A page's kv-head block is staged as
+// 128-byte rows with the 128-byte TMA swizzle: byte `off` of the block lies
+// at swz(off).
+template <int D>
+struct Cfg {
+  static_assert(D == 128 || D == 256, "head_dim");
+  static constexpr int kHeadBytes = 18 * D;
+  static constexpr int kRowsPerHead = kHeadBytes / 128;
+  static constexpr int kPagePitch = (kHeadBytes + 1023) / 1024 * 1024;
+  static constexpr int kStageBytes = kTilePages * kPagePitch;       // 20 KB
+  static constexpr int kKTileBytes = kTileTokens * D * 2;           // 32 KB
+  static constexpr int kVTileBytes = D * kTileTokens * 2;           // 32 KB
+  static constexpr int kOffK = kStages * kStageBytes;
+  static constexpr int kOffV = kOffK + 2 * kKTileBytes;
+  // V scales of a tile as f16 pairs [page][group][8], two tables (tile parity)
+  static constexpr int kVscBytes = kTilePages * (D / 16) * 8 * 4;
+  static constexpr int kOffVsc = kOffV + 2 * kVTileBytes;
+  static constexpr int kOffPages = kOffVsc + 2 * kVscBytes;         // int[stages][4]
+  static constexpr int kOffPres = kOffPages + kStages * kTilePages * 4;  // u32[4] (ScoreMod only)
+  static constexpr int kOffFlags = kOffPres + 16;
+  static constexpr int kOffBars = kOffFlags + 16;
+  // full, empty; kready, vready, sready, pready, pvdone; qready, final
+  static constexpr int kNumBars = 2 * kStages + 2 * 5 + 2;
+  static constexpr int kOffTmem = kOffBars + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffTmem + 16 + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(kOffK % 1024 == 0 && kOffPages % 16 == 0 && kOffBars % 8 == 0, "alignment");
+};
+
+// Where the 128-byte TMA swizzle puts byte `off` of a page block.
+__device__ __forceinline__ int swz(int off) { return off ^ ((off >> 3) & 0x70); }
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *flags,
                                          int32_t *err) {
@@ -89,7 +100,7 @@ __device__ __forceinline__ uint32_t dup_scale(uint32_t byte) {
   return e4m3x2_to_f16x2(byte | (byte << 8));
 }
 
-template <class Mod>
+template <int D, class Mod>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hkv,
                   const int32_t *__restrict__ page_table, int max_pages,
@@ -98,6 +109,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
                   int total_q, int Hq, float qscale, __nv_bfloat16 *__restrict__ out,
                   int num_splits, float *__restrict__ ws_o, float *__restrict__ ws_lse,
                   int32_t *err, Mod mod) {
+  using C = Cfg<D>;
+  constexpr int kHeadBytes = C::kHeadBytes, kRowsPerHead = C::kRowsPerHead,
+                kPagePitch = C::kPagePitch, kStageBytes = C::kStageBytes,
+                kKTileBytes = C::kKTileBytes, kVTileBytes = C::kVTileBytes;
   // blockIdx.x = m-tile * num_splits + split: split s of an m-tile takes the
   // s-th of num_splits equal runs of its key tiles and, when num_splits > 1,
   // leaves O / l and log2(l) + m of its rows in the workspace for the merge.
@@ -154,22 +169,22 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
   uint8_t *stages = smem;
-  uint8_t *ktiles = smem + kOffK;
-  uint8_t *vtiles = smem + kOffV;
-  uint32_t *vsc = reinterpret_cast<uint32_t *>(smem + kOffVsc);  // [2][page][group][8]
-  int32_t *spages = reinterpret_cast<int32_t *>(smem + kOffPages);
+  uint8_t *ktiles = smem + C::kOffK;
+  uint8_t *vtiles = smem + C::kOffV;
+  uint32_t *vsc = reinterpret_cast<uint32_t *>(smem + C::kOffVsc);  // [2][page][group][8]
+  int32_t *spages = reinterpret_cast<int32_t *>(smem + C::kOffPages);
   // ScoreMod: bit p of entry (tile & 3) is set when page p of the tile is
   // present, so the softmax leaves the keys of an absent page out.  Written
   // with the tile's K; the K of tile j + 4 is written after the scores of
   // tile j + 2, which wait for the value MMAs of tile j.
-  volatile uint32_t *present = reinterpret_cast<volatile uint32_t *>(smem + kOffPres);
-  volatile int *flags = reinterpret_cast<volatile int *>(smem + kOffFlags);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBars);
+  volatile uint32_t *present = reinterpret_cast<volatile uint32_t *>(smem + C::kOffPres);
+  volatile int *flags = reinterpret_cast<volatile int *>(smem + C::kOffFlags);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBars);
   uint64_t *full = bars, *empty = bars + kStages;
   uint64_t *kready = bars + 2 * kStages, *vready = kready + 2, *sready = kready + 4,
            *pready = kready + 6, *pvdone = kready + 8, *qready = kready + 10,
            *final_bar = kready + 11;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffTmem);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffTmem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (bad && threadIdx.x == 0) report(err, NVKV_DEVERR_LENGTH);
@@ -244,7 +259,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
     // ------------------------------------------------------------------ MMA
     if (lane == 0 && ntiles > 0) {
       const uint32_t idesc_qk = idesc_f16_f32(128, kTileTokens, false, false);
-      const uint32_t idesc_pv = idesc_f16_f32(128, kD, false, false);
+      const uint32_t idesc_pv = idesc_f16_f32(128, D, false, false);
       const uint32_t kb = smem_u32(ktiles), vb = smem_u32(vtiles);
       wait_bar(qready, 0, flags, err);
       tc_fence_after();
@@ -260,7 +275,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
           const uint32_t vt = vb + (pv & 1) * kVTileBytes;
 #pragma unroll
           for (int ks = 0; ks < kTileTokens / 16; ++ks) {
-            const uint64_t bd = smem_desc(vt + ks * 2 * 4096, 4096, 128);
+            const uint64_t bd = smem_desc(vt + ks * 2 * (D * 16), D * 16, 128);
             mma_f16_ts(tmem + kColO, pcol + ks * 8, bd, idesc_pv, (pv > 0 || ks > 0) ? 1u : 0u);
           }
           mma_commit(&pvdone[pv & 1]);
@@ -273,7 +288,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
           const uint32_t kt = kb + (qk & 1) * kKTileBytes;
           const uint32_t scol = tmem + kColS + (qk & 1) * 64;
 #pragma unroll
-          for (int ks = 0; ks < kD / 16; ++ks) {
+          for (int ks = 0; ks < D / 16; ++ks) {
             const uint64_t bd = smem_desc(kt + ks * 2 * 1024, 1024, 128);
             mma_f16_ts(scol, tmem + kColQ + ks * 8, bd, idesc_qk, ks > 0 ? 1u : 0u);
           }
@@ -308,17 +323,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
       const int4 pg4 = *reinterpret_cast<const int4 *>(spages + stage * kTilePages);
       const int pgs[4] = {pg4.x, pg4.y, pg4.z, pg4.w};
       const int tok0 = tile_key(j);
-      {
+      if (D == 256 || t < D) {
         // This tile's V scales, converted once: thread t takes 4 consecutive
         // tokens of one (page, group); the 16 V^T rows of a group share them.
         // (Absent pages convert stale bytes that are never used.)
-        const int p = t >> 6, g = (t >> 2) & 15, q4 = t & 3;
-        const int srow = 34 + (g >> 3);
+        const int p = t / (D / 4), g = (t >> 2) % (D / 16), q4 = t & 3;
         const uint32_t raw = *reinterpret_cast<const uint32_t *>(
-            stg + p * kPagePitch + srow * 128 + (((g & 7) ^ (srow & 7)) << 4) + 4 * q4);
+            stg + p * kPagePitch + swz(vs_off(D) + g * kPageTokens) + 4 * q4);
         uint32_t t2[2];
         e4m3x4_to_f16x2x2(raw, t2);
-        *reinterpret_cast<uint2 *>(vsc + ((slot * kTilePages + p) * 16 + g) * 8 + 2 * q4) =
+        *reinterpret_cast<uint2 *>(vsc + ((slot * kTilePages + p) * (D / 16) + g) * 8 + 2 * q4) =
             make_uint2(t2[0], t2[1]);
       }
       // K tile slot: its previous tile's QK must be done.
@@ -330,23 +344,26 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
         present[j & 3] = (pgs[0] >= 0 ? 1u : 0u) | (pgs[1] >= 0 ? 2u : 0u) |
                          (pgs[2] >= 0 ? 4u : 0u) | (pgs[3] >= 0 ? 8u : 0u);
       {
-        // thread = token n (32 consecutive per warp), two 32-d chunks
+        // thread = token n (32 consecutive per warp), D/128 chunks of 32 d
+        constexpr int kChunks = D / 128;
         const int n = t & 63, cp = t >> 6;
         const int p = n >> 4, s = n & 15;
         const bool ok = pgs[p] >= 0 && tok0 + n <= pos_last && (!Mod::kOn || tok0 + n >= key_lo);
         const uint8_t *pg = stg + p * kPagePitch;
-        uint32_t sc = 0;  // scale bytes of groups 4cp .. 4cp+3
-        if (ok)
-          sc = *reinterpret_cast<const uint32_t *>(pg + (16 + (s >> 3)) * 128 +
-                                                   (((s & 7) ^ (s >> 3)) << 4) + 4 * cp);
+        uint32_t sc = 0;  // scale bytes of the chunks' groups (two a chunk)
+        if (ok) {
+          const uint8_t *sp = pg + swz(ks_off(D) + s * (D / 16) + 2 * kChunks * cp);
+          sc = kChunks == 2 ? *reinterpret_cast<const uint32_t *>(sp)
+                            : *reinterpret_cast<const uint16_t *>(sp);
+        }
         uint8_t *kt = ktiles + slot * kKTileBytes + (n >> 3) * 128 + (n & 7) * 16;
 #pragma unroll
-        for (int ci = 0; ci < 2; ++ci) {
-          const int c = 2 * cp + ci;  // 32-d chunk: groups 2c, 2c+1
+        for (int ci = 0; ci < kChunks; ++ci) {
+          const int c = kChunks * cp + ci;  // 32-d chunk: groups 2c, 2c+1
           uint32_t words[16];
           if (ok) {
             const uint4 w4 =
-                *reinterpret_cast<const uint4 *>(pg + s * 128 + ((c ^ (s & 7)) << 4));
+                *reinterpret_cast<const uint4 *>(pg + swz(s * (D / 2) + c * 16));
             const uint32_t s0 = dup_scale((sc >> (16 * ci)) & 0xffu);
             const uint32_t s1 = dup_scale((sc >> (16 * ci + 8)) & 0xffu);
             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -381,21 +398,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
         tc_fence_after();
       }
       {
-        const int d = t;  // head_dim row
+        // thread = head_dim row d, D/64 of the tile's pages
+        constexpr int kPages = D / 64;
+        const int d = t % D;
         const int g = d >> 4;
-        const int vrow = 18 + (d >> 4);
-        const int vchunk = ((d & 15) >> 1) ^ (vrow & 7);
         uint8_t *vt = vtiles + slot * kVTileBytes + (d >> 3) * 128 + (d & 7) * 16;
 #pragma unroll
-        for (int p = 0; p < kTilePages; ++p) {
+        for (int pp = 0; pp < kPages; ++pp) {
+          const int p = (D == 256 ? 0 : t / D * kPages) + pp;
           const int ptok = tok0 + p * kPageTokens;
           uint32_t o8[8];
-          if (pgs[p] >= 0) {
+          if ((D == 256 ? pgs[pp] : t < D ? pgs[pp] : pgs[(pp + kPages) & 3]) >= 0) {
             const uint8_t *pg = stg + p * kPagePitch;
-            const uint2 cw =
-                *reinterpret_cast<const uint2 *>(pg + vrow * 128 + vchunk * 16 + (d & 1) * 8);
-            const uint4 *tb =
-                reinterpret_cast<const uint4 *>(vsc + ((slot * kTilePages + p) * 16 + g) * 8);
+            const uint2 cw = *reinterpret_cast<const uint2 *>(pg + swz(vc_off(D) + d * 8));
+            const uint4 *tb = reinterpret_cast<const uint4 *>(
+                vsc + ((slot * kTilePages + p) * (D / 16) + g) * 8);
             const uint4 sa = tb[0], sb = tb[1];
             const uint32_t sp[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
             uint32_t c0[4], c1[4];
@@ -423,9 +440,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
 #pragma unroll
             for (int i = 0; i < 8; ++i) o8[i] = 0u;
           }
-          // K-major (tokens) core matrices: element (d, t) at (t/8)*4096 + (d/8)*128 + (d%8)*16.
-          *reinterpret_cast<uint4 *>(vt + (2 * p) * 4096) = make_uint4(o8[0], o8[1], o8[2], o8[3]);
-          *reinterpret_cast<uint4 *>(vt + (2 * p + 1) * 4096) =
+          // K-major (tokens) core matrices: element (d, t) at (t/8)*16*D + (d/8)*128 + (d%8)*16.
+          *reinterpret_cast<uint4 *>(vt + (2 * p) * (16 * D)) =
+              make_uint4(o8[0], o8[1], o8[2], o8[3]);
+          *reinterpret_cast<uint4 *>(vt + (2 * p + 1) * (16 * D)) =
               make_uint4(o8[4], o8[5], o8[6], o8[7]);
         }
       }
@@ -455,9 +473,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
     }
     // Q row -> Tensor Memory (A operand), f16, pre-scaled to base-2 scores.
     {
-      const __nv_bfloat16 *qr = q + ((size_t)(q0 + i) * Hq + h * G + g) * kD;
+      const __nv_bfloat16 *qr = q + ((size_t)(q0 + i) * Hq + h * G + g) * D;
 #pragma unroll
-      for (int c32 = 0; c32 < 4; ++c32) {
+      for (int c32 = 0; c32 < D / 64; ++c32) {
         uint32_t w[32];
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
@@ -549,7 +567,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
         __syncwarp();
         tc_fence_after();
 #pragma unroll 1
-        for (int c16 = 0; c16 < kD / 16; ++c16) {
+        for (int c16 = 0; c16 < D / 16; ++c16) {
           uint32_t rr[16];
           tmem_ld16(tl + kColO + c16 * 16, rr);
           tmem_wait_ld();
@@ -598,7 +616,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
     const size_t plane = (size_t)split * total_q * Hq;
     if (ws_o && write) ws_lse[plane + orow_idx] = l > 0.f ? m + log2f(l) : -INFINITY;
 #pragma unroll 1
-    for (int c16 = 0; c16 < kD / 16; ++c16) {
+    for (int c16 = 0; c16 < D / 16; ++c16) {
       uint32_t rr[16];
       if (ntiles > 0) {
         tmem_ld16(tl + kColO + c16 * 16, rr);
@@ -609,7 +627,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
       }
       if (!write) continue;
       if (ws_o) {
-        float4 *dst = reinterpret_cast<float4 *>(ws_o + (plane + orow_idx) * kD + c16 * 16);
+        float4 *dst = reinterpret_cast<float4 *>(ws_o + (plane + orow_idx) * D + c16 * 16);
 #pragma unroll
         for (int e4 = 0; e4 < 4; ++e4)
           dst[e4] = make_float4(__uint_as_float(rr[4 * e4]) * inv, __uint_as_float(rr[4 * e4 + 1]) * inv,
@@ -623,7 +641,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
                                                     __uint_as_float(rr[2 * e + 1]) * inv);
           ow[e] = *reinterpret_cast<uint32_t *>(&b2);
         }
-        __nv_bfloat16 *orow = out + orow_idx * kD;
+        __nv_bfloat16 *orow = out + orow_idx * D;
         *reinterpret_cast<uint4 *>(orow + c16 * 16) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
         *reinterpret_cast<uint4 *>(orow + c16 * 16 + 8) = make_uint4(ow[4], ow[5], ow[6], ow[7]);
       }
@@ -639,10 +657,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
 // Merge of the key splits: row (token q0 + i, head hq) of sequence b is
 // sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M) with M the largest lse (the
 // log-sum-exp combination of partial softmax results; zero when no split saw
-// a key).  One warp per row, 8 head_dim elements per lane.
+// a key).  One warp per row, D/32 head_dim elements per lane.
 constexpr int kMaxSplits = 8;
 constexpr int kMergeWarps = 8;
 
+template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 prefill_merge_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_lse,
                      int num_splits, const int32_t *__restrict__ cu_q, int total_q, int Hq,
@@ -663,33 +682,46 @@ prefill_merge_kernel(const float *__restrict__ ws_o, const float *__restrict__ w
     lse[s] = s < num_splits ? ws_lse[s * plane + row] : -INFINITY;
     mx = fmaxf(mx, lse[s]);
   }
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, wsum = 0.f;
+  constexpr int kE = D / 32;  // elements of a lane: 4 or 8
+  float acc[kE], wsum = 0.f;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
   if (mx > -INFINITY) {
 #pragma unroll
     for (int s = 0; s < kMaxSplits; ++s) {
       if (s < num_splits && lse[s] > -INFINITY) {
         const float w = exp2f(lse[s] - mx);
-        const float4 *src = reinterpret_cast<const float4 *>(ws_o + (s * plane + row) * kD + 8 * lane);
-        const float4 a = src[0], c = src[1];
-        acc[0] += w * a.x; acc[1] += w * a.y; acc[2] += w * a.z; acc[3] += w * a.w;
-        acc[4] += w * c.x; acc[5] += w * c.y; acc[6] += w * c.z; acc[7] += w * c.w;
+        const float4 *src = reinterpret_cast<const float4 *>(ws_o + (s * plane + row) * D + kE * lane);
+#pragma unroll
+        for (int i = 0; i < kE / 4; ++i) {
+          const float4 a = src[i];
+          acc[4 * i] += w * a.x; acc[4 * i + 1] += w * a.y;
+          acc[4 * i + 2] += w * a.z; acc[4 * i + 3] += w * a.w;
+        }
         wsum += w;
       }
     }
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  uint32_t ow[4];
+  uint32_t ow[kE / 2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < kE / 2; ++e) {
     __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     ow[e] = *reinterpret_cast<uint32_t *>(&b2);
   }
-  *reinterpret_cast<uint4 *>(out + row * kD + 8 * lane) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+  __nv_bfloat16 *dst = out + row * D + kE * lane;
+  if constexpr (kE == 8)
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+  else
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(ow[0], ow[1]);
 }
 
 }  // namespace
 
-bool prefill_tc_supported(const nvkv_cache &c) { return c.head_dim == kD; }
+// The plain prefill of head_dim 128 stays on the CUDA-core kernel.
+bool prefill_tc_supported(const nvkv_cache &c, bool mod) {
+  return c.head_dim == 256 || (mod && c.head_dim == 128);
+}
 
 int prefill_max_splits() { return kMaxSplits; }
 
@@ -716,7 +748,7 @@ int prefill_tc_items(const nvkv_cache &c, const nvkv_seqs &s, int max_q, int Hq)
   return (int)(((int64_t)max_q * G + 127) / 128) * c.num_kv_heads * s.batch;
 }
 
-template <class Mod>
+template <int D, class Mod>
 static cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
                                       const int32_t *cu_q, int total_q, int max_q, int Hq,
                                       float sm_scale, void *out, int num_splits, float *ws_o,
@@ -727,11 +759,12 @@ static cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, c
     return cudaErrorInvalidValue;
   const int G = Hq / c.num_kv_heads;
   const int mtiles = (max_q * G + 127) / 128;
-  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<Mod>,
+  constexpr int kSmemBytes = Cfg<D>::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<D, Mod>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)(mtiles * num_splits), (unsigned)c.num_kv_heads, (unsigned)s.batch);
-  prefill_tc_kernel<Mod><<<grid, kThreads, kSmemBytes, stream>>>(
+  prefill_tc_kernel<D, Mod><<<grid, kThreads, kSmemBytes, stream>>>(
       map, c.num_pages, c.num_kv_heads, s.page_table, s.max_pages_per_seq, s.kv_lens,
       s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), cu_q, total_q, Hq,
       sm_scale * 1.4426950408889634f, static_cast<__nv_bfloat16 *>(out), num_splits,
@@ -739,7 +772,7 @@ static cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, c
   if ((e = cudaGetLastError()) != cudaSuccess || num_splits == 1) return e;
   const dim3 mgrid((unsigned)(((int64_t)max_q * Hq + kMergeWarps - 1) / kMergeWarps),
                    (unsigned)s.batch);
-  prefill_merge_kernel<<<mgrid, kMergeWarps * 32, 0, stream>>>(
+  prefill_merge_kernel<D><<<mgrid, kMergeWarps * 32, 0, stream>>>(
       ws_o, ws_lse, num_splits, cu_q, total_q, Hq, G, 128 * mtiles,
       static_cast<__nv_bfloat16 *>(out));
   return cudaGetLastError();
@@ -750,10 +783,16 @@ cudaError_t launch_prefill_tc(const nvkv_cache &c, const nvkv_seqs &s, const voi
                               const int32_t *cu_q, int total_q, int max_q, int Hq,
                               float sm_scale, void *out, int num_splits, float *ws_o,
                               float *ws_lse, cudaStream_t stream, const ScoreMod *mod) {
-  return mod ? launch_prefill_mod(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out, num_splits,
-                                  ws_o, ws_lse, stream, *mod)
-             : launch_prefill_mod(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out, num_splits,
-                                  ws_o, ws_lse, stream, NoMod{});
+  if (!mod)
+    return c.head_dim == 256
+               ? launch_prefill_mod<256>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
+                                         num_splits, ws_o, ws_lse, stream, NoMod{})
+               : cudaErrorNotSupported;
+  return c.head_dim == 256
+             ? launch_prefill_mod<256>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
+                                       num_splits, ws_o, ws_lse, stream, *mod)
+             : launch_prefill_mod<128>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
+                                       num_splits, ws_o, ws_lse, stream, *mod);
 }
 
 }  // namespace nvkv
