@@ -438,25 +438,44 @@ def nvkv_prefill_attn_k8v4(cache: Cache, seqs: Seqs, q: torch.Tensor, cu_q: torc
 # ---- masked attention, several-axis rotary append, reading rows back -------
 # These calls also check that their tensors are on one device and as large as
 # the call makes them, and run on that device whatever the current one is.
+# A serving step makes a few of them per layer, each shorter than ten
+# microseconds on the GPU, so the checks are kept to one test a tensor.
 
-def _same_device(device: torch.device, *named) -> None:
-    for t, name in named:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+def _arg(t: torch.Tensor, dtype: torch.dtype, device: int, n: int, name: str) -> int:
+    """Address of a tensor argument: contiguous, of the dtype, on the device
+    and of at least n elements."""
+    try:
+        if (t.dtype is dtype and t.get_device() == device and t.numel() >= n
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name)  # raises for a wrong type, dtype, place or layout
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device}")
+    raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
 
 
-def _at_least(t: torch.Tensor, n: int, name: str) -> None:
-    if t.numel() < n:
-        raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
+def _on(cache: Cache, seqs: Seqs) -> int:
+    """The device index of a call's cache and sequences."""
+    device = cache.pool.get_device()
+    for t, name in ((seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens")):
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {cache.pool.device}")
+    return device
 
 
-def _call(device: torch.device, fn, what: str, stream, *args) -> None:
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, _stream(stream))
+def _call(device: int, fn, what: str, stream, *args) -> None:
+    if device == torch._C._cuda_getDevice():
+        if stream is None:
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+        else:
+            status = fn(*args, _stream(stream))
     else:
         with torch.cuda.device(device):
             status = fn(*args, _stream(stream))
-    _check(status, what)
+    if status != OK:
+        raise NvkvError(status, what)
 
 
 class ScoreMod:
@@ -479,14 +498,14 @@ class ScoreMod:
             _dev(prefix_lens, torch.int32, "prefix_lens") if prefix_lens is not None else None,
             _dev(key_starts, torch.int32, "key_starts") if key_starts is not None else None)
 
-    def _check(self, device: torch.device, num_q_heads: int, batch: int, starts: int) -> None:
-        for t, n, name in ((self.alibi_slopes, num_q_heads, "alibi_slopes"),
-                           (self.prefix_lens, batch, "prefix_lens"),
-                           (self.key_starts, starts, "key_starts")):
-            if t is not None:
-                if t.device != device:
-                    raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-                _at_least(t, n, name)
+    def _ref(self, device: int, num_q_heads: int, batch: int, starts: int):
+        if self.alibi_slopes is not None:
+            _arg(self.alibi_slopes, torch.float32, device, num_q_heads, "alibi_slopes")
+        if self.prefix_lens is not None:
+            _arg(self.prefix_lens, torch.int32, device, batch, "prefix_lens")
+        if self.key_starts is not None:
+            _arg(self.key_starts, torch.int32, device, starts, "key_starts")
+        return ctypes.byref(self._c)
 
 
 def nvkv_decode_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, T: int, num_q_heads: int,
@@ -495,19 +514,14 @@ def nvkv_decode_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, T: int, num_
     """Decode attention of T queries per sequence with the scores and masks of
     mod, merged into out (bf16 [batch*T][Hq][D]); workspace as for
     nvkv_decode_attn.  For caches of either format."""
-    device = cache.pool.device
-    _same_device(device, (seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens"), (q, "q"),
-                 (workspace, "workspace"), (out, "out"))
-    mod._check(device, num_q_heads, seqs.batch, seqs.batch)
+    device, L = _on(cache, seqs), library()
     n = seqs.batch * T * num_q_heads * cache.head_dim
-    _at_least(q, n, "q")
-    _at_least(out, n, "out")
-    L = library()
-    _call(device, L.nvkv_decode_attn_mod_k8v4 if cache.kv_format == "k8v4" else L.nvkv_decode_attn_mod,
-          "nvkv_decode_attn_mod", stream, ctypes.byref(cache._c), ctypes.byref(seqs._c),
-          _dev(q, torch.bfloat16, "q"), int(T), int(num_q_heads), float(sm_scale),
-          ctypes.byref(mod._c), int(num_splits), _dev(workspace, torch.uint8, "workspace"),
-          workspace.numel(), _dev(out, torch.bfloat16, "out"))
+    fn = L.nvkv_decode_attn_mod_k8v4 if cache.kv_format == "k8v4" else L.nvkv_decode_attn_mod
+    _call(device, fn, "nvkv_decode_attn_mod", stream, ctypes.byref(cache._c),
+          ctypes.byref(seqs._c), _arg(q, torch.bfloat16, device, n, "q"), T, num_q_heads, sm_scale,
+          mod._ref(device, num_q_heads, seqs.batch, seqs.batch), num_splits,
+          _arg(workspace, torch.uint8, device, 0, "workspace"), workspace.numel(),
+          _arg(out, torch.bfloat16, device, n, "out"))
 
 
 def nvkv_prefill_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, cu_q: torch.Tensor,
@@ -515,23 +529,20 @@ def nvkv_prefill_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, cu_q: torch
                           mod: ScoreMod, num_splits: int, workspace: "torch.Tensor | None",
                           out: torch.Tensor, stream=None) -> None:
     """Chunked prefill with the scores and masks of mod; num_splits and
-    workspace as for nvkv_prefill_attn_split.  For caches of either format."""
-    device = cache.pool.device
-    _same_device(device, (seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens"), (q, "q"),
-                 (cu_q, "cu_q"), (workspace, "workspace"), (out, "out"))
-    mod._check(device, num_q_heads, seqs.batch, total_q)
+    workspace as for nvkv_prefill_attn_split (0 splits: as many of the
+    automatic count as the workspace has room for).  For caches of either
+    format."""
+    device, L = _on(cache, seqs), library()
     n = total_q * num_q_heads * cache.head_dim
-    _at_least(q, n, "q")
-    _at_least(out, n, "out")
-    _at_least(cu_q, seqs.batch + 1, "cu_q")
-    ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
-    L = library()
-    _call(device,
-          L.nvkv_prefill_attn_mod_k8v4 if cache.kv_format == "k8v4" else L.nvkv_prefill_attn_mod,
-          "nvkv_prefill_attn_mod", stream, ctypes.byref(cache._c), ctypes.byref(seqs._c),
-          _dev(q, torch.bfloat16, "q"), _dev(cu_q, torch.int32, "cu_q"), int(total_q), int(max_q),
-          int(num_q_heads), float(sm_scale), ctypes.byref(mod._c), int(num_splits), ws,
-          workspace.numel() if workspace is not None else 0, _dev(out, torch.bfloat16, "out"))
+    fn = L.nvkv_prefill_attn_mod_k8v4 if cache.kv_format == "k8v4" else L.nvkv_prefill_attn_mod
+    ws, size = None, 0
+    if workspace is not None:
+        ws, size = _arg(workspace, torch.uint8, device, 0, "workspace"), workspace.numel()
+    _call(device, fn, "nvkv_prefill_attn_mod", stream, ctypes.byref(cache._c),
+          ctypes.byref(seqs._c), _arg(q, torch.bfloat16, device, n, "q"),
+          _arg(cu_q, torch.int32, device, seqs.batch + 1, "cu_q"), total_q, max_q, num_q_heads,
+          sm_scale, mod._ref(device, num_q_heads, seqs.batch, total_q), num_splits, ws, size,
+          _arg(out, torch.bfloat16, device, n, "out"))
 
 
 def nvkv_append_rope_axes(cache: Cache, seqs: Seqs, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -541,40 +552,35 @@ def nvkv_append_rope_axes(cache: Cache, seqs: Seqs, k_new: torch.Tensor, v_new: 
                           q_out: torch.Tensor | None = None, stream=None) -> None:
     """nvkv_append_rope with the positions of every row on several axes:
     positions int32 [num_axes][total_new], axis_of_pair the axis (a whole
-    number) of each of the rotary_dim/2 pairs.  q (bf16 [total_new][Hq][D]) is
-    rotated into q_out in the same launch."""
+    number) of each of the rotary_dim/2 pairs, as bytes or a sequence.  q
+    (bf16 [total_new][Hq][D]) is rotated into q_out in the same launch."""
     _fmt(cache, "nvfp4", "nvkv_append_rope_axes")
-    device = cache.pool.device
-    _same_device(device, (seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens"),
-                 (k_new, "k_new"), (v_new, "v_new"), (cu_new, "cu_new"), (rope_cs, "rope_cs"),
-                 (positions, "positions"), (q, "q"), (q_out, "q_out"))
+    device = _on(cache, seqs)
     if positions.dim() != 2 or positions.shape[1] != total_new:
         raise ValueError("positions must be [num_axes][total_new]")
     if rope_cs.dim() != 3 or rope_cs.shape[1] * 2 != rotary_dim or rope_cs.shape[2] != 2:
         raise ValueError("rope_cs must be [max_pos][rotary_dim/2][2]")
     if len(axis_of_pair) * 2 != rotary_dim:
         raise ValueError("axis_of_pair must have rotary_dim/2 entries")
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
     n = total_new * cache.num_kv_heads * cache.head_dim
-    _at_least(k_new, n, "k_new")
-    _at_least(v_new, n, "v_new")
-    _at_least(cu_new, seqs.batch + 1, "cu_new")
-    hq = 0
-    if q is not None:
+    hq, qp, qo = 0, None, None
+    if q is not None and q_out is not None:
         if q.dim() != 3 or q.shape[0] != total_new or q.shape[2] != cache.head_dim:
             raise ValueError("q must be [total_new][Hq][D]")
         if q_out.shape != q.shape:
             raise ValueError("q_out must have the shape of q")
         hq = q.shape[1]
+        qp, qo = _arg(q, torch.bfloat16, device, 0, "q"), _arg(q_out, torch.bfloat16, device, 0, "q_out")
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out go together")
     _call(device, library().nvkv_append_rope_axes, "nvkv_append_rope_axes", stream,
-          ctypes.byref(cache._c), ctypes.byref(seqs._c), _dev(k_new, torch.bfloat16, "k_new"),
-          _dev(v_new, torch.bfloat16, "v_new"), _dev(cu_new, torch.int32, "cu_new"),
-          int(total_new), int(max_new), _dev(rope_cs, torch.float32, "rope_cs"),
-          int(rope_cs.shape[0]), int(rotary_dim), _dev(positions, torch.int32, "positions"),
-          int(positions.shape[0]), bytes(axis_of_pair),
-          _dev(q, torch.bfloat16, "q") if q is not None else None, int(hq),
-          _dev(q_out, torch.bfloat16, "q_out") if q_out is not None else None)
+          ctypes.byref(cache._c), ctypes.byref(seqs._c),
+          _arg(k_new, torch.bfloat16, device, n, "k_new"),
+          _arg(v_new, torch.bfloat16, device, n, "v_new"),
+          _arg(cu_new, torch.int32, device, seqs.batch + 1, "cu_new"), total_new, max_new,
+          _arg(rope_cs, torch.float32, device, 0, "rope_cs"), rope_cs.shape[0], rotary_dim,
+          _arg(positions, torch.int32, device, 0, "positions"), positions.shape[0],
+          bytes(axis_of_pair), qp, hq, qo)
 
 
 def nvkv_read_rows(cache: Cache, seqs: Seqs, starts: torch.Tensor, cu_rows: torch.Tensor,
@@ -583,17 +589,11 @@ def nvkv_read_rows(cache: Cache, seqs: Seqs, starts: torch.Tensor, cu_rows: torc
     """The cached K and V rows of positions starts[b] .. of every sequence as
     bf16, rows cu_rows[b] .. cu_rows[b+1]-1 of k_out and v_out
     ([total_rows][Hkv][D]).  For caches of either format."""
-    device = cache.pool.device
-    _same_device(device, (seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens"),
-                 (starts, "starts"), (cu_rows, "cu_rows"), (k_out, "k_out"), (v_out, "v_out"))
+    device, L = _on(cache, seqs), library()
     n = total_rows * cache.num_kv_heads * cache.head_dim
-    _at_least(k_out, n, "k_out")
-    _at_least(v_out, n, "v_out")
-    _at_least(starts, seqs.batch, "starts")
-    _at_least(cu_rows, seqs.batch + 1, "cu_rows")
-    L = library()
     _call(device, L.nvkv_read_rows_k8v4 if cache.kv_format == "k8v4" else L.nvkv_read_rows,
           "nvkv_read_rows", stream, ctypes.byref(cache._c), ctypes.byref(seqs._c),
-          _dev(starts, torch.int32, "starts"), _dev(cu_rows, torch.int32, "cu_rows"),
-          int(total_rows), int(max_rows), _dev(k_out, torch.bfloat16, "k_out"),
-          _dev(v_out, torch.bfloat16, "v_out"))
+          _arg(starts, torch.int32, device, seqs.batch, "starts"),
+          _arg(cu_rows, torch.int32, device, seqs.batch + 1, "cu_rows"), total_rows, max_rows,
+          _arg(k_out, torch.bfloat16, device, n, "k_out"),
+          _arg(v_out, torch.bfloat16, device, n, "v_out"))
