@@ -429,7 +429,15 @@ typedef struct nvkv_score_mod {
  * or a document start bounds what is read.  softcap, window and the pointers
  * are read when the call is made; the arrays by the kernels.
  *
- * nvkv_decode_attn_mod_k8v4: the same over a K8V4 cache. */
+ * The kernels and their arithmetic are those of nvkv_decode_attn, except that
+ * an NVFP4 cache of head_dim 128 also runs on decode_qk4 (its query rows in
+ * chunks of at most 6, each reading the keys once).
+ * nvkv_decode_mod_kernel_name names the kernel ("decode_qk4", "decode_tc",
+ * "decode_simt", or "none" on invalid arguments).
+ *
+ * nvkv_decode_attn_mod_k8v4: the same over a K8V4 cache, on the kernels of
+ * nvkv_decode_attn_k8v4 (nvkv_decode_kernel_name_k8v4). */
+const char *nvkv_decode_mod_kernel_name(const nvkv_cache *cache, int32_t T, int32_t num_q_heads);
 nvkv_status nvkv_decode_attn_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
                                  int32_t T, int32_t num_q_heads, float sm_scale,
                                  const nvkv_score_mod *mod, int32_t num_splits, void *workspace,

@@ -26,7 +26,8 @@ __all__ = [
     "nvkv_pages_spill", "nvkv_pages_restore", "nvkv_k8v4_page_bytes", "nvkv_append_k8v4",
     "nvkv_decode_attn_k8v4", "nvkv_prefill_attn_k8v4", "nvkv_pages_spill_k8v4",
     "nvkv_pages_restore_k8v4", "nvkv_prefill_attn_split", "nvkv_prefill_workspace_bytes",
-    "nvkv_prefill_num_splits", "ScoreMod", "nvkv_decode_attn_mod", "nvkv_prefill_attn_mod",
+    "nvkv_prefill_num_splits", "ScoreMod", "nvkv_decode_attn_mod",
+    "nvkv_decode_mod_kernel_name", "nvkv_prefill_attn_mod",
     "nvkv_append_rope_axes", "nvkv_read_rows",
 ]
 
@@ -106,6 +107,7 @@ def library():
             "nvkv_append_k8v4": (ctypes.c_int, [cp, sp, vp, vp, vp, i32, i32, vp]),
             "nvkv_decode_attn_k8v4": (ctypes.c_int, [cp, sp, vp, i32, i32, f32, i32, vp, sz, vp]),
             "nvkv_prefill_attn_k8v4": (ctypes.c_int, [cp, sp, vp, vp, i32, i32, i32, f32, vp, vp]),
+            "nvkv_decode_mod_kernel_name": (ctypes.c_char_p, [cp, i32, i32]),
             "nvkv_decode_attn_mod": (ctypes.c_int, decode_mod),
             "nvkv_decode_attn_mod_k8v4": (ctypes.c_int, decode_mod),
             "nvkv_prefill_attn_mod": (ctypes.c_int, prefill_mod),
@@ -506,6 +508,15 @@ class ScoreMod:
         if self.key_starts is not None:
             _arg(self.key_starts, torch.int32, device, starts, "key_starts")
         return ctypes.byref(self._c)
+
+
+def nvkv_decode_mod_kernel_name(cache: Cache, T: int, num_q_heads: int) -> str:
+    """The kernel that nvkv_decode_attn_mod launches for this cache and step
+    shape: one of the names of nvkv_decode_kernel_name."""
+    if cache.kv_format == "k8v4":
+        return nvkv_decode_kernel_name(cache, T, num_q_heads)
+    return library().nvkv_decode_mod_kernel_name(ctypes.byref(cache._c), int(T),
+                                                 int(num_q_heads)).decode()
 
 
 def nvkv_decode_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, T: int, num_q_heads: int,

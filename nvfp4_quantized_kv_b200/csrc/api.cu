@@ -18,7 +18,7 @@ cudaError_t launch_decode_simt(const nvkv_cache &, const nvkv_seqs &, const void
                                float, int, float *, float *, cudaStream_t, bool,
                                const ScoreMod *);
 bool decode_tc_supported(const nvkv_cache &, int, int);
-bool decode_qk4_supported(const nvkv_cache &, int, int);
+bool decode_qk4_supported(const nvkv_cache &, int, int, bool mod);
 cudaError_t launch_decode_qk4(const nvkv_cache &, const nvkv_seqs &, const void *, int, int, float,
                               int, float *, float *, cudaStream_t, const ScoreMod *);
 cudaError_t launch_decode_qk4_k8v4(const nvkv_cache &, const nvkv_seqs &, const void *, int, int,
@@ -33,7 +33,9 @@ int prefill_max_splits();
 int prefill_auto_splits(int64_t, int);
 int prefill_tc_items(const nvkv_cache &, const nvkv_seqs &, int, int);
 cudaError_t launch_combine(const nvkv_seqs &, const void *, const void *, int, int, int, int, int,
-                           void *, cudaStream_t, const ScoreMod *);
+                           void *, cudaStream_t);
+cudaError_t launch_combine_mod(const nvkv_seqs &, const float *, const float *, int, int, int, int,
+                               int, void *, cudaStream_t, const ScoreMod &);
 cudaError_t launch_prefill_simt(const nvkv_cache &, const nvkv_seqs &, const void *,
                                 const int32_t *, int, int, float, void *, cudaStream_t, bool,
                                 const ScoreMod *);
@@ -227,7 +229,7 @@ bool force_simt() { return force_kernel("simt"); }
 cudaError_t run_decode(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T, int Hq,
                        float sm_scale, const DecodeArgs &a, cudaStream_t stream,
                        const ScoreMod *mod) {
-  if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(c, T, Hq))
+  if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(c, T, Hq, mod != nullptr))
     return launch_decode_qk4(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, mod);
   if (!force_simt() && decode_tc_supported(c, T, Hq))
     return launch_decode_tc(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, mod);
@@ -238,7 +240,7 @@ cudaError_t run_decode(const nvkv_cache &c, const nvkv_seqs &s, const void *q, i
 cudaError_t run_decode_k8v4(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T, int Hq,
                             float sm_scale, const DecodeArgs &a, cudaStream_t stream,
                             const ScoreMod *mod) {
-  if (!force_simt() && decode_qk4_supported(c, T, Hq))
+  if (!force_simt() && decode_qk4_supported(c, T, Hq, false))
     return launch_decode_qk4_k8v4(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, mod);
   return launch_decode_simt(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, true, mod);
 }
@@ -288,8 +290,8 @@ nvkv_status decode_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const voi
       k8 ? run_decode_k8v4(*cache, *seqs, q, T, num_q_heads, sm_scale, a, s, &m)
          : run_decode(*cache, *seqs, q, T, num_q_heads, sm_scale, a, s, &m);
   if (e != cudaSuccess) return cuda_status(e);
-  return cuda_status(launch_combine(*seqs, a.ws_o, a.ws_lse, T, num_q_heads, cache->num_kv_heads,
-                                    cache->head_dim, a.S, out, s, &m));
+  return cuda_status(launch_combine_mod(*seqs, a.ws_o, a.ws_lse, T, num_q_heads,
+                                        cache->num_kv_heads, cache->head_dim, a.S, out, s, m));
 }
 
 nvkv_status prefill_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
@@ -430,7 +432,7 @@ const char *nvkv_decode_kernel_name(const nvkv_cache *cache, int32_t T, int32_t 
   if (!cache || cache->num_kv_heads <= 0 || T <= 0 || num_q_heads <= 0 ||
       num_q_heads % cache->num_kv_heads != 0)
     return "none";
-  if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(*cache, T, num_q_heads))
+  if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(*cache, T, num_q_heads, false))
     return "decode_qk4";
   if (!force_simt() && decode_tc_supported(*cache, T, num_q_heads)) return "decode_tc";
   return "decode_simt";
@@ -459,7 +461,7 @@ nvkv_status nvkv_combine(const nvkv_seqs *seqs, const void *workspace, int32_t T
   const WorkspaceLayout w = layout(seqs->batch, T, num_q_heads, num_kv_heads, head_dim, S);
   const void *ws_lse = static_cast<const char *>(workspace) + w.lse_off;
   return cuda_status(launch_combine(*seqs, workspace, ws_lse, T, num_q_heads, num_kv_heads,
-                                    head_dim, S, out, reinterpret_cast<cudaStream_t>(stream), nullptr));
+                                    head_dim, S, out, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 nvkv_status nvkv_prefill_attn(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
@@ -550,7 +552,7 @@ const char *nvkv_decode_kernel_name_k8v4(const nvkv_cache *cache, int32_t T,
   if (!cache || cache->num_kv_heads <= 0 || T <= 0 || num_q_heads <= 0 ||
       num_q_heads % cache->num_kv_heads != 0)
     return "none";
-  if (!force_simt() && decode_qk4_supported(*cache, T, num_q_heads)) return "decode_qk4_k8v4";
+  if (!force_simt() && decode_qk4_supported(*cache, T, num_q_heads, false)) return "decode_qk4_k8v4";
   return "decode_simt";
 }
 
@@ -563,6 +565,16 @@ nvkv_status nvkv_prefill_attn_k8v4(const nvkv_cache *cache, const nvkv_seqs *seq
   if (st != NVKV_OK || total_q == 0) return st;
   return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
                                          out, reinterpret_cast<cudaStream_t>(stream), true, nullptr));
+}
+
+const char *nvkv_decode_mod_kernel_name(const nvkv_cache *cache, int32_t T, int32_t num_q_heads) {
+  if (!cache || cache->num_kv_heads <= 0 || T <= 0 || num_q_heads <= 0 ||
+      num_q_heads % cache->num_kv_heads != 0)
+    return "none";
+  if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(*cache, T, num_q_heads, true))
+    return "decode_qk4";
+  if (!force_simt() && decode_tc_supported(*cache, T, num_q_heads)) return "decode_tc";
+  return "decode_simt";
 }
 
 nvkv_status nvkv_decode_attn_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,

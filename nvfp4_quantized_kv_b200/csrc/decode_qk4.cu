@@ -80,21 +80,17 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kD = 256;
-constexpr int kRowsPerHead = 36;         // 18*D bytes / 128
 constexpr int kUnitPages = 8;
-constexpr int kKRows = 16;               // K-code rows of a page block (one per token)
-constexpr int kKsRows = 2;               // K scales: 16 tokens x 16 groups
-constexpr int kVRows = 18;               // V codes (16), V scales (2)
-constexpr int kKPageBytes = kKRows * 128;         // 2048
-constexpr int kVPageBytes = kVRows * 128;         // 2304
-constexpr int kKsPageBytes = kKsRows * 128;       // 256
-constexpr int kVc = 0, kVs = 2048;       // V codes, V scales inside a page's V block
-constexpr int kKsSlotBytes = kUnitPages * kKsPageBytes;    // 2048
+// An NVFP4 page block of one kv-head is 36 rows of D/2 bytes: K codes (one
+// row a token), K scales, V codes, V scales.
+constexpr int kRowsPerHead = 36;
+constexpr int kKRows = 16;
+constexpr int kKsRows = 2;
+constexpr int kVRows = 18;
 // K8V4 page block of one kv-head (head_dim 256): K codes [16][256] (4096 B),
 // K row scales [16] fp32 (64 B), then the V codes and scales as above.
-constexpr int kK8HeadBytes = 25 * kD + 64;   // 6464
-constexpr int kK8KsOff = 16 * kD;            // 4096
+constexpr int kK8HeadBytes = 25 * 256 + 64;  // 6464
+constexpr int kK8KsOff = 16 * 256;           // 4096
 constexpr int kK8VOff = kK8KsOff + 64;       // 4160
 
 constexpr int kRowsCap = 6;              // query rows per pair (T * G) this kernel takes
@@ -105,6 +101,7 @@ constexpr int kPSlots = 4;               // P ring depth
 constexpr int kPSlotBytes = 2 * 2048;    // rows 0..7, rows 8..15 (zero) x 128 tokens
 constexpr int kVscWarpBytes = kUnitPages * 2 * 8 * 4;   // 512
 constexpr int kVSlots = 3;               // V^T ring depth (Tensor Memory)
+constexpr int kSegCap = 48;              // segments of a CTA that are listed (ScoreMod)
 
 constexpr int kDeqWarps = 8;             // warps 0..7
 constexpr int kSmxWarp0 = 8;             // warps 8..11
@@ -119,7 +116,7 @@ constexpr long long kWaitBudget = 2000000000LL;  // clock cycles (~1 s)
 constexpr float kLazyRescale = 8.0f;             // log2 units
 
 // Tensor Memory columns (all 512).
-constexpr uint32_t kColV = 0;      // kVSlots x 128: V^T (d-half h at +64h), f16 token pairs
+constexpr uint32_t kColV = 0;      // kVSlots x D/2: V^T (half h at +64h or +32h), f16 token pairs
 constexpr uint32_t kColS = 384;    // kNSMax: S^T, fp32, one token per lane
 constexpr uint32_t kColO = 432;    // 2 halves x kNP: O^T, fp32, column = query row
 constexpr uint32_t kColSFA = 464;  // 2 slots x 16: K scale factors, column 4*ks + m1
@@ -134,15 +131,27 @@ static_assert(kColV + kVSlots * 128 <= kColS && kColS + kNSMax <= kColO &&
 // pages' V blocks; the K scale bytes go to their own ring.  K8V4: the K code
 // tile is two head_dim halves [2][128 tokens][128 B], then the V blocks, then
 // the 8 pages' K row scales ([8][128 B] slots, 16 fp32 used); no scale ring.
-template <bool K8>
+//
+// head_dim 128 (NVFP4): the same rows, half as wide, so the K codes and the
+// query terms take the 64-byte swizzle, twice the stages fit, and V^T is one
+// tile of 128 rows: the two "halves" that the V^T writers and the value MMAs
+// work in are then the two halves of the unit's tokens, not of head_dim.
+template <int D, bool K8>
 struct Fmt {
+  static_assert(D == 256 || (D == 128 && !K8), "head_dim");
+  static constexpr int kRowBytes = D / 2;                  // a K row's codes
+  static constexpr int kKPageBytes = kKRows * kRowBytes;   // 2048 (K8: of one head_dim half)
+  static constexpr int kVPageBytes = kVRows * kRowBytes;   // 2304
+  static constexpr int kKsPageBytes = kKsRows * kRowBytes; // 256
+  static constexpr int kVs = 8 * D;                        // V scales inside a page's V block
+  static constexpr int kKsSlotBytes = kUnitPages * kKsPageBytes;   // 2048
   static constexpr int kKTileBytes = K8 ? 2 * kUnitPages * kKPageBytes : kUnitPages * kKPageBytes;
   static constexpr int kVOff = kKTileBytes;                       // V blocks [page][2304]
   static constexpr int kKsOff = kVOff + kUnitPages * kVPageBytes;  // K8: row scales [page][128 B]
   static constexpr int kStageBytes = K8 ? 52224 : kKsOff;          // 1024-aligned
-  static constexpr int kStages = K8 ? 3 : 5;
-  static constexpr int kKsSlots = K8 ? 0 : 8;                      // K scale ring (NVFP4)
-  static constexpr int kQBytes = (K8 ? 2 : 1) * kNSMax * 128;      // query terms, swizzled
+  static constexpr int kStages = K8 ? 3 : 5 * 256 / D;
+  static constexpr int kKsSlots = K8 ? 0 : 8 * 256 / D;            // K scale ring (NVFP4)
+  static constexpr int kQBytes = (K8 ? 256 : kRowBytes) * kNSMax;  // query terms, swizzled
   static constexpr int kOffKs = kStages * kStageBytes;
   static constexpr int kOffQ = kOffKs + kKsSlots * kKsSlotBytes;
   static constexpr int kOffP = kOffQ + kQBytes;                    // P tiles [slot], MN-major f16
@@ -160,7 +169,9 @@ struct Fmt {
   static constexpr int kOffBars = kOffKsv + ((kKsSlots > 0 ? kKsSlots : 1) * 4 + 7) / 8 * 8;
   static constexpr int kNumBars = 2 * kStages + 2 * kKsSlots + 4 + 4 * kVSlots + 2 * kPSlots + 5;
   static constexpr int kOffTmem = kOffBars + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffTmem + 16 + 1024;          // + alignment slack
+  static constexpr int kOffSegs = kOffTmem + 16;                   // ScoreMod: segment list
+  static constexpr int kSegBytes = 16 + kSegCap * 48;
+  static constexpr int kSmemBytes = kOffSegs + kSegBytes + 1024;   // + alignment slack
   // (TMA destinations are 128-byte aligned: each page's 64 bytes of K row
   // scales get a 128-byte slot)
   static_assert(kKsOff + (K8 ? kUnitPages * 128 : 0) <= kStageBytes && kStageBytes % 1024 == 0 &&
@@ -169,7 +180,7 @@ struct Fmt {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(kOffQ % 1024 == 0 && kOffP % 128 == 0 && kOffKs % 128 == 0 &&
                     kOffVsc % 16 == 0 && kOffSfb % 16 == 0 && kOffPages % 16 == 0 &&
-                    kOffRow % 16 == 0 && kOffBars % 8 == 0,
+                    kOffRow % 16 == 0 && kOffBars % 8 == 0 && kOffSegs % 8 == 0,
                 "alignment");
 };
 
@@ -211,19 +222,18 @@ struct Seg {
   int64_t pair_start, seg_end;
   bool bad;
 };
+static_assert(sizeof(Seg) == 48, "segment list entry");
 
+// The rest of a segment whose pair (b, h), pair_start, units and seg_end are
+// known.
 template <class Mod>
-__device__ __forceinline__ Seg segment_at(const Mod &mod, int T, int64_t u, int64_t u1,
-                                          const int32_t *kv_lens, int B, int Hkv, int max_kv_len,
-                                          int max_pages) {
-  Seg s;
-  locate_pair_mod(mod, kv_lens, B, Hkv, T, u, s.b, s.h, s.pair_start, s.units);
-  s.seg_end = min(u1, s.pair_start + s.units);
+__device__ __forceinline__ void fill_segment(Seg &s, const Mod &mod, int T, const int32_t *kv_lens,
+                                             int B, int max_kv_len, int max_pages) {
   s.lo = s.first_unit = 0;
   if (s.b >= B) {  // past the last unit
     s.kv_len = 0;
     s.bad = false;
-    return s;
+    return;
   }
   s.kv_len = kv_lens[s.b];
   if constexpr (Mod::kOn) {
@@ -232,7 +242,75 @@ __device__ __forceinline__ Seg segment_at(const Mod &mod, int T, int64_t u, int6
   }
   s.bad = s.kv_len > max_kv_len || s.kv_len > max_pages * kPageTokens;
   if (s.bad) s.kv_len = 0;  // nothing of a bad sequence is read
+}
+
+template <class Mod>
+__device__ __forceinline__ Seg segment_at(const Mod &mod, int T, int64_t u, int64_t u1,
+                                          const int32_t *kv_lens, int B, int Hkv, int max_kv_len,
+                                          int max_pages) {
+  Seg s;
+  locate_pair_mod(mod, kv_lens, B, Hkv, T, u, s.b, s.h, s.pair_start, s.units);
+  s.seg_end = min(u1, s.pair_start + s.units);
+  fill_segment(s, mod, T, kv_lens, B, max_kv_len, max_pages);
   return s;
+}
+
+// What one warp finds out for the CTA (ScoreMod): its unit range and its
+// first segments.  Walking all sequences for every segment, in every role,
+// costs microseconds at a batch of 64; here 32 sequences are looked at a
+// time, once.
+struct SegList {
+  int64_t u0, u1;
+};
+
+template <class Mod>
+__device__ void list_segments(const Mod &mod, const int32_t *kv_lens, int B, int Hkv, int T, int c,
+                              int S, int max_kv_len, int max_pages, SegList *head, Seg *segs) {
+  const int lane = threadIdx.x & 31;
+  int64_t U = 0;
+  for (int b = lane; b < B; b += 32) U += mod.units(kv_lens, b, T);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
+  U *= Hkv;
+  const int64_t u0 = U > 0 ? range_begin(c, U, S) : 0, u1 = U > 0 ? range_begin(c + 1, U, S) : 0;
+  if (lane == 0) head->u0 = u0, head->u1 = u1;
+  int64_t acc = 0;  // first unit of sequence b0
+  int count = 0;
+  for (int b0 = 0; b0 < B && acc < u1; b0 += 32) {
+    const int b = b0 + lane;
+    const int n = b < B ? mod.units(kv_lens, b, T) : 0;
+    int64_t end = (int64_t)n * Hkv;  // inclusive scan of the spans
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += v;
+    }
+    const int64_t start = acc + end - (int64_t)n * Hkv;
+    acc += __shfl_sync(0xffffffffu, end, 31);
+    // heads h0 .. h1 of this sequence have units in [u0, u1)
+    int h0 = 0, h1 = -1;
+    if (n > 0 && start < u1 && start + (int64_t)n * Hkv > u0) {
+      h0 = start < u0 ? (int)((u0 - start) / n) : 0;
+      h1 = (int)((min(u1, start + (int64_t)n * Hkv) - 1 - start) / n);
+    }
+    int at = h1 - h0 + 1;  // inclusive scan of the counts
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += v;
+    }
+    const int total = __shfl_sync(0xffffffffu, at, 31);
+    int i = count + at - (h1 - h0 + 1);
+    count += total;
+    for (int h = h0; h <= h1 && i < kSegCap; ++h, ++i) {
+      Seg g;
+      g.b = b, g.h = h, g.units = n;
+      g.pair_start = start + (int64_t)h * n;
+      g.seg_end = min(u1, g.pair_start + n);
+      fill_segment(g, mod, T, kv_lens, B, max_kv_len, max_pages);
+      segs[i] = g;
+    }
+  }
 }
 
 // Page of the 16 tokens from `tok` on; -1 when it is absent or when none of
@@ -273,12 +351,26 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// The D/16 scale bytes of a row (the words past them zero).
+template <int D>
+__device__ __forceinline__ uint4 scale_bytes(const uint8_t *p) {
+  if constexpr (D == 256) return *reinterpret_cast<const uint4 *>(p);
+  const uint2 v = *reinterpret_cast<const uint2 *>(p);
+  return make_uint4(v.x, v.y, 0u, 0u);
+}
+
+// Descriptor of a K-major tile of rows of kBytes bytes, swizzled as wide.
+template <int kBytes>
+__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t saddr) {
+  return kBytes == 128 ? smem_desc_sw128(saddr) : smem_desc_sw64(saddr);
+}
+
 // K8 selects the cache format: false = NVFP4 K (tmap_k: 16-row SW128 boxes of
 // K codes; tmap_ks: 2-row boxes of K scales; tmap_v: 18-row boxes of V codes
 // and scales, all over 128-byte rows of the pool), true = K8V4 (tmap_k: 3-D
 // [block][token][256 B], 128-byte SW128 boxes of 16 tokens, one per head_dim
 // half; tmap_ks: [block][64 B] row scales; tmap_v: [block][18][128 B]).
-template <int RM, bool K8, class Mod>
+template <int D, int RM, bool K8, class Mod>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_ks,
@@ -291,7 +383,10 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
   // zero); the score MMA has N = RM * kTerms columns.
   static_assert(RM % 2 == 0 && RM >= 2 && RM <= kRowsCap, "rows");
   constexpr int NS = RM * kTerms;
-  using F = Fmt<K8>;
+  using F = Fmt<D, K8>;
+  constexpr int kHalves = D / 128;  // of head_dim: tiles of 128 V^T rows
+  constexpr int kKPageBytes = F::kKPageBytes, kVPageBytes = F::kVPageBytes,
+                kKsPageBytes = F::kKsPageBytes, kKsSlotBytes = F::kKsSlotBytes, kVs = F::kVs;
   constexpr int kStages = F::kStages, kStageBytes = F::kStageBytes, kKTileBytes = F::kKTileBytes,
                 kKsSlots = F::kKsSlots;
   constexpr int kOffKs = F::kOffKs, kOffQ = F::kOffQ, kOffP = F::kOffP, kOffVsc = F::kOffVsc,
@@ -340,7 +435,11 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = Hq / Hkv;
-  const int R = T * G;
+  // This CTA's query rows: rows r0 .. r0 + R - 1 of the pair's R_all (all of
+  // them unless the launch has a row chunk for each blockIdx.y).
+  const int R_all = T * G;
+  const int r0 = Mod::kOn ? blockIdx.y * RM : 0;
+  const int R = Mod::kOn ? min(RM, R_all - r0) : R_all;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -379,16 +478,35 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     tmem_alloc(sh.tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  const int c = blockIdx.x;
+  SegList *seg_head = reinterpret_cast<SegList *>(smem + F::kOffSegs);
+  Seg *segs = reinterpret_cast<Seg *>(smem + F::kOffSegs + 16);
+  if constexpr (Mod::kOn) {
+    launch_dependents();  // the merge may be set up while this kernel runs
+    if (warp == kPvWarp)
+      list_segments(mod, kv_lens, B, Hkv, T, c, S, max_kv_len, max_pages, seg_head, segs);
+  }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *sh.tmem_slot;
 
-  const int64_t U = total_units(mod, kv_lens, B, Hkv, T);
-  const int c = blockIdx.x;
-  const int64_t u0 = U > 0 ? range_begin(c, U, S) : 0;
-  const int64_t u1 = U > 0 ? range_begin(c + 1, U, S) : 0;
+  int64_t u0, u1;
+  if constexpr (Mod::kOn) {
+    u0 = seg_head->u0, u1 = seg_head->u1;
+  } else {
+    const int64_t U = total_units(mod, kv_lens, B, Hkv, T);
+    u0 = U > 0 ? range_begin(c, U, S) : 0;
+    u1 = U > 0 ? range_begin(c + 1, U, S) : 0;
+  }
+  // The CTA's i-th segment, which starts at unit u.
+  auto segment = [&](uint32_t i, int64_t u) -> Seg {
+    if constexpr (Mod::kOn) {
+      if (i < (uint32_t)kSegCap && u < u1) return segs[i];
+    }
+    return segment_at(mod, T, u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+  };
   const uint32_t n_units = (uint32_t)(u1 - u0);
 
   if (K8 && warp == kKsProducerWarp) {
@@ -412,7 +530,8 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     const int p = lane & 7;
     int64_t u = u0;
-    Seg sg = segment_at(mod, T, u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+    uint32_t si = 0;
+    Seg sg = segment(0, u);
     auto page_for = [&](const Seg &g, int64_t uu) -> int {
       const int tok =
           unit_token<Mod>(g.first_unit, g.units, g.pair_start, uu) + p * kPageTokens;
@@ -429,7 +548,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
       int nxt = -1;
       Seg nsg = sg;
       if (u + 1 < u1) {
-        if (u + 1 >= sg.seg_end) nsg = segment_at(mod, T, u + 1, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+        if (u + 1 >= sg.seg_end) nsg = segment(++si, u + 1);
         nxt = page_for(nsg, u + 1);
       }
       if (uc >= (uint32_t)ring) {
@@ -488,7 +607,8 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // value MMAs of each unit once its V^T and P are ready.  Each commits
     // its own MMAs; the tensor pipe runs both streams.
     if (lane == 0) {
-      int64_t seg_end = segment_at(mod, T, u0, u1, kv_lens, B, Hkv, max_kv_len, max_pages).seg_end;
+      int64_t seg_end = segment(0, u0).seg_end;
+      uint32_t seg_idx = 0;
       bool issued = false;
       if (warp == kMmaWarp) {
         // NVFP4: E2M1 x E2M1 block-scaled; K8V4: E4M3 x E4M3 (kind::f8f6f4,
@@ -496,13 +616,11 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const uint32_t idesc_qk = K8 ? idesc_f16_f32(128, NS, false, false) : idesc_nvf4(128, NS);
         const uint32_t qb = smem_u32(sh.qtile);
         const uint32_t kt0 = smem_u32(sh.stages);
-        uint32_t seg_idx = 0;
         for (uint32_t qk = 0; qk < n_units && !sh.flags[2]; ++qk) {
           const int64_t uu = u0 + qk;
           const bool opens = qk == 0 || uu >= seg_end;
           if (uu >= seg_end) {
-            seg_end = segment_at(mod, T, uu, u1, kv_lens, B, Hkv, max_kv_len, max_pages).seg_end;
-            ++seg_idx;
+            seg_end = segment(++seg_idx, uu).seg_end;
           }
           if (opens) wait_bar(sh.qready, seg_idx & 1, sh.flags, err);
           const int stage = qk % kStages;
@@ -525,9 +643,10 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
                           (hf | ks) > 0);
           } else {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_nvf4_ss(sslot, smem_desc_sw128(kt + 32 * ks), smem_desc_sw128(qb + 32 * ks),
-                          idesc_qk, ks > 0, sfa + 4 * ks, tmem + kColSFB + 4 * ks);
+            for (int ks = 0; ks < D / 64; ++ks)
+              mma_nvf4_ss(sslot, smem_desc_rows<D / 2>(kt + 32 * ks),
+                          smem_desc_rows<D / 2>(qb + 32 * ks), idesc_qk, ks > 0, sfa + 4 * ks,
+                          tmem + kColSFB + 4 * ks);
           }
           mma_commit(sh.sready);
           mma_commit(&sh.empty[stage]);  // the K tile has been read
@@ -547,22 +666,25 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           const int64_t uu = u0 + pv;
           const bool first = pv == 0 || uu >= seg_end;  // O^T starts from zero
           if (uu >= seg_end)
-            seg_end = segment_at(mod, T, uu, u1, kv_lens, B, Hkv, max_kv_len, max_pages).seg_end;
+            seg_end = segment(++seg_idx, uu).seg_end;
           const int ps = pv % kPSlots;
           wait_bar(&sh.pready[ps], (pv / kPSlots) & 1, sh.flags, err);
           const uint32_t pslot = pb + ps * kPSlotBytes;
           const int vs = pv % kVSlots;
-          const uint32_t vslot = tmem + kColV + vs * 128;
-          // One head_dim half at a time: each half's V^T rows are released
-          // as soon as its MMAs complete.
+          const uint32_t vslot = tmem + kColV + vs * (D / 2);
+          // One half at a time (of head_dim; at head_dim 128 of the tokens):
+          // each half's V^T is released as soon as its MMAs complete.
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             wait_bar(&sh.vready[vs * 2 + hf], (pv / kVSlots) & 1, sh.flags, err);
             tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_f16_ts(tmem + kColO + hf * kNP, vslot + 64 * hf + ks * 8,
+            for (int k = 0; k < 4 * kHalves; ++k) {
+              const int ks = kHalves == 2 ? k : 4 * hf + k;  // K step: 16 tokens
+              mma_f16_ts(tmem + kColO + (kHalves == 2 ? hf * kNP : 0),
+                         vslot + (kHalves == 2 ? 64 * hf : 0) + ks * 8,
                          smem_desc(pslot + ks * 256, 128, 2048), idesc_pv, (!first) || ks > 0);
+            }
             mma_commit(&sh.pvdone[vs * 2 + hf]);
           }
           mma_commit(&sh.pfree[ps]);
@@ -602,7 +724,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
       uint32_t w[16];
 #pragma unroll
       for (int m1 = 0; m1 < 4; ++m1) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(kb + (32 * m1 + lane) * 16);
+        const uint4 v = scale_bytes<D>(kb + (32 * m1 + lane) * (D / 16));
         w[0 * 4 + m1] = v.x;
         w[1 * 4 + m1] = v.y;
         w[2 * 4 + m1] = v.z;
@@ -647,25 +769,33 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
       // columns r*8 .. r*8+7 summed and times 2^-k give the row's scores.
       // (Any rounding of the scales and codes would do: only the residual
       // bookkeeping has to be exact.)
+      constexpr int kE = D / 32;  // elements of a lane: 8 (4 at head_dim 128)
       for (int r = warp; r < RM; r += kDeqWarps) {
-        float y[8];
+        float y[kE];
         if (r < R) {
-          const int t = r / G, g = r % G;
-          const uint4 raw = *reinterpret_cast<const uint4 *>(
-              q + ((size_t)(pg.b * T + t) * Hq + pg.h * G + g) * kD + 8 * lane);
-          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+          const int t = (r0 + r) / G, g = (r0 + r) % G;
+          const __nv_bfloat16 *src =
+              q + ((size_t)(pg.b * T + t) * Hq + pg.h * G + g) * D + kE * lane;
+          uint32_t w[kE / 2];
+          if constexpr (kE == 8) {
+            const uint4 raw = *reinterpret_cast<const uint4 *>(src);
+            w[0] = raw.x, w[1] = raw.y, w[2] = raw.z, w[3] = raw.w;
+          } else {
+            const uint2 raw = *reinterpret_cast<const uint2 *>(src);
+            w[0] = raw.x, w[1] = raw.y;
+          }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kE / 2; ++i) {
             y[2 * i] = __uint_as_float(w[i] << 16) * qscale;
             y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * qscale;
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = 0.f;
+          for (int i = 0; i < kE; ++i) y[i] = 0.f;
         }
         float a = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(y[i]));
+        for (int i = 0; i < kE; ++i) a = fmaxf(a, fabsf(y[i]));
         a = warp_max(a);
         // A row whose largest element is below the smallest normal float
         // (2^-126) is taken as zero: its scores would be below 2^-110.
@@ -675,10 +805,10 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const int k = (K8 ? 134 : 135) - eb;
         if (eb > 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = scale_pow2(y[i], k);
+          for (int i = 0; i < kE; ++i) y[i] = scale_pow2(y[i], k);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = 0.f;
+          for (int i = 0; i < kE; ++i) y[i] = 0.f;
         }
         if constexpr (K8) {
           // Term l: E4M3 codes of y * 2^(4l), its value subtracted exactly.
@@ -711,15 +841,16 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           const int n = r * kTerms + l;
           float ga = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ga = fmaxf(ga, fabsf(y[i]));
+          for (int i = 0; i < kE; ++i) ga = fmaxf(ga, fabsf(y[i]));
           ga = fmaxf(ga, __shfl_xor_sync(0xffffffffu, ga, 1));  // 16-element group
+          if constexpr (kE == 4) ga = fmaxf(ga, __shfl_xor_sync(0xffffffffu, ga, 2));
           const uint32_t sb = (uint32_t)__nv_cvt_float_to_fp8(ga * (1.0f / 6.0f), __NV_SATFINITE,
                                                               __NV_E4M3);
           const float sv = e4m3_to_float((uint8_t)sb);
           const float rs = sv > 0.f ? 1.0f / sv : 0.f;
           uint32_t codes = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kE / 2; ++i) {
             // codes of y/s (the hardware's rounding; any choice is exact
             // bookkeeping below), then the chosen values, exact in f16
             const uint32_t pair = f32x2_to_e2m1x2(y[2 * i] * rs, y[2 * i + 1] * rs);
@@ -728,10 +859,18 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
             y[2 * i] -= v.x * sv;  // the products are exact
             y[2 * i + 1] -= v.y * sv;
           }
-          // Row n of the term tile: bytes 4*lane..4*lane+3, 128-byte swizzle.
-          *reinterpret_cast<uint32_t *>(sh.qtile + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) +
-                                        (lane & 3) * 4) = codes;
-          if ((lane & 1) == 0) sh.sfb[n * 16 + (lane >> 1)] = (uint8_t)sb;
+          // Row n of the term tile: kE/2 bytes from kE/2*lane on, swizzled
+          // over 128 (head_dim 128: 64) bytes.
+          if constexpr (kE == 8) {
+            *reinterpret_cast<uint32_t *>(sh.qtile + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) +
+                                          (lane & 3) * 4) = codes;
+            if ((lane & 1) == 0) sh.sfb[n * 16 + (lane >> 1)] = (uint8_t)sb;
+          } else {
+            *reinterpret_cast<uint16_t *>(sh.qtile + n * 64 +
+                                          (((lane >> 3) ^ ((n >> 1) & 3)) << 4) +
+                                          (lane & 7) * 2) = (uint16_t)codes;
+            if ((lane & 3) == 0) sh.sfb[n * 8 + (lane >> 2)] = (uint8_t)sb;
+          }
         }
         }
         if (lane == 0) sh.fac[r] = eb > 0 ? scale_pow2(1.f, -k) : 0.f;
@@ -748,7 +887,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           for (int i = 0; i < 16; ++i) w[i] = 0u;
 #pragma unroll
           for (int n1 = 0; n1 < 2; ++n1) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(sh.sfb + (32 * n1 + lane) * 16);
+            const uint4 v = scale_bytes<D>(sh.sfb + (32 * n1 + lane) * (D / 16));
             w[0 * 4 + n1] = v.x;
             w[1 * 4 + n1] = v.y;
             w[2 * 4 + n1] = v.z;
@@ -766,7 +905,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint32_t uc = 0;
     uint32_t seg_idx = 0;
     for (int64_t u = u0; u < u1; ++seg_idx) {
-      const Seg sg = segment_at(mod, T, u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+      const Seg sg = segment(seg_idx, u);
       if (sg.bad && threadIdx.x == 0) report(err, NVKV_DEVERR_LENGTH);
       const int64_t seg_start = u;
       const size_t slot = (size_t)c + (size_t)sg.b * Hkv + sg.h;
@@ -794,11 +933,11 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           if (stid < RM) {
             int4 row = make_int4(0, 0, 0, 0);
             if (stid < R) {
-              const int pos = sg.kv_len - T + stid / G;
+              const int pos = sg.kv_len - T + (r0 + stid) / G;
               key_range(pos, sg.kv_len, mod.start(sg.b), mod.window, mod.prefix_of(sg.b), row.x,
                         row.y);
               row.z = pos;
-              row.w = __float_as_int(mod.slope2(sg.h * G + stid % G));
+              row.w = __float_as_int(mod.slope2(sg.h * G + (r0 + stid) % G));
             }
             sh.row_s[stid] = row;
           }
@@ -828,8 +967,10 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           // anything, NaN patterns included. ----
           uint32_t *vsc = sh.vsc + (warp * kVscWarpBytes) / 4;
           {
-            const int gsel = lane >> 4, pp = (lane & 15) >> 1, h8 = lane & 1;
-            const int g = 8 * hv + 2 * lq + gsel;
+            // (head_dim 128: the warp's 4 pages, two lanes the same)
+            const int gsel = lane >> 4, h8 = lane & 1;
+            const int pp = kHalves == 2 ? (lane & 15) >> 1 : 4 * hv + ((lane & 7) >> 1);
+            const int g = (kHalves == 2 ? 8 * hv : 0) + 2 * lq + gsel;
             const uint2 sw = *reinterpret_cast<const uint2 *>(vb + pp * kVPageBytes + kVs +
                                                               g * 16 + 8 * h8);
             int nval = sg.kv_len - (tok0 + 16 * pp + 8 * h8);
@@ -863,13 +1004,13 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
             tc_fence_after();
           }
           {
-            const int d = 128 * hv + 32 * lq + lane;
-            const uint32_t vcol = kColV + vs * 128 + 64 * hv;
+            const int d = (kHalves == 2 ? 128 * hv : 0) + 32 * lq + lane;
+            const uint32_t vcol = kColV + vs * (D / 2) + (kHalves == 2 ? 64 * hv : 0);
             const uint32_t *vg = vsc + (lane >> 4) * 8;
 #pragma unroll
-            for (int p = 0; p < kUnitPages; ++p) {
-              const uint2 cw =
-                  *reinterpret_cast<const uint2 *>(vb + p * kVPageBytes + kVc + d * 8);
+            for (int pi = 0; pi < 4 * kHalves; ++pi) {
+              const int p = kHalves == 2 ? pi : 4 * hv + pi;
+              const uint2 cw = *reinterpret_cast<const uint2 *>(vb + p * kVPageBytes + d * 8);
               const uint4 s0 = *reinterpret_cast<const uint4 *>(vg + p * 16);
               const uint4 s1 = *reinterpret_cast<const uint4 *>(vg + p * 16 + 4);
               const uint32_t o8[8] = {
@@ -1027,7 +1168,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
               wait_bar(&sh.pfree[(uc - 1) % kPSlots], ((uc - 1) / kPSlots) & 1, sh.flags, err);
               tc_fence_after();
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
+              for (int half = 0; half < kHalves; ++half) {
                 uint32_t r8[8];
                 const uint32_t col = tl + kColO + half * kNP;
                 tmem_ld8(col, r8);
@@ -1097,7 +1238,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
         // The sums carry the 2^-14 of V^T: o = O * 2^14 / l, lse = m + log2(l).
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < kHalves; ++half) {
           uint32_t o8[8];
           tmem_ld8(tl + kColO + half * kNP, o8);
           tmem_wait_ld();
@@ -1106,7 +1247,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           for (int n = 0; n < RM; ++n) {
             if (n < R) {
               const float v = __uint_as_float(o8[n]);
-              ws_o[(slot * R + n) * kD + d] = lv[n] > 0.f ? v * 16384.f / lv[n] : 0.f;
+              ws_o[(slot * R_all + r0 + n) * D + d] = lv[n] > 0.f ? v * 16384.f / lv[n] : 0.f;
             }
           }
         }
@@ -1114,7 +1255,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           float l = 0.f;
 #pragma unroll
           for (int n = 0; n < RM; ++n) l = n == stid ? lv[n] : l;
-          ws_lse[slot * R + stid] = l > 0.f ? sh.m_s[stid] + log2f(l) : -INFINITY;
+          ws_lse[slot * R_all + r0 + stid] = l > 0.f ? sh.m_s[stid] + log2f(l) : -INFINITY;
         }
         tc_fence_before();
         named_barrier(1, kSmxWarps * 32);  // the sums and maxima have been read
@@ -1146,16 +1287,17 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// The pool as a 2-D byte tensor of 128-byte rows; a box of `rows` rows
+// The pool as a 2-D byte tensor of rows of D/2 bytes; a box of `rows` rows
 // starting at row (page * Hkv + h) * 36 + r0 is part of one page's kv-head
-// block (head_dim 256).
+// block.
 bool make_map(const nvkv_cache &c, int rows, CUtensorMapSwizzle swz, CUtensorMap *map) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t total = (cuuint64_t)c.num_pages * c.num_kv_heads * kRowsPerHead;
-  const cuuint64_t dims[2] = {128, total};
-  const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, (cuuint32_t)rows};
+  const cuuint32_t width = (cuuint32_t)c.head_dim / 2;
+  const cuuint64_t dims[2] = {width, total};
+  const cuuint64_t strides[1] = {width};
+  const cuuint32_t box[2] = {width, (cuuint32_t)rows};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.pool, dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1193,25 +1335,31 @@ bool make_k8_maps(const nvkv_cache &c, CUtensorMap *mk, CUtensorMap *mks, CUtens
              CUDA_SUCCESS;
 }
 
-template <bool K8, class Mod>
+template <int D, bool K8, class Mod>
 cudaError_t launch_fmt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T, int Hq,
                        float sm_scale, int S, float *ws_o, float *ws_lse, cudaStream_t stream,
                        const Mod &mod) {
   CUtensorMap map_k, map_ks, map_v;
+  const CUtensorMapSwizzle swz = D == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   const bool ok = K8 ? make_k8_maps(c, &map_k, &map_ks, &map_v)
-                     : make_map(c, kKRows, CU_TENSOR_MAP_SWIZZLE_128B, &map_k) &&
+                     : make_map(c, kKRows, swz, &map_k) &&
                            make_map(c, kKsRows, CU_TENSOR_MAP_SWIZZLE_NONE, &map_ks) &&
                            make_map(c, kVRows, CU_TENSOR_MAP_SWIZZLE_NONE, &map_v);
   if (!ok) return cudaErrorNotSupported;
   const float qscale = sm_scale * 1.4426950408889634f;
+  // Query rows of a pair in chunks of at most 6 (one, except at head_dim
+  // 128), as even as they come: 16 rows are 6 + 6 + 4.
   const int R = T * (Hq / c.num_kv_heads);
-  auto kernel = R <= 2   ? decode_qk4_kernel<2, K8, Mod>
-                : R <= 4 ? decode_qk4_kernel<4, K8, Mod>
-                         : decode_qk4_kernel<6, K8, Mod>;
-  const int smem = Fmt<K8>::kSmemBytes;
+  const int chunks = (R + kRowsCap - 1) / kRowsCap, Rc = (R + chunks - 1) / chunks;
+  auto kernel = Rc <= 2   ? decode_qk4_kernel<D, 2, K8, Mod>
+                : Rc <= 4 ? decode_qk4_kernel<D, 4, K8, Mod>
+                          : decode_qk4_kernel<D, 6, K8, Mod>;
+  const int smem = Fmt<D, K8>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<S, kThreads, smem, stream>>>(
+  const int RM = Rc <= 2 ? 2 : Rc <= 4 ? 4 : 6;
+  const dim3 grid((unsigned)S, (unsigned)((R + RM - 1) / RM));
+  kernel<<<grid, kThreads, smem, stream>>>(
       map_k, map_ks, map_v, c.num_pages, c.num_kv_heads, s.page_table, s.max_pages_per_seq,
       s.kv_lens, s.batch, s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), T, Hq, qscale, S,
       ws_o, ws_lse, s.err_word, mod);
@@ -1221,19 +1369,26 @@ cudaError_t launch_fmt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, i
 }  // namespace
 
 // True when this kernel takes the shape: head_dim 256 and at most 6 query
-// rows (T * Hq/Hkv) per (sequence, kv-head).  The same holds for both cache
-// formats.
-bool decode_qk4_supported(const nvkv_cache &c, int T, int Hq) {
+// rows (T * Hq/Hkv) per (sequence, kv-head), for both cache formats; with a
+// ScoreMod over an NVFP4 cache also head_dim 128 (more rows in chunks of 6,
+// each reading the keys once).
+bool decode_qk4_supported(const nvkv_cache &c, int T, int Hq, bool mod) {
   const int R = T * (Hq / c.num_kv_heads);
-  return c.head_dim == kD && R >= 1 && R <= kRowsCap && encode_fn() != nullptr;
+  if (R < 1 || encode_fn() == nullptr) return false;
+  return c.head_dim == 256 ? R <= kRowsCap : mod && c.head_dim == 128;
 }
 
 // mod: null for plain causal attention.
 cudaError_t launch_decode_qk4(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
                               int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
                               cudaStream_t stream, const ScoreMod *mod) {
-  return mod ? launch_fmt<false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod)
-             : launch_fmt<false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, NoMod{});
+  if (!mod)
+    return c.head_dim == 256 ? launch_fmt<256, false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse,
+                                                      stream, NoMod{})
+                             : cudaErrorNotSupported;
+  return c.head_dim == 256
+             ? launch_fmt<256, false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod)
+             : launch_fmt<128, false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod);
 }
 
 // The same kernel over a K8V4 cache (E4M3 K rows with an fp32 row scale,
@@ -1241,8 +1396,8 @@ cudaError_t launch_decode_qk4(const nvkv_cache &c, const nvkv_seqs &s, const voi
 cudaError_t launch_decode_qk4_k8v4(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
                                    int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
                                    cudaStream_t stream, const ScoreMod *mod) {
-  return mod ? launch_fmt<true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod)
-             : launch_fmt<true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, NoMod{});
+  return mod ? launch_fmt<256, true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod)
+             : launch_fmt<256, true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, NoMod{});
 }
 
 }  // namespace nvkv

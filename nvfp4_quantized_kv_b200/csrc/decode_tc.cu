@@ -225,6 +225,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
   const int R = T * G;
   const int R_all = T_all * G;
 
+  if constexpr (Mod::kOn) launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.full[i], 1);

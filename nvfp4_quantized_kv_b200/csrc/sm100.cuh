@@ -309,6 +309,28 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
   return d;
 }
 
+// The same for rows of 64 bytes in the 64-byte swizzle (the 16-byte chunk
+// index is XORed with address bits 7..8), 8-row groups of 512 bytes.
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(512 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;             // layout type: 64-byte swizzle
+  return d;
+}
+
+// Programmatic dependent launch: the next kernel of the stream, if it was
+// launched for it, may start once every CTA has said so; grid_dependency_wait
+// in that kernel returns when this one has finished and its writes are seen.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Instruction descriptor for kind::mxf4nvf4: E2M1 A and B (K-major), UE4M3
 // scale factors, K = 64, f32 accumulate; scale-factor ids 0.
 __host__ __device__ constexpr uint32_t idesc_nvf4(int M, int N) {

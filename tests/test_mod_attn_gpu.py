@@ -20,7 +20,7 @@ def slopes(h):
 
 # what a kernel rounds, by the kernel the step's shape runs on
 def decode_slack(case, T):
-    name = nv.nvkv_decode_kernel_name(case.cache, T, case.Hq)
+    name = nv.nvkv_decode_mod_kernel_name(case.cache, T, case.Hq)
     return "fp32" if name == "decode_simt" else "f16 weights"
 
 
@@ -44,6 +44,10 @@ DECODE = [
     ("verify_start_inside", 24, 4, 256, [300, 128], 6, lambda h: Mod(starts=[297, 126])),
     ("wide_verify", 24, 4, 256, [350], 16, lambda h: Mod(window=30, slopes=slopes(h))),
     ("one_head", 4, 4, 256, [200, 70], 5, lambda h: Mod(window=64, cap=5.0)),
+    ("chunked_128", 8, 2, 128, [700, 129, 16], 6, lambda h: Mod(cap=30.0, window=200)),
+    ("alibi_128", 8, 2, 128, [777, 5, 128], 1, lambda h: Mod(slopes=slopes(h))),
+    ("one_head_128", 4, 4, 128, [200, 70], 2, lambda h: Mod(prefix=[199, 3], cap=5.0)),
+    ("many_sequences", 4, 4, 256, [1 + 37 * i % 300 for i in range(70)], 1, lambda h: Mod(window=40)),
     ("short_T", 24, 4, 256, [2, 3, 150], 6, lambda h: Mod(cap=30.0, prefix=[2, 1, 0])),
     ("empty_seq", 24, 4, 256, [0, 40, 0], 1, lambda h: Mod(window=16)),
     ("nothing_seen", 24, 4, 256, [40, 50], 1, lambda h: Mod(starts=[40, 1000])),
@@ -69,7 +73,7 @@ def test_decode(c, kernel, monkeypatch):
 def test_decode_k8v4(D, Hq, T):
     case = Case(Hq, 2, D, [150, 33], [T, T], seed=3, k8=True).device()
     m = Mod(cap=10.0, window=70, slopes=slopes(Hq), starts=[100, 0])
-    name = nv.nvkv_decode_kernel_name(case.cache, T, Hq)
+    name = nv.nvkv_decode_mod_kernel_name(case.cache, T, Hq)
     ref, tol = case.reference(m, D ** -0.5, True, "fp32" if name == "decode_simt" else "f16 weights")
     assert_within(run_decode(case, m, T, D ** -0.5), ref, tol, name)
     assert int(case.err.item()) == 0
@@ -208,6 +212,18 @@ def test_bad_visible_pages_are_reported_and_left_out(kernel, monkeypatch):
                 # one page of about eight fewer keys: the same kinds of error,
                 # on weights at most 120/104 as large
                 assert ((out[i, hq].double().cpu() - o).abs() <= 2 * full[i, hq] + 2 ** -8 * o.abs() + 4e-3).all()
+
+
+def test_more_segments_than_the_list_holds():
+    """One split over many one-unit pairs: the CTA's segments run past its
+    list."""
+    for D in (128, 256):
+        case = Case(16, 16, D, [5, 130, 17, 9], [1] * 4, seed=21).device()
+        m = Mod(cap=10.0, window=100)
+        ref, tol = case.reference(m, D ** -0.5, True, decode_slack(case, 1))
+        for splits in (1, 2):
+            assert_within(run_decode(case, m, 1, D ** -0.5, splits), ref, tol, f"{D}/S{splits}")
+        assert int(case.err.item()) == 0
 
 
 def test_rows_behind_the_last_sequence_are_left_alone():
