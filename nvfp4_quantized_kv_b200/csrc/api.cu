@@ -41,7 +41,7 @@ cudaError_t launch_prefill_simt(const nvkv_cache &, const nvkv_seqs &, const voi
                                 const ScoreMod *);
 cudaError_t launch_page_copy(const uint8_t *, int64_t, uint8_t *, int64_t, const int32_t *,
                              const int32_t *, int, int64_t, int32_t *, cudaStream_t);
-int64_t read_rows_blocks(const nvkv_cache &, int);
+bool read_rows_fits(const nvkv_cache &, int);
 cudaError_t launch_read_rows(const nvkv_cache &, const nvkv_seqs &, const int32_t *,
                              const int32_t *, int, int, void *, void *, cudaStream_t, bool);
 bool append_axes_fits(const nvkv_cache &, int, int, bool);
@@ -323,7 +323,7 @@ nvkv_status read_rows(const nvkv_cache *cache, const nvkv_seqs *seqs, const int3
   if (total_rows == 0 || max_rows == 0) return NVKV_OK;
   if (!starts || !cu_rows || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
     return NVKV_ERR_INVALID_ARG;
-  if (read_rows_blocks(*cache, max_rows) > INT32_MAX) return NVKV_ERR_UNSUPPORTED;
+  if (!read_rows_fits(*cache, max_rows)) return NVKV_ERR_UNSUPPORTED;
   return cuda_status(launch_read_rows(*cache, *seqs, starts, cu_rows, total_rows, max_rows, k_out,
                                       v_out, reinterpret_cast<cudaStream_t>(stream), k8));
 }

@@ -225,3 +225,73 @@ def test_python_refusals():
             f(**kw)
     with pytest.raises(nv.NvkvError):
         f(a=[2] * 32)
+
+
+def test_every_value_under_every_scale_decides_as_the_plain_append():
+    """V: every bf16 value up to 7 scales, under every positive scale (the
+    group's first element is 6 scales): the bytes of nvkv_append."""
+    e4m3 = torch.arange(1, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    values = torch.arange(0, 0x7F80, dtype=torch.int16).view(torch.bfloat16).double()
+    groups = []
+    for s in e4m3.tolist():
+        v = values[(values <= 6.2 * s) & (values >= 0.1 * s)]
+        v = v[: len(v) // 15 * 15] if len(v) >= 15 else torch.cat([v, v.new_zeros(15 - len(v))])
+        v = v.reshape(-1, 15) * torch.where(torch.arange(15) % 2 == 0, 1.0, -1.0)
+        groups.append(torch.cat([torch.full((len(v), 1), 6 * s, dtype=torch.float64), v], 1))
+    g = torch.cat(groups)
+    Hkv, D = 4, 256
+    n = -(-len(g) // (Hkv * D // 16))
+    flat = torch.zeros(n * Hkv * D // 16, 16, dtype=torch.float64)
+    flat[: len(g)] = g
+    v = flat.reshape(n, Hkv, D).bfloat16().cuda()
+    assert torch.equal(v.double().cpu().reshape(-1, 16), flat)  # all exact bf16
+    pages = -(-n // 16)
+    seqs = nv.Seqs(torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+                   torch.tensor([n], dtype=torch.int32, device="cuda"), pages * 16)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    cs = torch.zeros(1, 16, 2, device="cuda")
+    cs[..., 0] = 1
+    pos = torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    a = nv.Cache.allocate(pages, Hkv, D, "cuda", fill=0)
+    b = nv.Cache.allocate(pages, Hkv, D, "cuda", fill=0)
+    nv.nvkv_append_rope_axes(a, seqs, v, v, cu, n, n, cs, 32, pos, [0] * 16)
+    nv.nvkv_append(b, seqs, v, v, cu, n, n)
+    torch.cuda.synchronize()
+    assert torch.equal(a.pool, b.pool)
+
+
+def test_fp32_neighbours_of_every_border_decide_as_the_plain_rotating_append():
+    """K: fp32 values on every rounding border m * s and up to 6 floats beside
+    it, for 40 scales, made by a table of (value, 0) under unit elements."""
+    D, half = 256, 128
+    rows = []
+    for byte in range(8, 127, 3):
+        s = torch.tensor([byte], dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+        vals = []
+        for m in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0):
+            base = (s * m).view(torch.int32)
+            vals += [(base + d).view(torch.float32) for d in range(-6, 7)]
+        vals = torch.cat(vals)
+        vals = torch.cat([vals, vals.new_zeros(-len(vals) % 15)]).reshape(-1, 15)
+        rows.append(torch.cat([torch.full((len(vals), 1), 6.0) * s, vals], 1))
+    g = torch.cat(rows)
+    n = -(-len(g) // (half // 16))
+    cs = torch.zeros(n, half, 2)
+    flat = torch.zeros(n * half // 16, 16)
+    flat[: len(g)] = g
+    cs[..., 0] = flat.reshape(n, half)
+    k = torch.zeros(n, 1, D, dtype=torch.bfloat16, device="cuda")
+    k[..., :half] = torch.where(torch.arange(half) % 3 == 0, -1.0, 1.0)
+    k[..., 0:half:16] = 1.0
+    pages = -(-n // 16)
+    seqs = nv.Seqs(torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+                   torch.tensor([n], dtype=torch.int32, device="cuda"), pages * 16)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")[None].contiguous()
+    a = nv.Cache.allocate(pages, 1, D, "cuda", fill=0)
+    b = nv.Cache.allocate(pages, 1, D, "cuda", fill=0)
+    cs = cs.cuda()
+    nv.nvkv_append_rope_axes(a, seqs, k, k, cu, n, n, cs, D, pos, [0] * half)
+    nv.nvkv_append_rope(b, seqs, k, k, cu, n, n, cs, D)
+    torch.cuda.synchronize()
+    assert torch.equal(a.pool, b.pool)
