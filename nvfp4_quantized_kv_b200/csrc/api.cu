@@ -25,10 +25,14 @@ cudaError_t launch_decode_qk4_k8v4(const nvkv_cache &, const nvkv_seqs &, const 
                                    float, int, float *, float *, cudaStream_t, const ScoreMod *);
 cudaError_t launch_decode_tc(const nvkv_cache &, const nvkv_seqs &, const void *, int, int, float,
                              int, float *, float *, cudaStream_t, const ScoreMod *);
-bool prefill_tc_supported(const nvkv_cache &, bool mod);
+bool prefill_tc_supported(const nvkv_cache &);
 cudaError_t launch_prefill_tc(const nvkv_cache &, const nvkv_seqs &, const void *, const int32_t *,
-                              int, int, int, float, void *, int, float *, float *, cudaStream_t,
-                              const ScoreMod *);
+                              int, int, int, float, void *, int, float *, float *, cudaStream_t);
+cudaError_t launch_prefill_mod(const nvkv_cache &, const nvkv_seqs &, const void *,
+                               const int32_t *, int, int, int, float, void *, int, float *,
+                               float *, cudaStream_t, const ScoreMod &);
+int prefill_mod_auto_splits(const nvkv_cache &, const nvkv_seqs &, int, int, int,
+                            const ScoreMod &, int);
 int prefill_max_splits();
 int prefill_auto_splits(int64_t, int);
 int prefill_tc_items(const nvkv_cache &, const nvkv_seqs &, int, int);
@@ -206,7 +210,12 @@ nvkv_status check_mod(const nvkv_score_mod *mod, ScoreMod &m) {
     return NVKV_ERR_INVALID_ARG;
   m.cap2 = mod->softcap * kLog2e;
   m.cap_in = mod->softcap > 0.f ? 2.f * kLog2e / m.cap2 : 0.f;
-  if (!std::isfinite(m.cap2) || !std::isfinite(m.cap_in)) return NVKV_ERR_INVALID_ARG;
+  m.cap_u = mod->softcap > 0.f ? 1.f / m.cap2 : 0.f;
+  // kCapSmall's polynomial of tanh
+  const double tanh_poly[5] = {0.9999972283, -0.3332307647, 0.1322609151, -0.04928044419, 0.01231882928};
+  for (int i = 0; i < 5; ++i) m.poly[i] = (float)(tanh_poly[i] * m.cap2);
+  if (!std::isfinite(m.cap2) || !std::isfinite(m.cap_in) || !std::isfinite(m.cap_u * 16384.f))
+    return NVKV_ERR_INVALID_ARG;
   m.window = mod->window;
   m.slopes = mod->alibi_slopes;
   m.prefix = mod->prefix_lens;
@@ -245,35 +254,6 @@ cudaError_t run_decode_k8v4(const nvkv_cache &c, const nvkv_seqs &s, const void 
   return launch_decode_simt(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, true, mod);
 }
 
-// The key-split tensor-core prefill, else the CUDA-core one (arguments
-// checked); mod: null for plain causal attention.
-nvkv_status run_prefill_split(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
-                              const int32_t *cu_q, int total_q, int max_q, int Hq, float sm_scale,
-                              int num_splits, void *workspace, size_t workspace_bytes, void *out,
-                              cudaStream_t stream, const ScoreMod *mod) {
-  if (force_simt() || !prefill_tc_supported(c, mod != nullptr))
-    return cuda_status(
-        launch_prefill_simt(c, s, q, cu_q, total_q, Hq, sm_scale, out, stream, false, mod));
-  int S = num_splits > 0 ? num_splits
-                         : prefill_auto_splits(prefill_tc_items(c, s, max_q, Hq),
-                                               nvkv_default_num_splits());
-  if (mod && num_splits == 0) {  // as many as the workspace has room for
-    const bool usable = workspace && aligned16(workspace);
-    while (S > 1 && (!usable || workspace_bytes < prefill_layout(total_q, Hq, c.head_dim, S).total))
-      --S;
-  }
-  float *ws_o = nullptr, *ws_lse = nullptr;
-  if (S > 1) {
-    const PrefillLayout w = prefill_layout(total_q, Hq, c.head_dim, S);
-    if (!workspace || !aligned16(workspace) || workspace_bytes < w.total)
-      return NVKV_ERR_WORKSPACE;
-    ws_o = static_cast<float *>(workspace);
-    ws_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.lse_off);
-  }
-  return cuda_status(launch_prefill_tc(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out, S, ws_o,
-                                       ws_lse, stream, mod));
-}
-
 nvkv_status decode_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q, int32_t T,
                        int32_t num_q_heads, float sm_scale, const nvkv_score_mod *mod,
                        int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
@@ -309,8 +289,27 @@ nvkv_status prefill_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const vo
   if (k8)
     return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
                                            out, s, true, &m));
-  return run_prefill_split(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale,
-                           num_splits, workspace, workspace_bytes, out, s, &m);
+  if (force_simt())
+    return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
+                                           out, s, false, &m));
+  const int D = cache->head_dim;
+  const bool usable = workspace && aligned16(workspace);
+  auto need = [&](int S) { return prefill_layout(total_q, num_q_heads, D, S).total; };
+  int S = num_splits;
+  if (S == 0) {  // the automatic count, as far as the workspace has room
+    S = prefill_mod_auto_splits(*cache, *seqs, total_q, max_q, num_q_heads, m,
+                                nvkv_default_num_splits());
+    while (S > 1 && (!usable || workspace_bytes < need(S))) --S;
+  }
+  float *ws_o = nullptr, *ws_lse = nullptr;
+  if (S > 1) {
+    if (!usable || workspace_bytes < need(S)) return NVKV_ERR_WORKSPACE;
+    ws_o = static_cast<float *>(workspace);
+    ws_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                       prefill_layout(total_q, num_q_heads, D, S).lse_off);
+  }
+  return cuda_status(launch_prefill_mod(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads,
+                                        sm_scale, out, S, ws_o, ws_lse, s, m));
 }
 
 nvkv_status read_rows(const nvkv_cache *cache, const nvkv_seqs *seqs, const int32_t *starts,
@@ -472,9 +471,9 @@ nvkv_status nvkv_prefill_attn(const nvkv_cache *cache, const nvkv_seqs *seqs, co
       check_prefill(cache, seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale, out);
   if (st != NVKV_OK || total_q == 0) return st;
   cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-  if (!force_simt() && prefill_tc_supported(*cache, false))
+  if (!force_simt() && prefill_tc_supported(*cache))
     return cuda_status(launch_prefill_tc(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads,
-                                         sm_scale, out, 1, nullptr, nullptr, st_, nullptr));
+                                         sm_scale, out, 1, nullptr, nullptr, st_));
   return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
                                          out, st_, false, nullptr));
 }
@@ -493,7 +492,7 @@ int32_t nvkv_prefill_num_splits(const nvkv_cache *cache, int32_t batch, int32_t 
   if (check_cache(cache) != NVKV_OK || batch <= 0 || max_q < 0 || num_q_heads <= 0 ||
       num_q_heads % cache->num_kv_heads != 0)
     return 0;
-  if (force_simt() || !prefill_tc_supported(*cache, false)) return 1;
+  if (force_simt() || !prefill_tc_supported(*cache)) return 1;
   nvkv_seqs s{};
   s.batch = batch;
   return prefill_auto_splits(prefill_tc_items(*cache, s, max_q, num_q_heads),
@@ -510,9 +509,24 @@ nvkv_status nvkv_prefill_attn_split(const nvkv_cache *cache, const nvkv_seqs *se
   if (st != NVKV_OK) return st;
   if (num_splits < 0 || num_splits > prefill_max_splits()) return NVKV_ERR_INVALID_ARG;
   if (total_q == 0) return NVKV_OK;
-  return run_prefill_split(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads, sm_scale,
-                           num_splits, workspace, workspace_bytes, out,
-                           reinterpret_cast<cudaStream_t>(stream), nullptr);
+  cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
+  if (force_simt() || !prefill_tc_supported(*cache))
+    return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
+                                           out, st_, false, nullptr));
+  const int S = num_splits > 0 ? num_splits
+                               : prefill_auto_splits(
+                                     prefill_tc_items(*cache, *seqs, max_q, num_q_heads),
+                                     nvkv_default_num_splits());
+  float *ws_o = nullptr, *ws_lse = nullptr;
+  if (S > 1) {
+    const PrefillLayout w = prefill_layout(total_q, num_q_heads, cache->head_dim, S);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < w.total)
+      return NVKV_ERR_WORKSPACE;
+    ws_o = static_cast<float *>(workspace);
+    ws_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.lse_off);
+  }
+  return cuda_status(launch_prefill_tc(*cache, *seqs, q, cu_q, total_q, max_q, num_q_heads,
+                                       sm_scale, out, S, ws_o, ws_lse, st_));
 }
 
 size_t nvkv_k8v4_page_bytes(int32_t num_kv_heads, int32_t head_dim) {

@@ -1,0 +1,858 @@
+// prefill_mod.cu -- chunked prefill with modified scores and masks
+// (nvkv_prefill_attn_mod) over the NVFP4 paged pool on the 5th-generation
+// tensor cores (tcgen05), head_dim 128 and 256.
+//
+// Per query row i (position p, head hq): x_j = sm_scale q_i.k_j, capped by
+// cap * tanh(x / cap), minus slope * |p - j|, over the keys lo_i <= j < hi_i
+// of its interval (score_mod.cuh); softmax; times V.
+//
+// One CTA owns 128 query rows (chunk tokens x GQA heads) of one kv-head and
+// streams the 64-token key tiles that any of its rows sees, from the newest
+// to the oldest: with a distance bias the largest scores come first, so the
+// running maximum is found in the first tile instead of being raised in every
+// one. Q (128 x D, f16, scaled to base-2 scores) sits in Tensor Memory as the
+// A operand of S = Q K^T (N = 64), S is double-buffered there, P (f16)
+// overwrites its own S slot as the A operand of O += P V (N = D), O stays in
+// Tensor Memory.
+//
+// The tile's time is set by the softmax: with one thread for a row's 64
+// scores and one such warp on each SM sub-partition, the tile took 3,900
+// cycles of that warp (a clock64 trace), while K (1,000), V (1,000 with 8
+// warps, 2,700 with 4) and the MMAs (1,800) waited. So two warpgroups share
+// every tile, 32 keys each; the two threads of a row agree on its running
+// maximum only when a score may pass it by 2^8, which one barrier of their
+// two warps detects (it also keeps P from overwriting scores not yet read).
+//   warps  0.. 3  K tile: a token a thread, D/64 chunks of 32 elements
+//   warps  4..11  V^T tile: a head_dim row a thread, D/64 pages
+//   warps 12..15  softmax of the tile's keys  0..31: a query row a thread
+//   warps 16..19  softmax of the tile's keys 32..63
+//   warp  20      TMA: the tile's 4 page blocks into a 4-stage ring
+//   warp  21      issues the MMAs (one thread, event-driven)
+// Warps 4..19 write the output. Every wait is bounded; a timeout sets
+// NVKV_DEVERR_TIMEOUT and drains.
+#include "score_mod.cuh"
+#include "sm100.cuh"
+
+namespace nvkv {
+
+bool make_pool_tmap(const nvkv_cache &c, CUtensorMap *map);
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kTileTokens = 64;
+constexpr int kTilePages = 4;
+constexpr int kStages = 4;
+constexpr int kKWarps = 4;        // warps 0..3
+constexpr int kVWarps = 8;        // warps 4..11
+constexpr int kDeqWarps = kKWarps + kVWarps;
+constexpr int kSmxWarps = 8;      // two warpgroups: warps 12..15 and 16..19
+constexpr int kProducerWarp = 20;
+constexpr int kMmaWarp = 21;
+constexpr int kThreads = 22 * 32;
+constexpr int kHalf = kTileTokens / 2;  // keys of a softmax thread
+constexpr uint32_t kTmemCols = 512;
+constexpr long long kWaitBudget = 2000000000LL;
+constexpr unsigned kPollSleepNs = 100;  // of the MMA thread after an idle poll
+constexpr float kLazyRescale = 8.0f;
+
+// Tensor Memory columns (head_dim 128 uses half of Q's and O's).
+constexpr uint32_t kColQ = 0;     // 128: Q (row lanes, d pairs)
+constexpr uint32_t kColS = 128;   // 2 x 64: S slots (P overwrites the first 32 columns)
+constexpr uint32_t kColO = 256;   // 256: O (row lanes, fp32 d)
+
+// Sizes and shared memory. A page's kv-head block is staged as 128-byte rows
+// with the 128-byte TMA swizzle: byte `off` of the block lies at swz(off).
+template <int D>
+struct Cfg {
+  static_assert(D == 128 || D == 256, "head_dim");
+  static constexpr int kHeadBytes = 18 * D;
+  static constexpr int kRowsPerHead = kHeadBytes / 128;
+  static constexpr int kPagePitch = (kHeadBytes + 1023) / 1024 * 1024;
+  static constexpr int kStageBytes = kTilePages * kPagePitch;
+  static constexpr int kKTileBytes = kTileTokens * D * 2;
+  static constexpr int kVTileBytes = D * kTileTokens * 2;
+  static constexpr int kOffK = kStages * kStageBytes;
+  static constexpr int kOffV = kOffK + 2 * kKTileBytes;
+  // V scales of a tile as f16 pairs [page][group][8], two tables (tile parity)
+  static constexpr int kVscBytes = kTilePages * (D / 16) * 8 * 4;
+  static constexpr int kOffVsc = kOffV + 2 * kVTileBytes;
+  static constexpr int kOffRed = kOffVsc + 2 * kVscBytes;           // float[2][128]: a half's maxima
+  static constexpr int kOffL = kOffRed + 2 * 128 * 4;               // float[2][128]: denominators
+  static constexpr int kOffPages = kOffL + 2 * 128 * 4;             // int[stages][4]
+  static constexpr int kOffPres = kOffPages + kStages * kTilePages * 4;  // u32[4]
+  static constexpr int kOffFlags = kOffPres + 16;
+  static constexpr int kOffBars = kOffFlags + 16;
+  // full, empty; kready, vready, sready, pready, pvdone; qready, final, lready
+  static constexpr int kNumBars = 2 * kStages + 2 * 5 + 3;
+  static constexpr int kOffTmem = kOffBars + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffTmem + 16 + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(kOffK % 1024 == 0 && kOffPages % 16 == 0 && kOffBars % 8 == 0, "alignment");
+};
+
+__device__ __forceinline__ int swz(int off) { return off ^ ((off >> 3) & 0x70); }
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *flags,
+                                         int32_t *err) {
+  return guarded_wait(bar, parity, flags + 2, err, kWaitBudget);  // flags[2]: abort
+}
+
+__device__ __forceinline__ uint32_t dup_scale(uint32_t byte) {
+  return e4m3x2_to_f16x2(byte | (byte << 8));
+}
+
+struct Args {
+  int num_pages, Hkv;
+  const int32_t *page_table;
+  int max_pages;
+  const int32_t *kv_lens;
+  int max_kv_len;
+  const __nv_bfloat16 *q;
+  const int32_t *cu_q;
+  int total_q, Hq;
+  float qscale;
+  __nv_bfloat16 *out;
+  int num_splits;
+  float *ws_o, *ws_lse;  // null when num_splits is 1
+  int32_t *err;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const ScoreMod mod) {
+  using C = Cfg<D>;
+  constexpr int kPagePitch = C::kPagePitch, kStageBytes = C::kStageBytes,
+                kKTileBytes = C::kKTileBytes, kVTileBytes = C::kVTileBytes;
+  // blockIdx.x = m-tile * num_splits + split: split s of an m-tile takes the
+  // s-th of num_splits equal runs of its key tiles and, when num_splits > 1,
+  // leaves O / l and log2(l) + m of its rows in the workspace for the merge.
+  launch_dependents();
+  const int mt = blockIdx.x / a.num_splits, split = blockIdx.x % a.num_splits;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int G = a.Hq / a.Hkv;
+  const int q0 = a.cu_q[b];
+  const int n_b = a.cu_q[b + 1] - q0;
+  const int kv_len = a.kv_lens[b];
+  const int prefix = mod.prefix_of(b);
+  const int rows = n_b * G;
+  if (128 * mt >= rows) return;  // uniform: this tile has no query row
+  const bool bad = n_b < 0 || q0 < 0 || q0 + n_b > a.total_q || kv_len < n_b ||
+                   kv_len > a.max_kv_len || kv_len > a.max_pages * kPageTokens;
+  // Output rows exist only when the chunk lies inside the total_q rows.
+  const bool rows_ok = n_b >= 0 && q0 >= 0 && q0 + n_b <= a.total_q;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  uint8_t *stages = smem;
+  uint8_t *ktiles = smem + C::kOffK;
+  uint8_t *vtiles = smem + C::kOffV;
+  uint32_t *vsc = reinterpret_cast<uint32_t *>(smem + C::kOffVsc);  // [2][page][group][8]
+  float *red_s = reinterpret_cast<float *>(smem + C::kOffRed);
+  float *l_s = reinterpret_cast<float *>(smem + C::kOffL);
+  int32_t *spages = reinterpret_cast<int32_t *>(smem + C::kOffPages);
+  // Bit p of entry (tile & 3) is set when page p of the tile is present, so
+  // the softmax leaves the keys of an absent page out. Written with the
+  // tile's K; the K of tile j + 4 is written after the scores of tile j + 2,
+  // which wait for the value MMAs of tile j.
+  volatile uint32_t *present = reinterpret_cast<volatile uint32_t *>(smem + C::kOffPres);
+  volatile int *flags = reinterpret_cast<volatile int *>(smem + C::kOffFlags);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBars);
+  uint64_t *full = bars, *empty = bars + kStages;
+  uint64_t *kready = bars + 2 * kStages, *vready = kready + 2, *sready = kready + 4,
+           *pready = kready + 6, *pvdone = kready + 8, *qready = kready + 10,
+           *final_bar = kready + 11, *lready = kready + 12;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffTmem);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // The keys [key_lo, key_hi) that any row of the tile sees: every warp scans
+  // the tile's tokens.
+  int key_lo = 0x7fffffff, key_hi = 0;
+  if (!bad) {
+    const int i_last = min(n_b - 1, (128 * mt + 127) / G);
+    for (int i = (128 * mt) / G + lane; i <= i_last; i += 32) {
+      int lo, hi;
+      key_range(kv_len - n_b + i, kv_len, mod.start(q0 + i), mod.window, prefix, lo, hi);
+      if (lo < hi) key_lo = min(key_lo, lo), key_hi = max(key_hi, hi);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    key_lo = min(key_lo, __shfl_xor_sync(0xffffffffu, key_lo, o));
+    key_hi = max(key_hi, __shfl_xor_sync(0xffffffffu, key_hi, o));
+  }
+  if (key_lo >= key_hi) key_lo = key_hi = 0;  // nothing is seen
+  const int tile_lo = key_lo / kTileTokens;
+  const int ntiles_all = (key_hi + kTileTokens - 1) / kTileTokens - tile_lo;
+  // This CTA's key tiles j0 .. j0 + ntiles - 1, counted from the newest; every
+  // ring and barrier below counts from its first tile.
+  const int j0 = (int)((int64_t)split * ntiles_all / a.num_splits);
+  const int ntiles = (int)((int64_t)(split + 1) * ntiles_all / a.num_splits) - j0;
+  auto tile_key = [&](int j) { return (tile_lo + ntiles_all - 1 - (j0 + j)) * kTileTokens; };
+
+  if (bad && threadIdx.x == 0) report(a.err, NVKV_DEVERR_LENGTH);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kDeqWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kready[i], kKWarps);
+      mbar_init(&vready[i], kVWarps);
+      mbar_init(&sready[i], 1);
+      mbar_init(&pready[i], kSmxWarps);
+      mbar_init(&pvdone[i], 1);
+    }
+    mbar_init(qready, 4);
+    mbar_init(final_bar, 1);
+    mbar_init(lready, kSmxWarps);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 4) flags[threadIdx.x] = 0;
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= kProducerWarp) {
+    if (warp == kProducerWarp) {
+      // ---------------------------------------------------------------- TMA
+      prefetch_tmap(&tmap);
+      const int32_t *pt = a.page_table + (size_t)b * a.max_pages;
+      const int p = lane & 3;
+      auto page_for = [&](int j) -> int {
+        const int tok = tile_key(j) + p * kPageTokens;
+        if (tok >= key_hi || tok + kPageTokens <= key_lo) return -1;  // nobody sees it
+        const int pg = pt[tok / kPageTokens];
+        if (pg < 0 || pg >= a.num_pages) {
+          if (lane < kTilePages) report(a.err, NVKV_DEVERR_PAGE_ID);
+          return -1;
+        }
+        return pg;
+      };
+      int cur = ntiles > 0 ? page_for(0) : -1;
+      for (int j = 0; j < ntiles; ++j) {
+        const int stage = j % kStages;
+        const int nxt = j + 1 < ntiles ? page_for(j + 1) : -1;
+        if (j >= kStages) {
+          if (lane == 0) wait_bar(&empty[stage], ((j / kStages) + 1) & 1, flags, a.err);
+          __syncwarp();
+        }
+        const bool mine = lane < kTilePages && cur >= 0;
+        if (lane < kTilePages) spages[stage * kTilePages + lane] = cur;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * C::kHeadBytes;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+        __syncwarp();
+        if (mine)
+          tma_load_2d(stages + stage * kStageBytes + lane * kPagePitch, &tmap, 0,
+                      (cur * a.Hkv + h) * C::kRowsPerHead, &full[stage]);
+        cur = nxt;
+      }
+      // Drain: every issued copy must land before the CTA may exit.
+      if (lane == 0) {
+        const int first = ntiles > kStages ? ntiles - kStages : 0;
+        for (int k = first; k < ntiles; ++k)
+          mbar_wait(&full[k % kStages], (k / kStages) & 1, kWaitBudget);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp && lane == 0 && ntiles > 0) {
+      // ---------------------------------------------------------------- MMA
+      const uint32_t idesc_qk = idesc_f16_f32(128, kTileTokens, false, false);
+      const uint32_t idesc_pv = idesc_f16_f32(128, D, false, false);
+      const uint32_t kb = smem_u32(ktiles), vb = smem_u32(vtiles);
+      wait_bar(qready, 0, flags, a.err);
+      tc_fence_after();
+      int qk = 0, pv = 0;
+      bool issued = false;
+      long long t_last = clock64();
+      while (pv < ntiles && !flags[2]) {
+        bool progress = false;
+        if (pv < qk && mbar_test(&pready[pv & 1], (pv >> 1) & 1) &&
+            mbar_test(&vready[pv & 1], (pv >> 1) & 1)) {
+          tc_fence_after();
+          const uint32_t pcol = tmem + kColS + (pv & 1) * 64;  // P: first 32 columns of the slot
+          const uint32_t vt = vb + (pv & 1) * kVTileBytes;
+#pragma unroll
+          for (int ks = 0; ks < kTileTokens / 16; ++ks) {
+            const uint64_t bd = smem_desc(vt + ks * 2 * (D * 16), D * 16, 128);
+            mma_f16_ts(tmem + kColO, pcol + ks * 8, bd, idesc_pv, (pv > 0 || ks > 0) ? 1u : 0u);
+          }
+          mma_commit(&pvdone[pv & 1]);
+          ++pv;
+          progress = issued = true;
+        } else if (qk < ntiles && (qk < 2 || mbar_test(&pvdone[qk & 1], ((qk >> 1) + 1) & 1)) &&
+                   mbar_test(&kready[qk & 1], (qk >> 1) & 1)) {
+          tc_fence_after();
+          const uint32_t kt = kb + (qk & 1) * kKTileBytes;
+          const uint32_t scol = tmem + kColS + (qk & 1) * 64;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t bd = smem_desc(kt + ks * 2 * 1024, 1024, 128);
+            mma_f16_ts(scol, tmem + kColQ + ks * 8, bd, idesc_qk, ks > 0 ? 1u : 0u);
+          }
+          mma_commit(&sready[qk & 1]);
+          ++qk;
+          progress = issued = true;
+        }
+        if (progress) {
+          t_last = clock64();
+        } else {
+          if (clock64() - t_last > kWaitBudget) {
+            flags[2] = 1;
+            report(a.err, NVKV_DEVERR_TIMEOUT);
+          }
+          __nanosleep(kPollSleepNs);
+        }
+      }
+      if (issued) {
+        mma_commit(final_bar);
+        mbar_wait(final_bar, 0, kWaitBudget);
+      }
+    }
+  } else if (warp < kDeqWarps) {
+    if (warp < kKWarps) {
+      // ------------------------------------------------------------------ K
+      const int t = threadIdx.x;  // 0..127
+      constexpr int kChunks = D / 64;
+      // thread = token n (32 consecutive per warp), chunks kChunks * cp + ..
+      const int n = t & 63, cp = t >> 6;
+      const int p = n >> 4, s = n & 15;
+      for (int j = 0; j < ntiles; ++j) {
+        const int stage = j % kStages, slot = j & 1;
+        const uint8_t *pg = stages + stage * kStageBytes + p * kPagePitch;
+        wait_bar(&full[stage], (j / kStages) & 1, flags, a.err);
+        const int4 pgs = *reinterpret_cast<const int4 *>(spages + stage * kTilePages);
+        const int tok = tile_key(j) + n;
+        const int mine = p < 2 ? (p == 0 ? pgs.x : pgs.y) : (p == 2 ? pgs.z : pgs.w);
+        const bool ok = mine >= 0 && tok >= key_lo && tok < key_hi;
+        // The stage's bytes, before the wait for the tile slot.
+        uint4 w4[kChunks];
+        uint2 sc = make_uint2(0u, 0u);  // scale bytes of the chunks' groups (two a chunk)
+#pragma unroll
+        for (int ci = 0; ci < kChunks; ++ci) w4[ci] = make_uint4(0u, 0u, 0u, 0u);
+        if (ok) {
+          const uint8_t *sp = pg + swz(ks_off(D) + s * (D / 16) + 2 * kChunks * cp);
+          if constexpr (kChunks == 4)
+            sc = *reinterpret_cast<const uint2 *>(sp);
+          else
+            sc.x = *reinterpret_cast<const uint32_t *>(sp);
+#pragma unroll
+          for (int ci = 0; ci < kChunks; ++ci)
+            w4[ci] = *reinterpret_cast<const uint4 *>(
+                pg + swz(s * (D / 2) + (kChunks * cp + ci) * 16));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);  // this warp's reads of the stage are done
+        // K tile slot: its previous tile's scores must be done.
+        if (j >= 2) {
+          wait_bar(&sready[slot], ((j >> 1) + 1) & 1, flags, a.err);
+          tc_fence_after();
+        }
+        if (t == 0)
+          present[j & 3] = (pgs.x >= 0 ? 1u : 0u) | (pgs.y >= 0 ? 2u : 0u) |
+                           (pgs.z >= 0 ? 4u : 0u) | (pgs.w >= 0 ? 8u : 0u);
+        uint8_t *kt = ktiles + slot * kKTileBytes + (n >> 3) * 128 + (n & 7) * 16;
+#pragma unroll
+        for (int ci = 0; ci < kChunks; ++ci) {
+          const int c = kChunks * cp + ci;  // 32-d chunk: groups 2c, 2c+1
+          const uint32_t two = (ci < 2 ? sc.x : sc.y) >> (16 * (ci & 1));
+          const uint32_t s0 = dup_scale(two & 0xffu), s1 = dup_scale((two >> 8) & 0xffu);
+          const uint32_t w[4] = {w4[ci].x, w4[ci].y, w4[ci].z, w4[ci].w};
+          // K-major core matrices: element (n, k) at (k/8)*1024 + (n/8)*128 + (n%8)*16.
+#pragma unroll
+          for (int wi = 0; wi < 4; ++wi) {
+            uint32_t t4[4];
+            e2m1x8_to_f16x2x4(w[wi], t4);
+            const uint32_t s2 = wi < 2 ? s0 : s1;
+            *reinterpret_cast<uint4 *>(kt + (4 * c + wi) * 1024) =
+                make_uint4(hmul2_u32(t4[0], s2), hmul2_u32(t4[1], s2), hmul2_u32(t4[2], s2),
+                           hmul2_u32(t4[3], s2));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kready[slot]);
+      }
+    } else {
+      // ------------------------------------------------------------------ V
+      const int t = threadIdx.x - kKWarps * 32;  // 0..255
+      // thread = head_dim row d, pages p0 .. p0 + kPages - 1 of the tile
+      constexpr int kPages = D / 64;
+      const int d = t % D, p0 = D == 256 ? 0 : t / D * kPages;
+      const int g = d >> 4;
+      for (int j = 0; j < ntiles; ++j) {
+        const int stage = j % kStages, slot = j & 1;
+        const uint8_t *stg = stages + stage * kStageBytes;
+        wait_bar(&full[stage], (j / kStages) & 1, flags, a.err);
+        const int4 pg4 = *reinterpret_cast<const int4 *>(spages + stage * kTilePages);
+        const int tok0 = tile_key(j);
+        if (t < D) {
+          // This tile's V scales, converted once (the 16 V^T rows of a group
+          // share them): a thread takes 4 consecutive tokens of one (page,
+          // group). (Absent pages convert stale bytes that are never used.)
+          const int p = t / (D / 4), gg = (t >> 2) % (D / 16), q4 = t & 3;
+          const uint32_t raw = *reinterpret_cast<const uint32_t *>(
+              stg + p * kPagePitch + swz(vs_off(D) + gg * kPageTokens) + 4 * q4);
+          uint32_t t2[2];
+          e4m3x4_to_f16x2x2(raw, t2);
+          *reinterpret_cast<uint2 *>(vsc + ((slot * kTilePages + p) * (D / 16) + gg) * 8 + 2 * q4) =
+              make_uint2(t2[0], t2[1]);
+        }
+        uint2 cw[kPages];
+#pragma unroll
+        for (int pp = 0; pp < kPages; ++pp)
+          cw[pp] = *reinterpret_cast<const uint2 *>(stg + (p0 + pp) * kPagePitch +
+                                                    swz(vc_off(D) + d * 8));
+        // The scale table of this tile is complete once every V thread is
+        // here; all of them finished reading the table of tile j-2 before
+        // arriving here for tile j-1.
+        named_barrier(1, kVWarps * 32);
+        if (lane == 0) mbar_arrive(&empty[stage]);  // (the barrier follows every read)
+        // V^T tile slot: its previous tile's value MMAs must be done.
+        if (j >= 2) {
+          wait_bar(&pvdone[slot], ((j >> 1) + 1) & 1, flags, a.err);
+          tc_fence_after();
+        }
+        uint8_t *vt = vtiles + slot * kVTileBytes + (d >> 3) * 128 + (d & 7) * 16;
+#pragma unroll
+        for (int pp = 0; pp < kPages; ++pp) {
+          const int p = p0 + pp;
+          const int ptok = tok0 + p * kPageTokens;
+          const int mine = p == 0 ? pg4.x : p == 1 ? pg4.y : p == 2 ? pg4.z : pg4.w;
+          uint32_t o8[8];
+          if (mine >= 0) {
+            const uint4 *tb = reinterpret_cast<const uint4 *>(
+                vsc + ((slot * kTilePages + p) * (D / 16) + g) * 8);
+            const uint4 sa = tb[0], sb = tb[1];
+            const uint32_t sp[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+            uint32_t c0[4], c1[4];
+            e2m1x8_to_f16x2x4(cw[pp].x, c0);
+            e2m1x8_to_f16x2x4(cw[pp].y, c1);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o8[e] = hmul2_u32(e < 4 ? c0[e] : c1[e - 4], sp[e]);
+            if (ptok < key_lo || ptok + kPageTokens > key_hi) {
+              // tokens that no row sees are zero, whatever their bytes
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int t0 = ptok + 2 * e;
+                if (t0 < key_lo || t0 >= key_hi) o8[e] &= 0xffff0000u;
+                if (t0 + 1 < key_lo || t0 + 1 >= key_hi) o8[e] &= 0xffffu;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o8[e] = 0u;
+          }
+          // K-major (tokens) core matrices: element (d, t) at (t/8)*16*D + (d/8)*128 + (d%8)*16.
+          *reinterpret_cast<uint4 *>(vt + (2 * p) * (16 * D)) =
+              make_uint4(o8[0], o8[1], o8[2], o8[3]);
+          *reinterpret_cast<uint4 *>(vt + (2 * p + 1) * (16 * D)) =
+              make_uint4(o8[4], o8[5], o8[6], o8[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vready[slot]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int hf = warp >= kDeqWarps + 4;     // keys 32 * hf .. of every tile
+    const int lq = warp & 3;
+    const int r = 32 * lq + lane;             // query row of the tile
+    const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
+    const int gr = 128 * mt + r;
+    const bool valid = gr < rows && !bad;
+    const int i = gr / G, g = gr % G;
+    const int pos = kv_len - n_b + i;
+    int row_lo = 0, row_hi = 0;               // keys row_lo .. row_hi - 1 are visible
+    float slope2 = 0.f;
+    if (valid) {
+      key_range(pos, kv_len, mod.start(q0 + i), mod.window, prefix, row_lo, row_hi);
+      slope2 = mod.slope2(h * G + g);
+    }
+    // Q row -> Tensor Memory (A operand), f16, pre-scaled to base-2 scores.
+    if (hf == 0) {
+      const __nv_bfloat16 *qr = a.q + ((size_t)(q0 + i) * a.Hq + h * G + g) * D;
+#pragma unroll
+      for (int c32 = 0; c32 < D / 64; ++c32) {
+        uint32_t w[32];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          uint4 raw = make_uint4(0, 0, 0, 0);
+          if (valid) raw = *reinterpret_cast<const uint4 *>(qr + c32 * 64 + v * 8);
+          const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            __half2 hh = __floats2half2_rn(__uint_as_float(rw[e] << 16) * a.qscale,
+                                           __uint_as_float(rw[e] & 0xffff0000u) * a.qscale);
+            w[4 * v + e] = *reinterpret_cast<uint32_t *>(&hh);
+          }
+        }
+        tmem_st16(tl + kColQ + c32 * 32, w);
+        tmem_st16(tl + kColQ + c32 * 32 + 16, w + 16);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
+    }
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < ntiles; ++j) {
+      const int slot = j & 1;
+      wait_bar(&sready[slot], (j >> 1) & 1, flags, a.err);
+      __syncwarp();  // the Tensor Memory loads below are warp-collective
+      tc_fence_after();
+      const uint32_t scol = tl + kColS + slot * 64;
+      float x[kHalf];
+      auto load_scores = [&]() {
+        uint32_t(&xr)[kHalf] = reinterpret_cast<uint32_t(&)[kHalf]>(x);
+        tmem_ld16(scol + kHalf * hf, reinterpret_cast<uint32_t(&)[16]>(xr[0]));
+        tmem_ld16(scol + kHalf * hf + 16, reinterpret_cast<uint32_t(&)[16]>(xr[16]));
+        tmem_wait_ld();
+      };
+      auto top_score = [&]() {
+        float t0 = max3(x[0], x[1], x[2]), t1 = max3(x[3], x[4], x[5]);
+#pragma unroll
+        for (int e = 6; e < 30; e += 4) {
+          t0 = max3(t0, x[e], x[e + 1]);
+          t1 = max3(t1, x[e + 2], x[e + 3]);
+        }
+        return max3(t0, t1, fmaxf(x[30], x[31]));
+      };
+      load_scores();
+      const int key0 = tile_key(j) + kHalf * hf;
+      float above;  // no visible score is larger
+      if (mod.cap2 > 0.f) {
+        // A polynomial, good for scores of at most 0.75 caps and increasing
+        // beyond: its own values tell whether all of them are. Where one is
+        // not, the exact form (two special functions a score).
+        const float2 us = make_float2(mod.cap_u, mod.cap_u);
+#pragma unroll
+        for (int e = 0; e < kHalf; e += 2) {
+          const float2 v = cap_small(mod, mul_f32x2(make_float2(x[e], x[e + 1]), us));
+          x[e] = v.x, x[e + 1] = v.y;
+        }
+        float t0 = max3_abs(x[0], x[1], x[2]), t1 = max3_abs(x[3], x[4], x[5]);
+#pragma unroll
+        for (int e = 6; e < 30; e += 4) {
+          t0 = max3_abs(t0, x[e], x[e + 1]);
+          t1 = max3_abs(t1, x[e + 2], x[e + 3]);
+        }
+        above = max3_abs(t0, t1, max3_abs(x[30], x[31], 0.f));
+        if (__any_sync(0xffffffffu, !(above <= kCapSmallTanh * mod.cap2))) {  // (a NaN too)
+          load_scores();
+#pragma unroll
+          for (int e = 0; e < kHalf; ++e) x[e] = mod.cap(x[e]);
+          above = mod.cap2;
+        }
+      } else {
+        above = top_score();
+      }
+      if (mod.slopes) {
+        // (distances are exact; with a prefix a key may lie ahead)
+        const float d0 = (float)(pos - key0);
+#pragma unroll
+        for (int e = 0; e < kHalf; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), x[e]);
+        above = top_score();
+      }
+      if (key0 < row_lo || key0 + kHalf > row_hi) {
+#pragma unroll
+        for (int e = 0; e < kHalf; ++e)
+          if (key0 + e < row_lo || key0 + e >= row_hi) x[e] = -INFINITY;
+      }
+      const uint32_t here = present[j & 3] >> (2 * hf);
+      if ((here & 3u) != 3u) {
+#pragma unroll
+        for (int e = 0; e < kHalf; ++e)
+          if (!((here >> (e / kPageTokens)) & 1u)) x[e] = -INFINITY;
+      }
+      // One barrier of the two warps that share these rows: may any score
+      // pass its row's running maximum by 2^8? (Every score of the tile has
+      // been read once it is passed.)
+      if (named_barrier_or(2 + lq, 64, above > m + kLazyRescale)) {
+        // The exact maximum of the row's visible scores decides; both threads
+        // of the row come to the same result.
+        red_s[128 * hf + r] = top_score();
+        named_barrier(2 + lq, 64);
+        const float tmax = fmaxf(red_s[r], red_s[128 + r]);
+        const bool raise = tmax > -INFINITY && (m == -INFINITY || tmax > m + kLazyRescale);
+        const float alpha = raise ? exp2f(m - tmax) : 1.f;  // 0 when m = -inf
+        // The Tensor Memory loads and stores of O are warp-collective: if any
+        // row of the warp moves, the whole warp rescales its half of the
+        // columns, rows that stay with alpha 1 -- once the value MMAs up to
+        // tile j-1 are done.
+        if (j > 0 && __any_sync(0xffffffffu, raise)) {
+          wait_bar(&pvdone[(j - 1) & 1], ((j - 1) >> 1) & 1, flags, a.err);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int c16 = 0; c16 < D / 32; ++c16) {
+            uint32_t rr[16];
+            const uint32_t col = tl + kColO + hf * (D / 2) + c16 * 16;
+            tmem_ld16(col, rr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
+            tmem_st16(col, rr);
+          }
+          tmem_wait_st();
+        }
+        if (raise) {
+          l *= alpha;
+          m = tmax;
+        }
+        named_barrier(2 + lq, 64);  // the maxima have been read
+      }
+      // Weights in f16, two per exponential instruction; masked keys are
+      // -inf and give 0 (a row with no visible key yet keeps m = -inf: it
+      // subtracts 0 instead). The denominator sums the same f16 weights.
+      const float ms = m == -INFINITY ? 0.f : m;
+      uint32_t pw[kHalf / 2];
+      float2 lv0 = make_float2(0.f, 0.f), lv1 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < kHalf / 2; ++e) {
+        float2 w;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.x) : "f"(x[2 * e] - ms));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.y) : "f"(x[2 * e + 1] - ms));
+        asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(pw[e]) : "f"(w.x), "f"(w.y));
+        (e & 1 ? lv1 : lv0) = add_f32x2(e & 1 ? lv1 : lv0, w);
+      }
+      l += (lv0.x + lv0.y) + (lv1.x + lv1.y);
+      // P overwrites the first 32 columns of its own S slot.
+      tmem_st16(scol + kHalf / 2 * hf, pw);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pready[slot]);
+    }
+    l_s[128 * hf + r] = l;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(lready);
+    // Split partial: O / l (fp32) and lse = m + log2(l), -inf without a
+    // visible key, in the split's plane of total_q * Hq rows.
+    if (a.ws_o && hf == 0) {
+      wait_bar(lready, 0, flags, a.err);
+      const float both = l_s[r] + l_s[128 + r];
+      if (gr < rows && rows_ok)
+        a.ws_lse[(size_t)split * a.total_q * a.Hq + (size_t)(q0 + i) * a.Hq + h * G + g] =
+            both > 0.f ? m + log2f(both) : -INFINITY;
+    }
+  }
+
+  if (warp >= kKWarps && warp < kProducerWarp) {
+    // ------------------------------------------------------------- epilogue
+    // O / l -> out (or the split's plane), 16 warps: lane quarter warp % 4,
+    // quarter warp / 4 of the columns.
+    if (ntiles > 0) {
+      wait_bar(final_bar, 0, flags, a.err);
+      __syncwarp();
+      tc_fence_after();
+    }
+    wait_bar(lready, 0, flags, a.err);
+    const int lq = warp & 3, part = (warp - kKWarps) >> 2;
+    const int r = 32 * lq + lane;
+    const int gr = 128 * mt + r;
+    const int i = gr / G, g2 = gr % G;
+    const bool write = gr < rows && rows_ok;
+    const float l = l_s[r] + l_s[128 + r];
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const size_t orow = (size_t)(q0 + i) * a.Hq + h * G + g2;
+    const size_t plane = (size_t)split * a.total_q * a.Hq;
+    const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16) + kColO + part * (D / 4);
+#pragma unroll
+    for (int c16 = 0; c16 < D / 64; ++c16) {
+      uint32_t rr[16];
+      if (ntiles > 0) {
+        __syncwarp();
+        tmem_ld16(tl + c16 * 16, rr);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) rr[e] = 0u;
+      }
+      if (!write) continue;
+      const int col = part * (D / 4) + c16 * 16;
+      if (a.ws_o) {
+        float4 *dst = reinterpret_cast<float4 *>(a.ws_o + (plane + orow) * D + col);
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4)
+          dst[e4] = make_float4(__uint_as_float(rr[4 * e4]) * inv,
+                                __uint_as_float(rr[4 * e4 + 1]) * inv,
+                                __uint_as_float(rr[4 * e4 + 2]) * inv,
+                                __uint_as_float(rr[4 * e4 + 3]) * inv);
+      } else {
+        uint32_t ow[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(rr[2 * e]) * inv,
+                                                    __uint_as_float(rr[2 * e + 1]) * inv);
+          ow[e] = *reinterpret_cast<uint32_t *>(&b2);
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + col);
+        dst[0] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+        dst[1] = make_uint4(ow[4], ow[5], ow[6], ow[7]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Merge of the key splits: row (token q0 + i, head hq) of sequence b is
+// sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M) with M the largest lse (zero
+// when no split saw a key). One warp per row, D/32 elements a lane. Set up
+// while the attention kernel runs (programmatic dependent launch).
+constexpr int kMaxSplits = 8;
+constexpr int kMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+prefill_mod_merge_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_lse,
+                         int num_splits, const int32_t *__restrict__ cu_q, int total_q, int Hq,
+                         int G, int row_cap, __nv_bfloat16 *__restrict__ out) {
+  const int b = blockIdx.y;
+  const int q0 = cu_q[b], n_b = cu_q[b + 1] - q0;
+  if (n_b <= 0 || q0 < 0 || q0 + n_b > total_q) return;  // no output rows (as in the attention)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t idx = (int64_t)blockIdx.x * kMergeWarps + warp;  // token idx / Hq, head idx % Hq
+  if (idx >= (int64_t)n_b * Hq) return;
+  // only the rows the attention grid covers (tile rows i*G + g < row_cap)
+  if ((idx / Hq) * G + (idx % Hq) % G >= row_cap) return;
+  const size_t row = (size_t)q0 * Hq + idx;
+  const size_t plane = (size_t)total_q * Hq;
+  grid_dependency_wait();
+  float lse[kMaxSplits], mx = -INFINITY;
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) {
+    lse[s] = s < num_splits ? ws_lse[s * plane + row] : -INFINITY;
+    mx = fmaxf(mx, lse[s]);
+  }
+  constexpr int kE = D / 32;  // elements of a lane: 4 or 8
+  float acc[kE], wsum = 0.f;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
+  if (mx > -INFINITY) {
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s) {
+      if (s < num_splits && lse[s] > -INFINITY) {
+        const float w = exp2f(lse[s] - mx);
+        const float4 *src =
+            reinterpret_cast<const float4 *>(ws_o + (s * plane + row) * D + kE * lane);
+#pragma unroll
+        for (int i = 0; i < kE / 4; ++i) {
+          const float4 v = src[i];
+          acc[4 * i] += w * v.x, acc[4 * i + 1] += w * v.y;
+          acc[4 * i + 2] += w * v.z, acc[4 * i + 3] += w * v.w;
+        }
+        wsum += w;
+      }
+    }
+  }
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  uint32_t ow[kE / 2];
+#pragma unroll
+  for (int e = 0; e < kE / 2; ++e) {
+    __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    ow[e] = *reinterpret_cast<uint32_t *>(&b2);
+  }
+  __nv_bfloat16 *dst = out + row * D + kE * lane;
+  if constexpr (kE == 8)
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+  else
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(ow[0], ow[1]);
+}
+
+template <int D>
+cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, const int32_t *cu_q,
+                     int total_q, int max_q, int Hq, float sm_scale, void *out, int num_splits,
+                     float *ws_o, float *ws_lse, cudaStream_t stream, const ScoreMod &mod) {
+  CUtensorMap map;
+  if (!make_pool_tmap(c, &map)) return cudaErrorNotSupported;
+  const int G = Hq / c.num_kv_heads;
+  const int mtiles = (int)(((int64_t)max_q * G + 127) / 128);
+  constexpr int smem = Cfg<D>::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(prefill_mod_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  Args a;
+  a.num_pages = c.num_pages, a.Hkv = c.num_kv_heads;
+  a.page_table = s.page_table, a.max_pages = s.max_pages_per_seq;
+  a.kv_lens = s.kv_lens, a.max_kv_len = s.max_kv_len;
+  a.q = static_cast<const __nv_bfloat16 *>(q), a.cu_q = cu_q;
+  a.total_q = total_q, a.Hq = Hq, a.qscale = sm_scale * kLog2e;
+  a.out = static_cast<__nv_bfloat16 *>(out);
+  a.num_splits = num_splits;
+  a.ws_o = num_splits > 1 ? ws_o : nullptr, a.ws_lse = ws_lse;
+  a.err = s.err_word;
+  const dim3 grid((unsigned)(mtiles * num_splits), (unsigned)c.num_kv_heads, (unsigned)s.batch);
+  prefill_mod_kernel<D><<<grid, kThreads, smem, stream>>>(map, a, mod);
+  if ((e = cudaGetLastError()) != cudaSuccess || num_splits == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((int64_t)max_q * Hq + kMergeWarps - 1) / kMergeWarps),
+                     (unsigned)s.batch);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_mod_merge_kernel<D>, (const float *)ws_o,
+                            (const float *)ws_lse, num_splits, cu_q, total_q, Hq, G, 128 * mtiles,
+                            static_cast<__nv_bfloat16 *>(out));
+}
+
+}  // namespace
+
+// Key splits of a call: the count in 1 .. 8 with the least estimated time. A
+// CTA takes about kSetup tiles' time before its first and after its last
+// tile; n CTAs a split run in ceil(n S / SMs) waves; the merge reads S fp32
+// planes of the output and writes one of bf16 (kMergeBytes a tile's time).
+// Keys from documents (key_starts) are not known here: splits then only fill
+// the first wave.
+int prefill_mod_auto_splits(const nvkv_cache &c, const nvkv_seqs &s, int total_q, int max_q,
+                            int Hq, const ScoreMod &mod, int sms) {
+  constexpr double kSetup = 6.0, kMergeBytes = 6.0e6;
+  const int G = Hq / c.num_kv_heads;
+  const int64_t n = ((int64_t)max_q * G + 127) / 128 * c.num_kv_heads * s.batch;
+  int64_t keys = s.max_kv_len;
+  if (mod.window > 0 && keys > (int64_t)mod.window + 128 / G)
+    keys = (int64_t)mod.window + 128 / G;  // (a prefix may add to it)
+  const int64_t tiles = (keys + kTileTokens - 1) / kTileTokens + (mod.window > 0 ? 1 : 0);
+  int best = 1;
+  double least = 0;
+  for (int S = 1; S <= kMaxSplits; ++S) {
+    if (S > 1 && mod.starts && n * S > sms) break;
+    const double waves = (double)((n * S + sms - 1) / sms);
+    double cost = waves * (kSetup + (double)((tiles + S - 1) / S));
+    if (S > 1)
+      cost += 2.0 + (double)total_q * Hq * c.head_dim * (8.0 * S + 2.0) / kMergeBytes;
+    if (S == 1 || cost < least) best = S, least = cost;
+  }
+  return best;
+}
+
+cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
+                               const int32_t *cu_q, int total_q, int max_q, int Hq,
+                               float sm_scale, void *out, int num_splits, float *ws_o,
+                               float *ws_lse, cudaStream_t stream, const ScoreMod &mod) {
+  if (num_splits < 1 || num_splits > kMaxSplits || (num_splits > 1 && (!ws_o || !ws_lse)))
+    return cudaErrorInvalidValue;
+  return c.head_dim == 256 ? launch_d<256>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
+                                           num_splits, ws_o, ws_lse, stream, mod)
+                           : launch_d<128>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
+                                           num_splits, ws_o, ws_lse, stream, mod);
+}
+
+}  // namespace nvkv

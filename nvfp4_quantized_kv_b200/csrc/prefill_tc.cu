@@ -1,6 +1,5 @@
 // prefill_tc.cu -- chunked-prefill attention over the NVFP4 paged pool on the
-// 5th-generation tensor cores (tcgen05): head_dim 256, and 128 with a
-// ScoreMod (the comments' sizes are those of head_dim 256).
+// 5th-generation tensor cores (tcgen05), head_dim 256.
 //
 // Computes the chunked prefill of the "knoopx/ninfer" README, "Capabilities
 // and limits": the n_b newest positions of a sequence (their K/V rows already
@@ -26,7 +25,7 @@
 //    running max (raised lazily, only when it grows by more than 2^8, then O
 //    is rescaled), the denominator of the f16 weights, and the final O / l.
 //  * One thread issues the MMAs, event-driven; every wait is bounded.
-#include "score_mod.cuh"
+#include "nvkv_common.cuh"
 #include "sm100.cuh"
 
 namespace nvkv {
@@ -37,9 +36,16 @@ namespace {
 
 using namespace sm100;
 
+constexpr int kD = 256;
+constexpr int kRowsPerHead = 36;
+constexpr int kHeadBytes = 18 * kD;
+constexpr int kPagePitch = 5120;
 constexpr int kTileTokens = 64;
 constexpr int kTilePages = 4;
 constexpr int kStages = 4;
+constexpr int kStageBytes = kTilePages * kPagePitch;   // 20 KB
+constexpr int kKTileBytes = kTileTokens * kD * 2;      // 32 KB
+constexpr int kVTileBytes = kD * kTileTokens * 2;      // 32 KB
 constexpr int kDeqWarps = 8;                           // warps 0..7
 constexpr int kSmxWarp0 = 8;                           // warps 8..11
 constexpr int kSmxWarps = 4;
@@ -59,37 +65,19 @@ constexpr uint32_t kColQ = 0;     // 128: Q (row lanes, d pairs)
 constexpr uint32_t kColS = 128;   // 2 x 64: S slots (P overwrites the first 32 columns)
 constexpr uint32_t kColO = 256;   // 256: O (row lanes, fp32 d)
 
-// Sizes and shared memory by head_dim.  A page's kv-head block is staged as
-// 128-byte rows with the 128-byte TMA swizzle: byte `off` of the block lies
-// at swz(off).
-template <int D>
-struct Cfg {
-  static_assert(D == 128 || D == 256, "head_dim");
-  static constexpr int kHeadBytes = 18 * D;
-  static constexpr int kRowsPerHead = kHeadBytes / 128;
-  static constexpr int kPagePitch = (kHeadBytes + 1023) / 1024 * 1024;
-  static constexpr int kStageBytes = kTilePages * kPagePitch;       // 20 KB
-  static constexpr int kKTileBytes = kTileTokens * D * 2;           // 32 KB
-  static constexpr int kVTileBytes = D * kTileTokens * 2;           // 32 KB
-  static constexpr int kOffK = kStages * kStageBytes;
-  static constexpr int kOffV = kOffK + 2 * kKTileBytes;
-  // V scales of a tile as f16 pairs [page][group][8], two tables (tile parity)
-  static constexpr int kVscBytes = kTilePages * (D / 16) * 8 * 4;
-  static constexpr int kOffVsc = kOffV + 2 * kVTileBytes;
-  static constexpr int kOffPages = kOffVsc + 2 * kVscBytes;         // int[stages][4]
-  static constexpr int kOffPres = kOffPages + kStages * kTilePages * 4;  // u32[4] (ScoreMod only)
-  static constexpr int kOffFlags = kOffPres + 16;
-  static constexpr int kOffBars = kOffFlags + 16;
-  // full, empty; kready, vready, sready, pready, pvdone; qready, final
-  static constexpr int kNumBars = 2 * kStages + 2 * 5 + 2;
-  static constexpr int kOffTmem = kOffBars + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffTmem + 16 + 1024;
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-  static_assert(kOffK % 1024 == 0 && kOffPages % 16 == 0 && kOffBars % 8 == 0, "alignment");
-};
-
-// Where the 128-byte TMA swizzle puts byte `off` of a page block.
-__device__ __forceinline__ int swz(int off) { return off ^ ((off >> 3) & 0x70); }
+// Shared memory.
+constexpr int kOffK = kStages * kStageBytes;
+constexpr int kOffV = kOffK + 2 * kKTileBytes;
+constexpr int kVscBytes = kTilePages * 16 * 8 * 4;            // V scales of a tile as f16 pairs
+constexpr int kOffVsc = kOffV + 2 * kVTileBytes;              // 2 tables (tile parity)
+constexpr int kOffPages = kOffVsc + 2 * kVscBytes;            // int[stages][4]
+constexpr int kOffFlags = kOffPages + kStages * kTilePages * 4;
+constexpr int kOffBars = kOffFlags + 16;
+constexpr int kNumBars = 2 * kStages + 2 * 5 + 2;  // full, empty; kready, vready, sready, pready, pvdone; qready, final
+constexpr int kOffTmem = kOffBars + kNumBars * 8;
+constexpr int kSmemBytes = kOffTmem + 16 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+static_assert(kOffK % 1024 == 0 && kOffPages % 16 == 0 && kOffBars % 8 == 0, "alignment");
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *flags,
                                          int32_t *err) {
@@ -100,7 +88,6 @@ __device__ __forceinline__ uint32_t dup_scale(uint32_t byte) {
   return e4m3x2_to_f16x2(byte | (byte << 8));
 }
 
-template <int D, class Mod>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hkv,
                   const int32_t *__restrict__ page_table, int max_pages,
@@ -108,11 +95,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
                   const __nv_bfloat16 *__restrict__ q, const int32_t *__restrict__ cu_q,
                   int total_q, int Hq, float qscale, __nv_bfloat16 *__restrict__ out,
                   int num_splits, float *__restrict__ ws_o, float *__restrict__ ws_lse,
-                  int32_t *err, Mod mod) {
-  using C = Cfg<D>;
-  constexpr int kHeadBytes = C::kHeadBytes, kRowsPerHead = C::kRowsPerHead,
-                kPagePitch = C::kPagePitch, kStageBytes = C::kStageBytes,
-                kKTileBytes = C::kKTileBytes, kVTileBytes = C::kVTileBytes;
+                  int32_t *err) {
   // blockIdx.x = m-tile * num_splits + split: split s of an m-tile takes the
   // s-th of num_splits equal runs of its key tiles and, when num_splits > 1,
   // leaves O / l and log2(l) + m of its rows in the workspace for the merge.
@@ -128,40 +111,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
                    kv_len > max_kv_len || kv_len > max_pages * kPageTokens;
   const int i_first = (128 * mt) / G;
   const int i_last = min(n_b - 1, (128 * mt + 127) / G);
-  int pos_last = kv_len - n_b + i_last;     // keys 0 .. pos_last are needed
-  int key_lo = 0;                           // (ScoreMod: keys key_lo .. pos_last)
-  if constexpr (Mod::kOn) {
-    // The union of the rows' intervals: every warp scans all rows.
-    int lo = 0x7fffffff, hi = 0;
-    if (!bad) {
-      const int prefix = mod.prefix_of(b);
-      for (int i = i_first + (threadIdx.x & 31); i <= i_last; i += 32) {
-        int l, h2;
-        key_range(kv_len - n_b + i, kv_len, mod.start(q0 + i), mod.window, prefix, l, h2);
-        if (l < h2) lo = min(lo, l), hi = max(hi, h2);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    key_lo = min(lo, hi);  // (hi = 0: nothing is seen)
-    pos_last = hi - 1;
-  }
-  const int tile_lo = key_lo / kTileTokens;
-  const int ntiles_all =
-      bad || pos_last < key_lo ? 0 : pos_last / kTileTokens + 1 - tile_lo;
+  const int pos_last = kv_len - n_b + i_last;     // keys 0 .. pos_last are needed
+  const int ntiles_all = bad ? 0 : pos_last / kTileTokens + 1;
   // This CTA's key tiles j0 .. j0 + ntiles - 1; every ring and barrier below
   // counts from its first tile.
   const int j0 = (int)((int64_t)split * ntiles_all / num_splits);
   const int ntiles = (int)((int64_t)(split + 1) * ntiles_all / num_splits) - j0;
-  // First key of the CTA's j-th tile.  The masked attention goes from the
-  // newest tile to the oldest: with a distance bias the largest scores come
-  // first and the running maximum is not raised again in every tile.
-  auto tile_key = [&](int j) {
-    return (Mod::kOn ? tile_lo + ntiles_all - 1 - (j0 + j) : j0 + j) * kTileTokens;
-  };
   // Output rows exist only when the chunk lies inside the total_q rows.
   const bool rows_ok = n_b >= 0 && q0 >= 0 && q0 + n_b <= total_q;
 
@@ -169,22 +124,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
   uint8_t *stages = smem;
-  uint8_t *ktiles = smem + C::kOffK;
-  uint8_t *vtiles = smem + C::kOffV;
-  uint32_t *vsc = reinterpret_cast<uint32_t *>(smem + C::kOffVsc);  // [2][page][group][8]
-  int32_t *spages = reinterpret_cast<int32_t *>(smem + C::kOffPages);
-  // ScoreMod: bit p of entry (tile & 3) is set when page p of the tile is
-  // present, so the softmax leaves the keys of an absent page out.  Written
-  // with the tile's K; the K of tile j + 4 is written after the scores of
-  // tile j + 2, which wait for the value MMAs of tile j.
-  volatile uint32_t *present = reinterpret_cast<volatile uint32_t *>(smem + C::kOffPres);
-  volatile int *flags = reinterpret_cast<volatile int *>(smem + C::kOffFlags);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBars);
+  uint8_t *ktiles = smem + kOffK;
+  uint8_t *vtiles = smem + kOffV;
+  uint32_t *vsc = reinterpret_cast<uint32_t *>(smem + kOffVsc);  // [2][page][group][8]
+  int32_t *spages = reinterpret_cast<int32_t *>(smem + kOffPages);
+  volatile int *flags = reinterpret_cast<volatile int *>(smem + kOffFlags);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBars);
   uint64_t *full = bars, *empty = bars + kStages;
   uint64_t *kready = bars + 2 * kStages, *vready = kready + 2, *sready = kready + 4,
            *pready = kready + 6, *pvdone = kready + 8, *qready = kready + 10,
            *final_bar = kready + 11;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffTmem);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffTmem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (bad && threadIdx.x == 0) report(err, NVKV_DEVERR_LENGTH);
@@ -220,9 +170,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
     prefetch_tmap(&tmap);
     const int p = lane & 3;
     auto page_for = [&](int j) -> int {
-      const int tok = tile_key(j) + p * kPageTokens;
+      const int tok = j * kTileTokens + p * kPageTokens;
       if (tok > pos_last) return -1;  // keys past the last query are never needed
-      if (Mod::kOn && tok + kPageTokens <= key_lo) return -1;
       const int pg = pt[tok / kPageTokens];
       if (pg < 0 || pg >= num_pages) {
         if (lane < kTilePages) report(err, NVKV_DEVERR_PAGE_ID);
@@ -230,10 +179,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
       }
       return pg;
     };
-    int cur = ntiles > 0 ? page_for(0) : -1;
+    int cur = ntiles > 0 ? page_for(j0) : -1;
     for (int j = 0; j < ntiles; ++j) {
       const int stage = j % kStages;
-      const int nxt = j + 1 < ntiles ? page_for(j + 1) : -1;
+      const int nxt = j + 1 < ntiles ? page_for(j0 + j + 1) : -1;
       if (j >= kStages) {
         if (lane == 0) wait_bar(&empty[stage], ((j / kStages) + 1) & 1, flags, err);
         __syncwarp();
@@ -259,7 +208,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
     // ------------------------------------------------------------------ MMA
     if (lane == 0 && ntiles > 0) {
       const uint32_t idesc_qk = idesc_f16_f32(128, kTileTokens, false, false);
-      const uint32_t idesc_pv = idesc_f16_f32(128, D, false, false);
+      const uint32_t idesc_pv = idesc_f16_f32(128, kD, false, false);
       const uint32_t kb = smem_u32(ktiles), vb = smem_u32(vtiles);
       wait_bar(qready, 0, flags, err);
       tc_fence_after();
@@ -275,7 +224,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
           const uint32_t vt = vb + (pv & 1) * kVTileBytes;
 #pragma unroll
           for (int ks = 0; ks < kTileTokens / 16; ++ks) {
-            const uint64_t bd = smem_desc(vt + ks * 2 * (D * 16), D * 16, 128);
+            const uint64_t bd = smem_desc(vt + ks * 2 * 4096, 4096, 128);
             mma_f16_ts(tmem + kColO, pcol + ks * 8, bd, idesc_pv, (pv > 0 || ks > 0) ? 1u : 0u);
           }
           mma_commit(&pvdone[pv & 1]);
@@ -288,7 +237,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
           const uint32_t kt = kb + (qk & 1) * kKTileBytes;
           const uint32_t scol = tmem + kColS + (qk & 1) * 64;
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
+          for (int ks = 0; ks < kD / 16; ++ks) {
             const uint64_t bd = smem_desc(kt + ks * 2 * 1024, 1024, 128);
             mma_f16_ts(scol, tmem + kColQ + ks * 8, bd, idesc_qk, ks > 0 ? 1u : 0u);
           }
@@ -322,17 +271,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
       wait_bar(&full[stage], (j / kStages) & 1, flags, err);
       const int4 pg4 = *reinterpret_cast<const int4 *>(spages + stage * kTilePages);
       const int pgs[4] = {pg4.x, pg4.y, pg4.z, pg4.w};
-      const int tok0 = tile_key(j);
-      if (D == 256 || t < D) {
+      const int tok0 = (j0 + j) * kTileTokens;
+      {
         // This tile's V scales, converted once: thread t takes 4 consecutive
         // tokens of one (page, group); the 16 V^T rows of a group share them.
         // (Absent pages convert stale bytes that are never used.)
-        const int p = t / (D / 4), g = (t >> 2) % (D / 16), q4 = t & 3;
+        const int p = t >> 6, g = (t >> 2) & 15, q4 = t & 3;
+        const int srow = 34 + (g >> 3);
         const uint32_t raw = *reinterpret_cast<const uint32_t *>(
-            stg + p * kPagePitch + swz(vs_off(D) + g * kPageTokens) + 4 * q4);
+            stg + p * kPagePitch + srow * 128 + (((g & 7) ^ (srow & 7)) << 4) + 4 * q4);
         uint32_t t2[2];
         e4m3x4_to_f16x2x2(raw, t2);
-        *reinterpret_cast<uint2 *>(vsc + ((slot * kTilePages + p) * (D / 16) + g) * 8 + 2 * q4) =
+        *reinterpret_cast<uint2 *>(vsc + ((slot * kTilePages + p) * 16 + g) * 8 + 2 * q4) =
             make_uint2(t2[0], t2[1]);
       }
       // K tile slot: its previous tile's QK must be done.
@@ -340,30 +290,24 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
         wait_bar(&sready[slot], ((j >> 1) + 1) & 1, flags, err);
         tc_fence_after();
       }
-      if (Mod::kOn && t == 0)
-        present[j & 3] = (pgs[0] >= 0 ? 1u : 0u) | (pgs[1] >= 0 ? 2u : 0u) |
-                         (pgs[2] >= 0 ? 4u : 0u) | (pgs[3] >= 0 ? 8u : 0u);
       {
-        // thread = token n (32 consecutive per warp), D/128 chunks of 32 d
-        constexpr int kChunks = D / 128;
+        // thread = token n (32 consecutive per warp), two 32-d chunks
         const int n = t & 63, cp = t >> 6;
         const int p = n >> 4, s = n & 15;
-        const bool ok = pgs[p] >= 0 && tok0 + n <= pos_last && (!Mod::kOn || tok0 + n >= key_lo);
+        const bool ok = pgs[p] >= 0 && tok0 + n <= pos_last;
         const uint8_t *pg = stg + p * kPagePitch;
-        uint32_t sc = 0;  // scale bytes of the chunks' groups (two a chunk)
-        if (ok) {
-          const uint8_t *sp = pg + swz(ks_off(D) + s * (D / 16) + 2 * kChunks * cp);
-          sc = kChunks == 2 ? *reinterpret_cast<const uint32_t *>(sp)
-                            : *reinterpret_cast<const uint16_t *>(sp);
-        }
+        uint32_t sc = 0;  // scale bytes of groups 4cp .. 4cp+3
+        if (ok)
+          sc = *reinterpret_cast<const uint32_t *>(pg + (16 + (s >> 3)) * 128 +
+                                                   (((s & 7) ^ (s >> 3)) << 4) + 4 * cp);
         uint8_t *kt = ktiles + slot * kKTileBytes + (n >> 3) * 128 + (n & 7) * 16;
 #pragma unroll
-        for (int ci = 0; ci < kChunks; ++ci) {
-          const int c = kChunks * cp + ci;  // 32-d chunk: groups 2c, 2c+1
+        for (int ci = 0; ci < 2; ++ci) {
+          const int c = 2 * cp + ci;  // 32-d chunk: groups 2c, 2c+1
           uint32_t words[16];
           if (ok) {
             const uint4 w4 =
-                *reinterpret_cast<const uint4 *>(pg + swz(s * (D / 2) + c * 16));
+                *reinterpret_cast<const uint4 *>(pg + s * 128 + ((c ^ (s & 7)) << 4));
             const uint32_t s0 = dup_scale((sc >> (16 * ci)) & 0xffu);
             const uint32_t s1 = dup_scale((sc >> (16 * ci + 8)) & 0xffu);
             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -398,21 +342,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
         tc_fence_after();
       }
       {
-        // thread = head_dim row d, D/64 of the tile's pages
-        constexpr int kPages = D / 64;
-        const int d = t % D;
+        const int d = t;  // head_dim row
         const int g = d >> 4;
+        const int vrow = 18 + (d >> 4);
+        const int vchunk = ((d & 15) >> 1) ^ (vrow & 7);
         uint8_t *vt = vtiles + slot * kVTileBytes + (d >> 3) * 128 + (d & 7) * 16;
 #pragma unroll
-        for (int pp = 0; pp < kPages; ++pp) {
-          const int p = (D == 256 ? 0 : t / D * kPages) + pp;
+        for (int p = 0; p < kTilePages; ++p) {
           const int ptok = tok0 + p * kPageTokens;
           uint32_t o8[8];
-          if ((D == 256 ? pgs[pp] : t < D ? pgs[pp] : pgs[(pp + kPages) & 3]) >= 0) {
+          if (pgs[p] >= 0) {
             const uint8_t *pg = stg + p * kPagePitch;
-            const uint2 cw = *reinterpret_cast<const uint2 *>(pg + swz(vc_off(D) + d * 8));
-            const uint4 *tb = reinterpret_cast<const uint4 *>(
-                vsc + ((slot * kTilePages + p) * (D / 16) + g) * 8);
+            const uint2 cw =
+                *reinterpret_cast<const uint2 *>(pg + vrow * 128 + vchunk * 16 + (d & 1) * 8);
+            const uint4 *tb =
+                reinterpret_cast<const uint4 *>(vsc + ((slot * kTilePages + p) * 16 + g) * 8);
             const uint4 sa = tb[0], sb = tb[1];
             const uint32_t sp[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
             uint32_t c0[4], c1[4];
@@ -428,22 +372,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
                 else if (t0 + 1 > pos_last) o8[i] &= 0xffffu;
               }
             }
-            if (Mod::kOn && ptok < key_lo) {  // and those before the first visible key
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int t0 = ptok + 2 * i;
-                if (t0 + 1 < key_lo) o8[i] = 0u;
-                else if (t0 < key_lo) o8[i] &= 0xffff0000u;
-              }
-            }
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) o8[i] = 0u;
           }
-          // K-major (tokens) core matrices: element (d, t) at (t/8)*16*D + (d/8)*128 + (d%8)*16.
-          *reinterpret_cast<uint4 *>(vt + (2 * p) * (16 * D)) =
-              make_uint4(o8[0], o8[1], o8[2], o8[3]);
-          *reinterpret_cast<uint4 *>(vt + (2 * p + 1) * (16 * D)) =
+          // K-major (tokens) core matrices: element (d, t) at (t/8)*4096 + (d/8)*128 + (d%8)*16.
+          *reinterpret_cast<uint4 *>(vt + (2 * p) * 4096) = make_uint4(o8[0], o8[1], o8[2], o8[3]);
+          *reinterpret_cast<uint4 *>(vt + (2 * p + 1) * 4096) =
               make_uint4(o8[4], o8[5], o8[6], o8[7]);
         }
       }
@@ -463,19 +398,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
     const bool valid = gr < rows && !bad;
     const int i = gr / G, g = gr % G;
     const int pos = kv_len - n_b + i;        // keys 0 .. pos are visible
-    int row_lo = 0, row_hi = 0;              // (ScoreMod: keys row_lo .. row_hi - 1)
-    float slope2 = 0.f;
-    if constexpr (Mod::kOn) {
-      if (valid) {
-        key_range(pos, kv_len, mod.start(q0 + i), mod.window, mod.prefix_of(b), row_lo, row_hi);
-        slope2 = mod.slope2(h * G + g);
-      }
-    }
     // Q row -> Tensor Memory (A operand), f16, pre-scaled to base-2 scores.
     {
-      const __nv_bfloat16 *qr = q + ((size_t)(q0 + i) * Hq + h * G + g) * D;
+      const __nv_bfloat16 *qr = q + ((size_t)(q0 + i) * Hq + h * G + g) * kD;
 #pragma unroll
-      for (int c32 = 0; c32 < D / 64; ++c32) {
+      for (int c32 = 0; c32 < 4; ++c32) {
         uint32_t w[32];
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
@@ -520,33 +447,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
           x[48 + e] = __uint_as_float(r3[e]);
         }
       }
-      const int key0 = tile_key(j);
+      const int key0 = (j0 + j) * kTileTokens;
       float tmax = -INFINITY;
-      if constexpr (Mod::kOn) {
-        if (mod.cap2 > 0.f) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e) x[e] = mod.cap(x[e]);
-        }
-        if (mod.slopes) {
-          // (distances are exact; with a prefix a key may lie ahead)
-          const float d0 = (float)(pos - key0);
-#pragma unroll
-          for (int e = 0; e < 64; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), x[e]);
-        }
-        if (key0 < row_lo || key0 + kTileTokens > row_hi) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (key0 + e < row_lo || key0 + e >= row_hi) x[e] = -INFINITY;
-        }
-        const uint32_t here = present[j & 3];
-        if (here != 15u) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (!((here >> (e / kPageTokens)) & 1u)) x[e] = -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 64; ++e) tmax = fmaxf(tmax, x[e]);
-      } else if (valid && key0 + kTileTokens - 1 <= pos) {
+      if (valid && key0 + kTileTokens - 1 <= pos) {
 #pragma unroll
         for (int e = 0; e < 64; ++e) tmax = fmaxf(tmax, x[e]);
       } else {
@@ -567,7 +470,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
         __syncwarp();
         tc_fence_after();
 #pragma unroll 1
-        for (int c16 = 0; c16 < D / 16; ++c16) {
+        for (int c16 = 0; c16 < kD / 16; ++c16) {
           uint32_t rr[16];
           tmem_ld16(tl + kColO + c16 * 16, rr);
           tmem_wait_ld();
@@ -616,7 +519,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
     const size_t plane = (size_t)split * total_q * Hq;
     if (ws_o && write) ws_lse[plane + orow_idx] = l > 0.f ? m + log2f(l) : -INFINITY;
 #pragma unroll 1
-    for (int c16 = 0; c16 < D / 16; ++c16) {
+    for (int c16 = 0; c16 < kD / 16; ++c16) {
       uint32_t rr[16];
       if (ntiles > 0) {
         tmem_ld16(tl + kColO + c16 * 16, rr);
@@ -627,7 +530,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
       }
       if (!write) continue;
       if (ws_o) {
-        float4 *dst = reinterpret_cast<float4 *>(ws_o + (plane + orow_idx) * D + c16 * 16);
+        float4 *dst = reinterpret_cast<float4 *>(ws_o + (plane + orow_idx) * kD + c16 * 16);
 #pragma unroll
         for (int e4 = 0; e4 < 4; ++e4)
           dst[e4] = make_float4(__uint_as_float(rr[4 * e4]) * inv, __uint_as_float(rr[4 * e4 + 1]) * inv,
@@ -641,7 +544,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
                                                     __uint_as_float(rr[2 * e + 1]) * inv);
           ow[e] = *reinterpret_cast<uint32_t *>(&b2);
         }
-        __nv_bfloat16 *orow = out + orow_idx * D;
+        __nv_bfloat16 *orow = out + orow_idx * kD;
         *reinterpret_cast<uint4 *>(orow + c16 * 16) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
         *reinterpret_cast<uint4 *>(orow + c16 * 16 + 8) = make_uint4(ow[4], ow[5], ow[6], ow[7]);
       }
@@ -657,11 +560,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int H
 // Merge of the key splits: row (token q0 + i, head hq) of sequence b is
 // sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M) with M the largest lse (the
 // log-sum-exp combination of partial softmax results; zero when no split saw
-// a key).  One warp per row, D/32 head_dim elements per lane.
+// a key).  One warp per row, 8 head_dim elements per lane.
 constexpr int kMaxSplits = 8;
 constexpr int kMergeWarps = 8;
 
-template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 prefill_merge_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_lse,
                      int num_splits, const int32_t *__restrict__ cu_q, int total_q, int Hq,
@@ -682,46 +584,33 @@ prefill_merge_kernel(const float *__restrict__ ws_o, const float *__restrict__ w
     lse[s] = s < num_splits ? ws_lse[s * plane + row] : -INFINITY;
     mx = fmaxf(mx, lse[s]);
   }
-  constexpr int kE = D / 32;  // elements of a lane: 4 or 8
-  float acc[kE], wsum = 0.f;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, wsum = 0.f;
   if (mx > -INFINITY) {
 #pragma unroll
     for (int s = 0; s < kMaxSplits; ++s) {
       if (s < num_splits && lse[s] > -INFINITY) {
         const float w = exp2f(lse[s] - mx);
-        const float4 *src = reinterpret_cast<const float4 *>(ws_o + (s * plane + row) * D + kE * lane);
-#pragma unroll
-        for (int i = 0; i < kE / 4; ++i) {
-          const float4 a = src[i];
-          acc[4 * i] += w * a.x; acc[4 * i + 1] += w * a.y;
-          acc[4 * i + 2] += w * a.z; acc[4 * i + 3] += w * a.w;
-        }
+        const float4 *src = reinterpret_cast<const float4 *>(ws_o + (s * plane + row) * kD + 8 * lane);
+        const float4 a = src[0], c = src[1];
+        acc[0] += w * a.x; acc[1] += w * a.y; acc[2] += w * a.z; acc[3] += w * a.w;
+        acc[4] += w * c.x; acc[5] += w * c.y; acc[6] += w * c.z; acc[7] += w * c.w;
         wsum += w;
       }
     }
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  uint32_t ow[kE / 2];
+  uint32_t ow[4];
 #pragma unroll
-  for (int e = 0; e < kE / 2; ++e) {
+  for (int e = 0; e < 4; ++e) {
     __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     ow[e] = *reinterpret_cast<uint32_t *>(&b2);
   }
-  __nv_bfloat16 *dst = out + row * D + kE * lane;
-  if constexpr (kE == 8)
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-  else
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(ow[0], ow[1]);
+  *reinterpret_cast<uint4 *>(out + row * kD + 8 * lane) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
 }
 
 }  // namespace
 
-// The plain prefill of head_dim 128 stays on the CUDA-core kernel.
-bool prefill_tc_supported(const nvkv_cache &c, bool mod) {
-  return c.head_dim == 256 || (mod && c.head_dim == 128);
-}
+bool prefill_tc_supported(const nvkv_cache &c) { return c.head_dim == kD; }
 
 int prefill_max_splits() { return kMaxSplits; }
 
@@ -748,51 +637,32 @@ int prefill_tc_items(const nvkv_cache &c, const nvkv_seqs &s, int max_q, int Hq)
   return (int)(((int64_t)max_q * G + 127) / 128) * c.num_kv_heads * s.batch;
 }
 
-template <int D, class Mod>
-static cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
-                                      const int32_t *cu_q, int total_q, int max_q, int Hq,
-                                      float sm_scale, void *out, int num_splits, float *ws_o,
-                                      float *ws_lse, cudaStream_t stream, const Mod &mod) {
+cudaError_t launch_prefill_tc(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
+                              const int32_t *cu_q, int total_q, int max_q, int Hq,
+                              float sm_scale, void *out, int num_splits, float *ws_o,
+                              float *ws_lse, cudaStream_t stream) {
   CUtensorMap map;
   if (!make_pool_tmap(c, &map)) return cudaErrorNotSupported;
   if (num_splits < 1 || num_splits > kMaxSplits || (num_splits > 1 && (!ws_o || !ws_lse)))
     return cudaErrorInvalidValue;
   const int G = Hq / c.num_kv_heads;
   const int mtiles = (max_q * G + 127) / 128;
-  constexpr int kSmemBytes = Cfg<D>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<D, Mod>,
+  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)(mtiles * num_splits), (unsigned)c.num_kv_heads, (unsigned)s.batch);
-  prefill_tc_kernel<D, Mod><<<grid, kThreads, kSmemBytes, stream>>>(
+  prefill_tc_kernel<<<grid, kThreads, kSmemBytes, stream>>>(
       map, c.num_pages, c.num_kv_heads, s.page_table, s.max_pages_per_seq, s.kv_lens,
       s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), cu_q, total_q, Hq,
       sm_scale * 1.4426950408889634f, static_cast<__nv_bfloat16 *>(out), num_splits,
-      num_splits > 1 ? ws_o : nullptr, ws_lse, s.err_word, mod);
+      num_splits > 1 ? ws_o : nullptr, ws_lse, s.err_word);
   if ((e = cudaGetLastError()) != cudaSuccess || num_splits == 1) return e;
   const dim3 mgrid((unsigned)(((int64_t)max_q * Hq + kMergeWarps - 1) / kMergeWarps),
                    (unsigned)s.batch);
-  prefill_merge_kernel<D><<<mgrid, kMergeWarps * 32, 0, stream>>>(
+  prefill_merge_kernel<<<mgrid, kMergeWarps * 32, 0, stream>>>(
       ws_o, ws_lse, num_splits, cu_q, total_q, Hq, G, 128 * mtiles,
       static_cast<__nv_bfloat16 *>(out));
   return cudaGetLastError();
-}
-
-// mod: null for plain causal attention.
-cudaError_t launch_prefill_tc(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
-                              const int32_t *cu_q, int total_q, int max_q, int Hq,
-                              float sm_scale, void *out, int num_splits, float *ws_o,
-                              float *ws_lse, cudaStream_t stream, const ScoreMod *mod) {
-  if (!mod)
-    return c.head_dim == 256
-               ? launch_prefill_mod<256>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
-                                         num_splits, ws_o, ws_lse, stream, NoMod{})
-               : cudaErrorNotSupported;
-  return c.head_dim == 256
-             ? launch_prefill_mod<256>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
-                                       num_splits, ws_o, ws_lse, stream, *mod)
-             : launch_prefill_mod<128>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
-                                       num_splits, ws_o, ws_lse, stream, *mod);
 }
 
 }  // namespace nvkv

@@ -355,3 +355,14 @@ def test_long_context_offsets():
             # 3e5 at 2^-24 each and the cap's 2^-19): relative to sum w |v - o|,
             # which softmax weights keep below 2 here, plus the bf16 rounding
             assert ((out[0, h].double().cpu() - o).abs() <= 2 ** -8 * o.abs() + 2 * (2 ** -11 + 3e-4)).all()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(256, 24, 4), (128, 8, 2)])
+def test_prefill_cap_from_linear_to_saturated(D, Hq, Hkv):
+    """Scores from far below the cap to far above it, in one chunk: rows whose
+    scores all lie in the polynomial's range and rows past it."""
+    for gain, cap in ((0.1, 50.0), (1.0, 12.0), (30.0, 20.0)):
+        case = Case(Hq, Hkv, D, [200], [200], seed=17, q_gain=gain).device()
+        m = Mod(cap=cap)
+        ref, tol = case.reference(m, D ** -0.5, False, "f16 scores")
+        assert_within(run_prefill(case, m, D ** -0.5), ref, tol, f"{gain}/{cap}")
