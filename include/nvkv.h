@@ -429,11 +429,14 @@ typedef struct nvkv_score_mod {
  * or a document start bounds what is read.  softcap, window and the pointers
  * are read when the call is made; the arrays by the kernels.
  *
- * The kernels and their arithmetic are those of nvkv_decode_attn, except that
- * an NVFP4 cache of head_dim 128 also runs on decode_qk4 (its query rows in
- * chunks of at most 6, each reading the keys once).
- * nvkv_decode_mod_kernel_name names the kernel ("decode_qk4", "decode_tc",
- * "decode_simt", or "none" on invalid arguments).
+ * nvkv_decode_mod_kernel_name names the kernel ("none" on invalid arguments):
+ *   "decode_qk4"  (T*Hq/Hkv <= 6, head_dim 128 and 256): the arithmetic of
+ *                 nvkv_decode_attn's decode_qk4.
+ *   "prefill_mod" (more rows): the kernel of nvkv_prefill_attn_mod, the keys
+ *                 of each (sequence, kv-head) split over as many CTAs as the
+ *                 workspace has room for; q * sm_scale * log2(e) enters as one
+ *                 f16 (11 significant bits; |q * sm_scale| below about 45000).
+ *   "decode_simt" (NVKV_DECODE_KERNEL=simt).
  *
  * nvkv_decode_attn_mod_k8v4: the same over a K8V4 cache, on the kernels of
  * nvkv_decode_attn_k8v4 (nvkv_decode_kernel_name_k8v4). */
@@ -449,7 +452,10 @@ nvkv_status nvkv_decode_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs *
                                       size_t workspace_bytes, void *out, nvkv_stream_t stream);
 
 /* nvkv_prefill_attn_split (same arguments, layouts, workspace and checks),
- * with the scores of `mod`, on the tensor cores for both head_dims.
+ * with the scores of `mod`, on the tensor cores for both head_dims: q *
+ * sm_scale * log2(e) as f16, products with the exact K in fp32, the scores'
+ * modifications and the softmax in fp32, weights rounded to f16 for the value
+ * sum, which accumulates in fp32.
  * num_splits = 0 takes the automatic count that the workspace has room for
  * (1 for a NULL one; nvkv_prefill_workspace_bytes(..., 0) is enough for any).
  * A prefix is seen in both directions as far as it is cached: put it into one

@@ -24,13 +24,16 @@ cudaError_t launch_decode_qk4(const nvkv_cache &, const nvkv_seqs &, const void 
 cudaError_t launch_decode_qk4_k8v4(const nvkv_cache &, const nvkv_seqs &, const void *, int, int,
                                    float, int, float *, float *, cudaStream_t, const ScoreMod *);
 cudaError_t launch_decode_tc(const nvkv_cache &, const nvkv_seqs &, const void *, int, int, float,
-                             int, float *, float *, cudaStream_t, const ScoreMod *);
+                             int, float *, float *, cudaStream_t);
 bool prefill_tc_supported(const nvkv_cache &);
 cudaError_t launch_prefill_tc(const nvkv_cache &, const nvkv_seqs &, const void *, const int32_t *,
                               int, int, int, float, void *, int, float *, float *, cudaStream_t);
 cudaError_t launch_prefill_mod(const nvkv_cache &, const nvkv_seqs &, const void *,
                                const int32_t *, int, int, int, float, void *, int, float *,
                                float *, cudaStream_t, const ScoreMod &);
+cudaError_t launch_decode_rows(const nvkv_cache &, const nvkv_seqs &, const void *, int, int,
+                               float, int64_t, float *, float *, void *, int, cudaStream_t,
+                               const ScoreMod &);
 int prefill_mod_auto_splits(const nvkv_cache &, const nvkv_seqs &, int, int, int,
                             const ScoreMod &, int);
 int prefill_max_splits();
@@ -233,27 +236,6 @@ bool force_kernel(const char *name) {
 }
 bool force_simt() { return force_kernel("simt"); }
 
-// The decode kernel of the step's shape (nvkv_decode_kernel_name); mod: null
-// for plain causal attention.
-cudaError_t run_decode(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T, int Hq,
-                       float sm_scale, const DecodeArgs &a, cudaStream_t stream,
-                       const ScoreMod *mod) {
-  if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(c, T, Hq, mod != nullptr))
-    return launch_decode_qk4(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, mod);
-  if (!force_simt() && decode_tc_supported(c, T, Hq))
-    return launch_decode_tc(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, mod);
-  return launch_decode_simt(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, false, mod);
-}
-
-// The same over a K8V4 cache (nvkv_decode_kernel_name_k8v4).
-cudaError_t run_decode_k8v4(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T, int Hq,
-                            float sm_scale, const DecodeArgs &a, cudaStream_t stream,
-                            const ScoreMod *mod) {
-  if (!force_simt() && decode_qk4_supported(c, T, Hq, false))
-    return launch_decode_qk4_k8v4(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, mod);
-  return launch_decode_simt(c, s, q, T, Hq, sm_scale, a.S, a.ws_o, a.ws_lse, stream, true, mod);
-}
-
 nvkv_status decode_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q, int32_t T,
                        int32_t num_q_heads, float sm_scale, const nvkv_score_mod *mod,
                        int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
@@ -266,12 +248,23 @@ nvkv_status decode_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const voi
   if ((st = check_mod(mod, m)) != NVKV_OK) return st;
   if (!out || !aligned16(out)) return NVKV_ERR_INVALID_ARG;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      k8 ? run_decode_k8v4(*cache, *seqs, q, T, num_q_heads, sm_scale, a, s, &m)
-         : run_decode(*cache, *seqs, q, T, num_q_heads, sm_scale, a, s, &m);
+  const nvkv_cache &c = *cache;
+  const bool simt = force_simt();
+  cudaError_t e;
+  if (!simt && k8 && decode_qk4_supported(c, T, num_q_heads, false)) {
+    e = launch_decode_qk4_k8v4(c, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o, a.ws_lse, s, &m);
+  } else if (!simt && !k8 && !force_kernel("tc") && decode_qk4_supported(c, T, num_q_heads, true)) {
+    e = launch_decode_qk4(c, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o, a.ws_lse, s, &m);
+  } else if (!simt && !k8) {
+    return cuda_status(launch_decode_rows(c, *seqs, q, T, num_q_heads, sm_scale,
+                                          (int64_t)a.S + (int64_t)seqs->batch * c.num_kv_heads - 1,
+                                          a.ws_o, a.ws_lse, out, nvkv_default_num_splits(), s, m));
+  } else {
+    e = launch_decode_simt(c, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o, a.ws_lse, s, k8, &m);
+  }
   if (e != cudaSuccess) return cuda_status(e);
-  return cuda_status(launch_combine_mod(*seqs, a.ws_o, a.ws_lse, T, num_q_heads,
-                                        cache->num_kv_heads, cache->head_dim, a.S, out, s, m));
+  return cuda_status(launch_combine_mod(*seqs, a.ws_o, a.ws_lse, T, num_q_heads, c.num_kv_heads,
+                                        c.head_dim, a.S, out, s, m));
 }
 
 nvkv_status prefill_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,
@@ -444,8 +437,15 @@ nvkv_status nvkv_decode_attn(const nvkv_cache *cache, const nvkv_seqs *seqs, con
   const nvkv_status st = check_decode(cache, seqs, q, T, num_q_heads, sm_scale, num_splits,
                                       workspace, workspace_bytes, a);
   if (st != NVKV_OK) return st;
-  return cuda_status(run_decode(*cache, *seqs, q, T, num_q_heads, sm_scale, a,
-                                reinterpret_cast<cudaStream_t>(stream), nullptr));
+  cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
+  if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(*cache, T, num_q_heads, false))
+    return cuda_status(launch_decode_qk4(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o,
+                                         a.ws_lse, st_, nullptr));
+  if (!force_simt() && decode_tc_supported(*cache, T, num_q_heads))
+    return cuda_status(
+        launch_decode_tc(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o, a.ws_lse, st_));
+  return cuda_status(launch_decode_simt(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o,
+                                        a.ws_lse, st_, false, nullptr));
 }
 
 nvkv_status nvkv_combine(const nvkv_seqs *seqs, const void *workspace, int32_t T,
@@ -557,8 +557,12 @@ nvkv_status nvkv_decode_attn_k8v4(const nvkv_cache *cache, const nvkv_seqs *seqs
   const nvkv_status st = check_decode(cache, seqs, q, T, num_q_heads, sm_scale, num_splits,
                                       workspace, workspace_bytes, a);
   if (st != NVKV_OK) return st;
-  return cuda_status(run_decode_k8v4(*cache, *seqs, q, T, num_q_heads, sm_scale, a,
-                                     reinterpret_cast<cudaStream_t>(stream), nullptr));
+  cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
+  if (!force_simt() && decode_qk4_supported(*cache, T, num_q_heads, false))
+    return cuda_status(launch_decode_qk4_k8v4(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S,
+                                              a.ws_o, a.ws_lse, st_, nullptr));
+  return cuda_status(launch_decode_simt(*cache, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o,
+                                        a.ws_lse, st_, true, nullptr));
 }
 
 const char *nvkv_decode_kernel_name_k8v4(const nvkv_cache *cache, int32_t T,
@@ -587,8 +591,7 @@ const char *nvkv_decode_mod_kernel_name(const nvkv_cache *cache, int32_t T, int3
     return "none";
   if (!force_simt() && !force_kernel("tc") && decode_qk4_supported(*cache, T, num_q_heads, true))
     return "decode_qk4";
-  if (!force_simt() && decode_tc_supported(*cache, T, num_q_heads)) return "decode_tc";
-  return "decode_simt";
+  return force_simt() ? "decode_simt" : "prefill_mod";
 }
 
 nvkv_status nvkv_decode_attn_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q,

@@ -435,11 +435,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = Hq / Hkv;
-  // This CTA's query rows: rows r0 .. r0 + R - 1 of the pair's R_all (all of
-  // them unless the launch has a row chunk for each blockIdx.y).
-  const int R_all = T * G;
-  const int r0 = Mod::kOn ? blockIdx.y * RM : 0;
-  const int R = Mod::kOn ? min(RM, R_all - r0) : R_all;
+  const int R = T * G;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -773,7 +769,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
       for (int r = warp; r < RM; r += kDeqWarps) {
         float y[kE];
         if (r < R) {
-          const int t = (r0 + r) / G, g = (r0 + r) % G;
+          const int t = r / G, g = r % G;
           const __nv_bfloat16 *src =
               q + ((size_t)(pg.b * T + t) * Hq + pg.h * G + g) * D + kE * lane;
           uint32_t w[kE / 2];
@@ -927,23 +923,28 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // writers published them with the terms)
         if (stid < kNP) {
           sh.nvis_s[stid] = stid < R ? sg.kv_len - T + stid / G + 1 : 0;
-          sh.m_s[stid] = -FLT_MAX;
+          // (ScoreMod: a padding row's scores are 0 and its maximum stays 0, so
+          // it needs no mask and never asks for a new maximum)
+          sh.m_s[stid] = Mod::kOn && stid >= R ? 0.f : -FLT_MAX;
         }
         if constexpr (Mod::kOn) {
           if (stid < RM) {
             int4 row = make_int4(0, 0, 0, 0);
             if (stid < R) {
-              const int pos = sg.kv_len - T + (r0 + stid) / G;
+              const int pos = sg.kv_len - T + stid / G;
               key_range(pos, sg.kv_len, mod.start(sg.b), mod.window, mod.prefix_of(sg.b), row.x,
                         row.y);
               row.z = pos;
-              row.w = __float_as_int(mod.slope2(sg.h * G + (r0 + stid) % G));
+              row.w = __float_as_int(mod.slope2(sg.h * G + stid % G));
             }
             sh.row_s[stid] = row;
           }
         }
 #pragma unroll
-        for (int i = 0; i < RM; ++i) l_part[i] = 0.f, mr[i] = -FLT_MAX;
+        for (int i = 0; i < RM; ++i) {
+          l_part[i] = 0.f;
+          mr[i] = Mod::kOn && i >= R ? 0.f : -FLT_MAX;
+        }
         wait_bar(sh.qready, seg_idx & 1, sh.flags, err);
 #pragma unroll
         for (int i = 0; i < RM; ++i) facr[i] = sh.fac[i];
@@ -1067,12 +1068,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
             } else {
               present = (pm_cur >> ((32 * lq + lane) >> 4)) & 1u;
             }
-            // every key of the unit is visible to every query (the first
-            // query's interval ends first, the last one's starts last)
-            bool vis_all = tok0 + kUnitTokens <= sg.kv_len - T + 1 && present;
-            if constexpr (Mod::kOn)
-              vis_all = vis_all && tok0 >= sg.lo &&
-                        (mod.window <= 0 || tok0 >= sg.kv_len - mod.window);
+            const bool vis_all = tok0 + kUnitTokens <= sg.kv_len - T + 1 && present;
 #pragma unroll
             for (int j = 0; j < RM; ++j) {
               const uint32_t *c8 = rr + j * kTerms;
@@ -1094,20 +1090,34 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 sc = (a2.x + a2.y) * facr[j];
               }
               if constexpr (Mod::kOn) {
-                if (mod.cap2 > 0.f) sc = mod.cap(sc);
-                if (mod.slopes) {
-                  const int4 row = sh.row_s[j];
-                  sc = fmaf(-__int_as_float(row.w), fabsf((float)(row.z - pos)), sc);
-                }
-                bool in = j < R;
-                if (!vis_all) {
-                  const int4 row = sh.row_s[j];
-                  in = pos >= row.x && pos < row.y && present;
-                }
-                x[j] = in ? sc : -INFINITY;
+                x[j] = sc;
               } else {
                 const int nv = vis_all ? (j < R ? 0x7fffffff : 0) : sh.nvis_s[j];
                 x[j] = pos < nv && present ? sc : -INFINITY;
+              }
+            }
+            if constexpr (Mod::kOn) {
+              if (mod.cap2 > 0.f) {
+#pragma unroll
+                for (int j = 0; j < RM; ++j) x[j] = mod.cap(x[j]);
+              }
+              if (mod.slopes) {
+#pragma unroll
+                for (int j = 0; j < RM; ++j) {
+                  const int4 row = sh.row_s[j];
+                  x[j] = fmaf(-__int_as_float(row.w), fabsf((float)(row.z - pos)), x[j]);
+                }
+              }
+              // Is every key of the unit visible to every query? (The first
+              // query's interval ends first, the last one's starts last.)
+              const bool all = tok0 + kUnitTokens <= sg.kv_len - T + 1 && tok0 >= sg.lo &&
+                               (mod.window <= 0 || tok0 >= sg.kv_len - mod.window);
+              if (!all || (K8 ? !present : pm_cur != 0xffu)) {
+#pragma unroll
+                for (int j = 0; j < RM; ++j) {
+                  const int4 row = sh.row_s[j];
+                  if (pos < row.x || pos >= row.y || !present) x[j] = j < R ? -INFINITY : 0.f;
+                }
               }
             }
           }
@@ -1247,7 +1257,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           for (int n = 0; n < RM; ++n) {
             if (n < R) {
               const float v = __uint_as_float(o8[n]);
-              ws_o[(slot * R_all + r0 + n) * D + d] = lv[n] > 0.f ? v * 16384.f / lv[n] : 0.f;
+              ws_o[(slot * R + n) * D + d] = lv[n] > 0.f ? v * 16384.f / lv[n] : 0.f;
             }
           }
         }
@@ -1255,7 +1265,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           float l = 0.f;
 #pragma unroll
           for (int n = 0; n < RM; ++n) l = n == stid ? lv[n] : l;
-          ws_lse[slot * R_all + r0 + stid] = l > 0.f ? sh.m_s[stid] + log2f(l) : -INFINITY;
+          ws_lse[slot * R + stid] = l > 0.f ? sh.m_s[stid] + log2f(l) : -INFINITY;
         }
         tc_fence_before();
         named_barrier(1, kSmxWarps * 32);  // the sums and maxima have been read
@@ -1347,19 +1357,14 @@ cudaError_t launch_fmt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, i
                            make_map(c, kVRows, CU_TENSOR_MAP_SWIZZLE_NONE, &map_v);
   if (!ok) return cudaErrorNotSupported;
   const float qscale = sm_scale * 1.4426950408889634f;
-  // Query rows of a pair in chunks of at most 6 (one, except at head_dim
-  // 128), as even as they come: 16 rows are 6 + 6 + 4.
   const int R = T * (Hq / c.num_kv_heads);
-  const int chunks = (R + kRowsCap - 1) / kRowsCap, Rc = (R + chunks - 1) / chunks;
-  auto kernel = Rc <= 2   ? decode_qk4_kernel<D, 2, K8, Mod>
-                : Rc <= 4 ? decode_qk4_kernel<D, 4, K8, Mod>
-                          : decode_qk4_kernel<D, 6, K8, Mod>;
+  auto kernel = R <= 2   ? decode_qk4_kernel<D, 2, K8, Mod>
+                : R <= 4 ? decode_qk4_kernel<D, 4, K8, Mod>
+                         : decode_qk4_kernel<D, 6, K8, Mod>;
   const int smem = Fmt<D, K8>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int RM = Rc <= 2 ? 2 : Rc <= 4 ? 4 : 6;
-  const dim3 grid((unsigned)S, (unsigned)((R + RM - 1) / RM));
-  kernel<<<grid, kThreads, smem, stream>>>(
+  kernel<<<S, kThreads, smem, stream>>>(
       map_k, map_ks, map_v, c.num_pages, c.num_kv_heads, s.page_table, s.max_pages_per_seq,
       s.kv_lens, s.batch, s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), T, Hq, qscale, S,
       ws_o, ws_lse, s.err_word, mod);
@@ -1370,12 +1375,11 @@ cudaError_t launch_fmt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, i
 
 // True when this kernel takes the shape: head_dim 256 and at most 6 query
 // rows (T * Hq/Hkv) per (sequence, kv-head), for both cache formats; with a
-// ScoreMod over an NVFP4 cache also head_dim 128 (more rows in chunks of 6,
-// each reading the keys once).
+// ScoreMod over an NVFP4 cache also head_dim 128.
 bool decode_qk4_supported(const nvkv_cache &c, int T, int Hq, bool mod) {
   const int R = T * (Hq / c.num_kv_heads);
   if (R < 1 || encode_fn() == nullptr) return false;
-  return c.head_dim == 256 ? R <= kRowsCap : mod && c.head_dim == 128;
+  return R <= kRowsCap && (c.head_dim == 256 || (mod && c.head_dim == 128));
 }
 
 // mod: null for plain causal attention.

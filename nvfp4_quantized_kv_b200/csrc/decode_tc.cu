@@ -38,9 +38,7 @@
 //  * Every wait is bounded; a timeout sets NVKV_DEVERR_TIMEOUT, turns all
 //    later waits into no-ops and lets the kernel drain and free its Tensor
 //    Memory.
-#include <cfloat>
-
-#include "score_mod.cuh"
+#include "nvkv_common.cuh"
 #include "sm100.cuh"
 
 namespace nvkv {
@@ -94,9 +92,7 @@ struct Cfg {
   static constexpr int kOffM = kOffMask + 2 * kSoftmaxWarps * 4 * 4;
   static constexpr int kOffAlpha = kOffM + N * 4;
   static constexpr int kOffNvis = kOffAlpha + N * 4;
-  static constexpr int kOffRow = kOffNvis + N * 4;              // int4 [N] (ScoreMod only)
-  static constexpr int kOffPres = kOffRow + N * 16;             // u32 [4] (ScoreMod only)
-  static constexpr int kOffFlags = kOffPres + 16;               // int[4]: abort at [2]
+  static constexpr int kOffFlags = kOffNvis + N * 4;            // int[4]: abort at [2]
   static constexpr int kOffPages = kOffFlags + 16;              // int[stages][8]
   static constexpr int kOffBars = kOffPages + kStages * kUnitPages * 4;
   static constexpr int kNumBars = 2 * kStages + 12;
@@ -104,20 +100,14 @@ struct Cfg {
   static constexpr int kSmemBytes = kOffTmem + 16 + 1024;      // + alignment slack
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(kOffQ % 1024 == 0 && kOffP % 16 == 0 && kPBytes % 16 == 0 &&
-                kOffPages % 16 == 0 && kOffRow % 16 == 0 && kOffBars % 8 == 0, "alignment");
+                kOffPages % 16 == 0 && kOffBars % 8 == 0, "alignment");
 };
 
 struct Shared {
   uint8_t *stages, *qtile, *qtile_lo, *ptile;
   float *red, *m_s, *alpha_s;
   int32_t *nvis_s, *pages;
-  int4 *row_s;  // ScoreMod: (first visible key, one past the last, position, slope bits) of a row
   uint32_t *masks;
-  // ScoreMod: bit p of entry (unit & 3) is set when page p of the unit is
-  // present, so the softmax leaves the keys of an absent page out.  Written
-  // with the unit's K tile; the K tile of unit u + 4 is written after the
-  // softmax of unit u (its scores wait for the value MMAs of unit u + 1).
-  volatile uint32_t *present;
   volatile int *flags;
   // sready, pready, vready and pvdone exist once per S^T / P^T / V^T slot:
   // slot s completes once per unit with (unit & 1) == s, so no wait is ever
@@ -132,44 +122,27 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
   return guarded_wait(bar, parity, flags + 2, err, kWaitBudget);  // flags[2]: abort
 }
 
-// Segment of the CTA's range: units [u, seg_end) of pair (b, h).  With a
-// ScoreMod the pair's units start at first_unit of the sequence and no key
-// below lo is visible.
+// Segment of the CTA's range: units [u, seg_end) of pair (b, h).
 struct Seg {
   int b, h, kv_len;
-  int lo, first_unit, units;
   int64_t pair_start, seg_end;
   bool bad;
 };
 
-template <class Mod>
-__device__ __forceinline__ Seg segment_at(const Mod &mod, int T, int64_t u, int64_t u1,
-                                          const int32_t *kv_lens, int B, int Hkv, int max_kv_len,
-                                          int max_pages) {
+__device__ __forceinline__ Seg segment_at(int64_t u, int64_t u1, const int32_t *kv_lens, int B,
+                                          int Hkv, int max_kv_len, int max_pages) {
   Seg s;
-  locate_pair_mod(mod, kv_lens, B, Hkv, T, u, s.b, s.h, s.pair_start, s.units);
-  s.seg_end = min(u1, s.pair_start + s.units);
-  s.lo = s.first_unit = 0;
-  if (s.b >= B) {  // past the last unit
-    s.kv_len = 0;
-    s.bad = false;
-    return s;
-  }
+  int units;
+  locate_pair(kv_lens, B, Hkv, u, s.b, s.h, s.pair_start, units);
+  s.seg_end = min(u1, s.pair_start + units);
   s.kv_len = kv_lens[s.b];
-  if constexpr (Mod::kOn) {
-    int n;
-    visible_units(s.kv_len, T, mod.start(s.b), mod.window, s.lo, s.first_unit, n);
-  }
   s.bad = s.kv_len > max_kv_len || s.kv_len > max_pages * kPageTokens;
   if (s.bad) s.kv_len = 0;  // nothing of a bad sequence is read
   return s;
 }
 
-// Page of the 16 tokens from `tok` on; -1 when it is absent or when none of
-// them is in [lo, kv_len).
-__device__ __forceinline__ int page_of(const int32_t *pt_row, int tok, int lo, int kv_len,
-                                       int num_pages) {
-  if (tok >= kv_len || tok + kPageTokens <= lo) return -1;
+__device__ __forceinline__ int page_of(const int32_t *pt_row, int tok, int kv_len, int num_pages) {
+  if (tok >= kv_len) return -1;
   const int p = pt_row[tok / kPageTokens];
   return (p >= 0 && p < num_pages) ? p : -1;
 }
@@ -178,14 +151,14 @@ __device__ __forceinline__ uint32_t dup_scale(uint32_t byte) {
   return e4m3x2_to_f16x2(byte | (byte << 8));
 }
 
-template <int N, class Mod>
+template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hkv,
                  const int32_t *__restrict__ page_table, int max_pages,
                  const int32_t *__restrict__ kv_lens, int B, int max_kv_len,
                  const __nv_bfloat16 *__restrict__ q, int T, int t0, int T_all, int Hq,
                  float qscale, int S,
-                 float *__restrict__ ws_o, float *__restrict__ ws_lse, int32_t *err, Mod mod) {
+                 float *__restrict__ ws_o, float *__restrict__ ws_lse, int32_t *err) {
   using C = Cfg<N>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -201,8 +174,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
   sh.m_s = reinterpret_cast<float *>(smem + C::kOffM);
   sh.alpha_s = reinterpret_cast<float *>(smem + C::kOffAlpha);
   sh.nvis_s = reinterpret_cast<int32_t *>(smem + C::kOffNvis);
-  sh.row_s = reinterpret_cast<int4 *>(smem + C::kOffRow);
-  sh.present = reinterpret_cast<volatile uint32_t *>(smem + C::kOffPres);
   sh.flags = reinterpret_cast<volatile int *>(smem + C::kOffFlags);
   sh.pages = reinterpret_cast<int32_t *>(smem + C::kOffPages);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBars);
@@ -225,7 +196,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
   const int R = T * G;
   const int R_all = T_all * G;
 
-  if constexpr (Mod::kOn) launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -255,7 +225,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
   tc_fence_after();
   const uint32_t tmem = *sh.tmem_slot;
 
-  const int64_t U = total_units(mod, kv_lens, B, Hkv, T_all);
+  int64_t U = 0;
+  for (int b = 0; b < B; ++b) U += (int64_t)units_of_len(kv_lens[b]) * Hkv;
   const int c = blockIdx.x;
   const int64_t u0 = U > 0 ? range_begin(c, U, S) : 0;
   const int64_t u1 = U > 0 ? range_begin(c + 1, U, S) : 0;
@@ -268,14 +239,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
     prefetch_tmap(&tmap);
     const int p = lane & 7;
     int64_t u = u0;
-    Seg sg = segment_at(mod, T_all, u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+    Seg sg = segment_at(u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
     auto page_for = [&](const Seg &g, int64_t uu) -> int {
-      const int tok =
-          unit_token<Mod>(g.first_unit, g.units, g.pair_start, uu) + p * kPageTokens;
+      const int tok = (int)(uu - g.pair_start) * kUnitTokens + p * kPageTokens;
       const int32_t *pt = page_table + (size_t)g.b * max_pages;
-      const int pg = page_of(pt, tok, g.lo, g.kv_len, num_pages);
-      if (lane < kUnitPages && tok < g.kv_len && tok + kPageTokens > g.lo && pg < 0)
-        report(err, NVKV_DEVERR_PAGE_ID);
+      const int pg = page_of(pt, tok, g.kv_len, num_pages);
+      if (lane < kUnitPages && tok < g.kv_len && pg < 0) report(err, NVKV_DEVERR_PAGE_ID);
       return pg;
     };
     int cur = u < u1 ? page_for(sg, u) : -1;
@@ -286,7 +255,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
       int nxt = -1;
       Seg nsg = sg;
       if (u + 1 < u1) {
-        if (u + 1 >= sg.seg_end) nsg = segment_at(mod, T_all, u + 1, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+        if (u + 1 >= sg.seg_end) nsg = segment_at(u + 1, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
         nxt = page_for(nsg, u + 1);
       }
       if (uc >= (uint32_t)kStages) {
@@ -332,7 +301,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
       int qk_phase = 0;
       uint32_t first_bits = 0;  // bit (unit & 31): unit starts its segment
       int64_t u = u0;
-      Seg sg = segment_at(mod, T_all, u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+      Seg sg = segment_at(u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
       int64_t seg_start = u;
       bool issued = false;
       long long t_last = clock64();
@@ -358,7 +327,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
                    mbar_test(sh.kready_a, qk & 1)) {
           tc_fence_after();
           if (u >= sg.seg_end) {
-            sg = segment_at(mod, T_all, u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+            sg = segment_at(u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
             seg_start = u;
           }
           if (u == seg_start) first_bits |= 1u << (qk & 31);
@@ -423,7 +392,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
 
     uint32_t uc = 0;
     for (int64_t u = u0; u < u1;) {
-      const Seg sg = segment_at(mod, T_all, u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
+      const Seg sg = segment_at(u, u1, kv_lens, B, Hkv, max_kv_len, max_pages);
       if (sg.bad && tid == 0) report(err, NVKV_DEVERR_LENGTH);
       const int64_t seg_start = u;
       const size_t slot = (size_t)c + (size_t)sg.b * Hkv + sg.h;
@@ -468,20 +437,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
           // Keys visible to score row n (query t0 + n / G of the step, at
           // position kv_len - T_all + t0 + n / G).
           sh.nvis_s[tid] = tid < R ? sg.kv_len - T_all + t0 + tid / G + 1 : 0;
-          // (a ScoreMod's row may see nothing in its first unit and keys in a
-          // later one: -FLT_MAX keeps -inf - m at -inf)
-          sh.m_s[tid] = Mod::kOn ? -FLT_MAX : -INFINITY;
-          if constexpr (Mod::kOn) {
-            int4 row = make_int4(0, 0, 0, 0);
-            if (tid < R) {
-              const int pos = sg.kv_len - T_all + t0 + tid / G;
-              key_range(pos, sg.kv_len, mod.start(sg.b), mod.window, mod.prefix_of(sg.b), row.x,
-                        row.y);
-              row.z = pos;
-              row.w = __float_as_int(mod.slope2(sg.h * G + tid % G));
-            }
-            sh.row_s[tid] = row;
-          }
+          sh.m_s[tid] = -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) l_part[i] = 0.f;
@@ -492,30 +448,21 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
         const bool first = (u == seg_start);
         const int stage = uc % kStages;
         const uint8_t *stg = sh.stages + stage * kStageBytes;
-        const int tok0 = unit_token<Mod>(sg.first_unit, sg.units, sg.pair_start, u);
+        const int tok0 = (int)(u - sg.pair_start) * kUnitTokens;
         if (!smx) {
           wait_bar(&sh.full[stage], (uc / kStages) & 1, sh.flags, err);
           const int4 pa = *reinterpret_cast<const int4 *>(sh.pages + stage * kUnitPages);
           const int4 pb4 = *reinterpret_cast<const int4 *>(sh.pages + stage * kUnitPages + 4);
-          const bool full_unit = tok0 + kUnitTokens <= sg.kv_len && tok0 >= sg.lo &&
+          const bool full_unit = tok0 + kUnitTokens <= sg.kv_len &&
                                  min(min(min(pa.x, pa.y), min(pa.z, pa.w)),
                                      min(min(pb4.x, pb4.y), min(pb4.z, pb4.w))) >= 0;
-
-          if (Mod::kOn && tid == 0) {
-            const int pg[8] = {pa.x, pa.y, pa.z, pa.w, pb4.x, pb4.y, pb4.z, pb4.w};
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m |= (pg[i] >= 0 ? 1u : 0u) << i;
-            sh.present[uc & 3] = m;
-          }
 
           // K tile half (phase 0: d 0..127, phase 1: d 128..255): thread = token
           // jl, one 16-byte chunk (32 d, two scale groups) per warp.
           const int jl = 32 * lq + lane;
           const int kp = jl >> 4, kslot = jl & 15;
           const bool kok = full_unit ||
-                           (sh.pages[stage * kUnitPages + kp] >= 0 && tok0 + jl < sg.kv_len &&
-                            tok0 + jl >= sg.lo);
+                           (sh.pages[stage * kUnitPages + kp] >= 0 && tok0 + jl < sg.kv_len);
           const uint8_t *kpg = stg + kp * kPagePitch;
           // Scale bytes of the chunk's two groups: 2*sub, 2*sub+1 (phase 0) and
           // 8 + 2*sub, 8 + 2*sub + 1 (phase 1); 2-byte loads at 2-byte offsets.
@@ -609,14 +556,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
                     else if (t0 + 1 >= sg.kv_len) o8[i] &= 0xffffu;
                   }
                 }
-                if (Mod::kOn && ptok < sg.lo) {  // tokens before every query's interval
-  #pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    const int t0 = ptok + 2 * i;
-                    if (t0 + 1 < sg.lo) o8[i] = 0u;
-                    else if (t0 < sg.lo) o8[i] &= 0xffff0000u;
-                  }
-                }
               } else {
   #pragma unroll
                 for (int i = 0; i < 8; ++i) o8[i] = 0u;
@@ -647,13 +586,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
           wait_bar(&sh.sready[uc & 1], (uc >> 1) & 1, sh.flags, err);
           tc_fence_after();
           const int pos = tok0 + 32 * lq + lane;
-          // every key of the unit is visible to every query of the launch
-          bool vis_all = tok0 + kUnitTokens <= sg.kv_len - T_all + t0 + 1;
-          if constexpr (Mod::kOn)
-            vis_all = vis_all && tok0 >= sg.lo &&
-                      (mod.window <= 0 || tok0 >= sg.kv_len - mod.window);
+          const bool vis_all = tok0 + kUnitTokens <= sg.kv_len - T_all + t0 + 1;
           const uint32_t sslot = tl + C::kColS + (uc & 1) * N;
-          const bool here = !Mod::kOn || ((sh.present[uc & 3] >> ((32 * lq + lane) >> 4)) & 1u);
           uint32_t *my_mask = sh.masks + ((uc & 1) * kSoftmaxWarps + lq) * 4;
           // Scores of one 16-row chunk, masked: invisible keys and padding
           // rows (n >= R) become -inf.  Branch-free over the 16 rows.
@@ -661,22 +595,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmap, int num_pages, int Hk
             uint32_t r[16];
             tmem_ld16(sslot + 16 * c16, r);
             tmem_wait_ld();
-            if constexpr (Mod::kOn) {
-              if (mod.cap2 > 0.f) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  r[j] = __float_as_uint(mod.cap(__uint_as_float(r[j])));
-              }
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int4 row = sh.row_s[16 * c16 + j];
-                const float sc = fmaf(-__int_as_float(row.w), fabsf((float)(row.z - pos)),
-                                      __uint_as_float(r[j]));
-                const bool in = vis_all ? 16 * c16 + j < R : pos >= row.x && pos < row.y;
-                x[j] = in && here ? sc : -INFINITY;
-              }
-              return;
-            }
             int nv[16];
             if (vis_all) {
 #pragma unroll
@@ -904,18 +822,18 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-template <int N, class Mod>
+template <int N>
 cudaError_t launch_n(const CUtensorMap &map, const nvkv_cache &c, const nvkv_seqs &s,
                      const void *q, int T, int t0, int T_all, int Hq, float qscale, int S,
-                     float *ws_o, float *ws_lse, cudaStream_t stream, const Mod &mod) {
+                     float *ws_o, float *ws_lse, cudaStream_t stream) {
   const int smem = Cfg<N>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<N, Mod>,
+  cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<N>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode_tc_kernel<N, Mod><<<S, kThreads, smem, stream>>>(
+  decode_tc_kernel<N><<<S, kThreads, smem, stream>>>(
       map, c.num_pages, c.num_kv_heads, s.page_table, s.max_pages_per_seq, s.kv_lens, s.batch,
       s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), T, t0, T_all, Hq, qscale, S, ws_o,
-      ws_lse, s.err_word, mod);
+      ws_lse, s.err_word);
   return cudaGetLastError();
 }
 
@@ -931,7 +849,7 @@ bool decode_tc_supported(const nvkv_cache &c, int T, int Hq) {
 
 // The pool as a 2-D byte tensor of 128-byte rows; one box of 18*D/128 rows (36
 // at head_dim 256) is one page's kv-head block.  Shared with the prefill
-// kernel.
+// kernels.
 bool make_pool_tmap(const nvkv_cache &c, CUtensorMap *map) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
@@ -946,12 +864,9 @@ bool make_pool_tmap(const nvkv_cache &c, CUtensorMap *map) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-namespace {
-
-template <class Mod>
-cudaError_t launch_chunks(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T, int Hq,
-                          float sm_scale, int S, float *ws_o, float *ws_lse, cudaStream_t stream,
-                          const Mod &mod) {
+cudaError_t launch_decode_tc(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
+                             int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
+                             cudaStream_t stream) {
   CUtensorMap map;
   if (!make_pool_tmap(c, &map)) return cudaErrorNotSupported;
   const int G = Hq / c.num_kv_heads;
@@ -965,24 +880,14 @@ cudaError_t launch_chunks(const nvkv_cache &c, const nvkv_seqs &s, const void *q
     const int R = Tn * G;
     cudaError_t e;
     if (R <= 16)
-      e = launch_n<16>(map, c, s, q, Tn, t0, T, Hq, qscale, S, ws_o, ws_lse, stream, mod);
+      e = launch_n<16>(map, c, s, q, Tn, t0, T, Hq, qscale, S, ws_o, ws_lse, stream);
     else if (R <= 32)
-      e = launch_n<32>(map, c, s, q, Tn, t0, T, Hq, qscale, S, ws_o, ws_lse, stream, mod);
+      e = launch_n<32>(map, c, s, q, Tn, t0, T, Hq, qscale, S, ws_o, ws_lse, stream);
     else
-      e = launch_n<48>(map, c, s, q, Tn, t0, T, Hq, qscale, S, ws_o, ws_lse, stream, mod);
+      e = launch_n<48>(map, c, s, q, Tn, t0, T, Hq, qscale, S, ws_o, ws_lse, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
-}
-
-}  // namespace
-
-// mod: null for plain causal attention.
-cudaError_t launch_decode_tc(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
-                             int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
-                             cudaStream_t stream, const ScoreMod *mod) {
-  return mod ? launch_chunks(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod)
-             : launch_chunks(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, NoMod{});
 }
 
 }  // namespace nvkv

@@ -111,6 +111,8 @@ struct Args {
   int max_kv_len;
   const __nv_bfloat16 *q;
   const int32_t *cu_q;
+  int T;                 // > 0: a decode step of T queries per sequence (cu_q is not used,
+                         // key_starts has one entry per sequence); 0: a chunk
   int total_q, Hq;
   float qscale;
   __nv_bfloat16 *out;
@@ -132,13 +134,15 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   const int mt = blockIdx.x / a.num_splits, split = blockIdx.x % a.num_splits;
   const int h = blockIdx.y, b = blockIdx.z;
   const int G = a.Hq / a.Hkv;
-  const int q0 = a.cu_q[b];
-  const int n_b = a.cu_q[b + 1] - q0;
+  const int q0 = a.T > 0 ? b * a.T : a.cu_q[b];
+  const int n_b = a.T > 0 ? a.T : a.cu_q[b + 1] - q0;
   const int kv_len = a.kv_lens[b];
+  auto start_of = [&](int i) { return mod.start(a.T > 0 ? b : q0 + i); };
   const int prefix = mod.prefix_of(b);
   const int rows = n_b * G;
   if (128 * mt >= rows) return;  // uniform: this tile has no query row
-  const bool bad = n_b < 0 || q0 < 0 || q0 + n_b > a.total_q || kv_len < n_b ||
+  // (a decode step may have more queries than tokens: the first see nothing)
+  const bool bad = n_b < 0 || q0 < 0 || q0 + n_b > a.total_q || (a.T == 0 && kv_len < n_b) ||
                    kv_len > a.max_kv_len || kv_len > a.max_pages * kPageTokens;
   // Output rows exist only when the chunk lies inside the total_q rows.
   const bool rows_ok = n_b >= 0 && q0 >= 0 && q0 + n_b <= a.total_q;
@@ -175,7 +179,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     const int i_last = min(n_b - 1, (128 * mt + 127) / G);
     for (int i = (128 * mt) / G + lane; i <= i_last; i += 32) {
       int lo, hi;
-      key_range(kv_len - n_b + i, kv_len, mod.start(q0 + i), mod.window, prefix, lo, hi);
+      key_range(kv_len - n_b + i, kv_len, start_of(i), mod.window, prefix, lo, hi);
       if (lo < hi) key_lo = min(key_lo, lo), key_hi = max(key_hi, hi);
     }
   }
@@ -475,7 +479,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     int row_lo = 0, row_hi = 0;               // keys row_lo .. row_hi - 1 are visible
     float slope2 = 0.f;
     if (valid) {
-      key_range(pos, kv_len, mod.start(q0 + i), mod.window, prefix, row_lo, row_hi);
+      key_range(pos, kv_len, start_of(i), mod.window, prefix, row_lo, row_hi);
       slope2 = mod.slope2(h * G + g);
     }
     // Q row -> Tensor Memory (A operand), f16, pre-scaled to base-2 scores.
@@ -709,56 +713,66 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Merge of the key splits: row (token q0 + i, head hq) of sequence b is
+// Merge of the key splits: row (token, head) of `rows` is
 // sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M) with M the largest lse (zero
-// when no split saw a key). One warp per row, D/32 elements a lane. Set up
-// while the attention kernel runs (programmatic dependent launch).
-constexpr int kMaxSplits = 8;
-constexpr int kMergeWarps = 8;
+// when no split saw a key). kW warps a row (a decode step's few rows have up
+// to 32 splits), D/32 elements a lane; the warps' sums are added in order.
+// Rows outside every sequence's chunk are left alone. Set up while the
+// attention kernel runs (programmatic dependent launch).
+constexpr int kMaxSplits = 8;        // of a chunk
+constexpr int kMaxStepSplits = 32;   // of a decode step
+constexpr int kMergeThreads = 256;
 
-template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32)
+template <int D, int kW>
+__global__ void __launch_bounds__(kMergeThreads)
 prefill_mod_merge_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_lse,
-                         int num_splits, const int32_t *__restrict__ cu_q, int total_q, int Hq,
-                         int G, int row_cap, __nv_bfloat16 *__restrict__ out) {
+                         int num_splits, const int32_t *__restrict__ cu_q, int T, int total_q,
+                         int Hq, int G, int row_cap, __nv_bfloat16 *__restrict__ out) {
+  constexpr int kRows = kMergeThreads / 32 / kW;  // rows of a block
+  constexpr int kE = D / 32;                      // elements of a lane: 4 or 8
+  __shared__ float s_acc[kW > 1 ? kMergeThreads / 32 : 1][D], s_w[kMergeThreads / 32];
   const int b = blockIdx.y;
-  const int q0 = cu_q[b], n_b = cu_q[b + 1] - q0;
+  const int q0 = T > 0 ? b * T : cu_q[b], n_b = T > 0 ? T : cu_q[b + 1] - q0;
   if (n_b <= 0 || q0 < 0 || q0 + n_b > total_q) return;  // no output rows (as in the attention)
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t idx = (int64_t)blockIdx.x * kMergeWarps + warp;  // token idx / Hq, head idx % Hq
-  if (idx >= (int64_t)n_b * Hq) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kW;
+  const int64_t idx = (int64_t)blockIdx.x * kRows + warp / kW;  // token idx / Hq, head idx % Hq
   // only the rows the attention grid covers (tile rows i*G + g < row_cap)
-  if ((idx / Hq) * G + (idx % Hq) % G >= row_cap) return;
-  const size_t row = (size_t)q0 * Hq + idx;
+  const bool live = idx < (int64_t)n_b * Hq && (idx / Hq) * G + (idx % Hq) % G < row_cap;
+  const size_t row = (size_t)q0 * Hq + (live ? idx : 0);
   const size_t plane = (size_t)total_q * Hq;
   grid_dependency_wait();
-  float lse[kMaxSplits], mx = -INFINITY;
-#pragma unroll
-  for (int s = 0; s < kMaxSplits; ++s) {
-    lse[s] = s < num_splits ? ws_lse[s * plane + row] : -INFINITY;
-    mx = fmaxf(mx, lse[s]);
-  }
-  constexpr int kE = D / 32;  // elements of a lane: 4 or 8
+  const float my_lse = live && lane < num_splits ? ws_lse[lane * plane + row] : -INFINITY;
+  const float mx = warp_max(my_lse);
+  const float my_w = my_lse > -INFINITY ? exp2f(my_lse - mx) : 0.f;
   float acc[kE], wsum = 0.f;
 #pragma unroll
   for (int e = 0; e < kE; ++e) acc[e] = 0.f;
-  if (mx > -INFINITY) {
+#pragma unroll 4
+  for (int s = sub; s < num_splits; s += kW) {  // warp-uniform
+    const float w = __shfl_sync(0xffffffffu, my_w, s);
+    if (w == 0.f) continue;
+    const float4 *src = reinterpret_cast<const float4 *>(ws_o + (s * plane + row) * D + kE * lane);
 #pragma unroll
-    for (int s = 0; s < kMaxSplits; ++s) {
-      if (s < num_splits && lse[s] > -INFINITY) {
-        const float w = exp2f(lse[s] - mx);
-        const float4 *src =
-            reinterpret_cast<const float4 *>(ws_o + (s * plane + row) * D + kE * lane);
+    for (int i = 0; i < kE / 4; ++i) {
+      const float4 v = src[i];
+      acc[4 * i] = fmaf(w, v.x, acc[4 * i]), acc[4 * i + 1] = fmaf(w, v.y, acc[4 * i + 1]);
+      acc[4 * i + 2] = fmaf(w, v.z, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(w, v.w, acc[4 * i + 3]);
+    }
+    wsum += w;
+  }
+  if constexpr (kW > 1) {
 #pragma unroll
-        for (int i = 0; i < kE / 4; ++i) {
-          const float4 v = src[i];
-          acc[4 * i] += w * v.x, acc[4 * i + 1] += w * v.y;
-          acc[4 * i + 2] += w * v.z, acc[4 * i + 3] += w * v.w;
-        }
-        wsum += w;
-      }
+    for (int e = 0; e < kE; ++e) s_acc[warp][kE * lane + e] = acc[e];
+    if (lane == 0) s_w[warp] = wsum;
+    __syncthreads();
+    if (sub != 0) return;
+    for (int w = 1; w < kW; ++w) {
+      wsum += s_w[warp + w];
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[e] += s_acc[warp + w][kE * lane + e];
     }
   }
+  if (!live) return;
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
   uint32_t ow[kE / 2];
 #pragma unroll
@@ -775,8 +789,9 @@ prefill_mod_merge_kernel(const float *__restrict__ ws_o, const float *__restrict
 
 template <int D>
 cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, const int32_t *cu_q,
-                     int total_q, int max_q, int Hq, float sm_scale, void *out, int num_splits,
-                     float *ws_o, float *ws_lse, cudaStream_t stream, const ScoreMod &mod) {
+                     int T, int total_q, int max_q, int Hq, float sm_scale, void *out,
+                     int num_splits, float *ws_o, float *ws_lse, cudaStream_t stream,
+                     const ScoreMod &mod) {
   CUtensorMap map;
   if (!make_pool_tmap(c, &map)) return cudaErrorNotSupported;
   const int G = Hq / c.num_kv_heads;
@@ -790,7 +805,7 @@ cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, con
   a.page_table = s.page_table, a.max_pages = s.max_pages_per_seq;
   a.kv_lens = s.kv_lens, a.max_kv_len = s.max_kv_len;
   a.q = static_cast<const __nv_bfloat16 *>(q), a.cu_q = cu_q;
-  a.total_q = total_q, a.Hq = Hq, a.qscale = sm_scale * kLog2e;
+  a.T = T, a.total_q = total_q, a.Hq = Hq, a.qscale = sm_scale * kLog2e;
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.num_splits = num_splits;
   a.ws_o = num_splits > 1 ? ws_o : nullptr, a.ws_lse = ws_lse;
@@ -798,49 +813,59 @@ cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, con
   const dim3 grid((unsigned)(mtiles * num_splits), (unsigned)c.num_kv_heads, (unsigned)s.batch);
   prefill_mod_kernel<D><<<grid, kThreads, smem, stream>>>(map, a, mod);
   if ((e = cudaGetLastError()) != cudaSuccess || num_splits == 1) return e;
+  const int per_block = num_splits > 8 ? 1 : kMergeThreads / 32;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((int64_t)max_q * Hq + kMergeWarps - 1) / kMergeWarps),
+  cfg.gridDim = dim3((unsigned)(((int64_t)max_q * Hq + per_block - 1) / per_block),
                      (unsigned)s.batch);
-  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_mod_merge_kernel<D>, (const float *)ws_o,
-                            (const float *)ws_lse, num_splits, cu_q, total_q, Hq, G, 128 * mtiles,
-                            static_cast<__nv_bfloat16 *>(out));
+  return cudaLaunchKernelEx(
+      &cfg, num_splits > 8 ? prefill_mod_merge_kernel<D, 8> : prefill_mod_merge_kernel<D, 1>,
+      (const float *)ws_o, (const float *)ws_lse, num_splits, cu_q, T, total_q, Hq, G,
+      128 * mtiles, static_cast<__nv_bfloat16 *>(out));
 }
 
 }  // namespace
 
-// Key splits of a call: the count in 1 .. 8 with the least estimated time. A
-// CTA takes about kSetup tiles' time before its first and after its last
-// tile; n CTAs a split run in ceil(n S / SMs) waves; the merge reads S fp32
-// planes of the output and writes one of bf16 (kMergeBytes a tile's time).
-// Keys from documents (key_starts) are not known here: splits then only fill
-// the first wave.
-int prefill_mod_auto_splits(const nvkv_cache &c, const nvkv_seqs &s, int total_q, int max_q,
-                            int Hq, const ScoreMod &mod, int sms) {
+// Key splits of a call with n query tiles (of all kv-heads and sequences): the
+// count in 1 .. most with the least estimated time. A CTA takes about kSetup
+// tiles' time before its first and after its last tile; n CTAs a split run in
+// ceil(n S / SMs) waves; the merge of S fp32 planes of `values` outputs takes
+// kMergeBytes a tile's time. Keys from documents (key_starts) are not known
+// here: the splits of a chunk then only fill the first wave.
+static int estimate_splits(int64_t n, int64_t keys, int64_t values, bool first_wave, int most,
+                           int sms) {
   constexpr double kSetup = 6.0, kMergeBytes = 6.0e6;
-  const int G = Hq / c.num_kv_heads;
-  const int64_t n = ((int64_t)max_q * G + 127) / 128 * c.num_kv_heads * s.batch;
-  int64_t keys = s.max_kv_len;
-  if (mod.window > 0 && keys > (int64_t)mod.window + 128 / G)
-    keys = (int64_t)mod.window + 128 / G;  // (a prefix may add to it)
-  const int64_t tiles = (keys + kTileTokens - 1) / kTileTokens + (mod.window > 0 ? 1 : 0);
+  const int64_t tiles = (keys + kTileTokens - 1) / kTileTokens;
   int best = 1;
   double least = 0;
-  for (int S = 1; S <= kMaxSplits; ++S) {
-    if (S > 1 && mod.starts && n * S > sms) break;
+  for (int S = 1; S <= most; ++S) {
+    if (S > 1 && first_wave && n * S > sms) break;
     const double waves = (double)((n * S + sms - 1) / sms);
     double cost = waves * (kSetup + (double)((tiles + S - 1) / S));
-    if (S > 1)
-      cost += 2.0 + (double)total_q * Hq * c.head_dim * (8.0 * S + 2.0) / kMergeBytes;
+    if (S > 1) cost += 2.0 + (double)values * (8.0 * S + 2.0) / kMergeBytes;
     if (S == 1 || cost < least) best = S, least = cost;
   }
   return best;
+}
+
+// Keys that a tile of `span` consecutive queries can see.
+static int64_t visible_keys(const nvkv_seqs &s, const ScoreMod &mod, int span) {
+  const int64_t w = (int64_t)mod.window + span + kTileTokens;  // (a prefix may add to it)
+  return mod.window > 0 && w < s.max_kv_len ? w : s.max_kv_len;
+}
+
+int prefill_mod_auto_splits(const nvkv_cache &c, const nvkv_seqs &s, int total_q, int max_q,
+                            int Hq, const ScoreMod &mod, int sms) {
+  const int G = Hq / c.num_kv_heads;
+  const int64_t n = ((int64_t)max_q * G + 127) / 128 * c.num_kv_heads * s.batch;
+  return estimate_splits(n, visible_keys(s, mod, 128 / G), (int64_t)total_q * Hq * c.head_dim,
+                         mod.starts != nullptr, kMaxSplits, sms);
 }
 
 cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
@@ -849,10 +874,27 @@ cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, const vo
                                float *ws_lse, cudaStream_t stream, const ScoreMod &mod) {
   if (num_splits < 1 || num_splits > kMaxSplits || (num_splits > 1 && (!ws_o || !ws_lse)))
     return cudaErrorInvalidValue;
-  return c.head_dim == 256 ? launch_d<256>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
+  return c.head_dim == 256 ? launch_d<256>(c, s, q, cu_q, 0, total_q, max_q, Hq, sm_scale, out,
                                            num_splits, ws_o, ws_lse, stream, mod)
-                           : launch_d<128>(c, s, q, cu_q, total_q, max_q, Hq, sm_scale, out,
+                           : launch_d<128>(c, s, q, cu_q, 0, total_q, max_q, Hq, sm_scale, out,
                                            num_splits, ws_o, ws_lse, stream, mod);
+}
+
+// A decode step of T queries per sequence (T * Hq/Hkv <= 128 rows, one query
+// tile for each kv-head and sequence). ws_o and ws_lse have room for `slots`
+// partial results of a (sequence, kv-head) pair's rows each.
+cudaError_t launch_decode_rows(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
+                               int Hq, float sm_scale, int64_t slots, float *ws_o, float *ws_lse,
+                               void *out, int sms, cudaStream_t stream, const ScoreMod &mod) {
+  const int64_t n = (int64_t)c.num_kv_heads * s.batch;
+  const int total_q = s.batch * T;
+  const int room = (int)(slots / n < kMaxStepSplits ? slots / n : kMaxStepSplits);
+  const int S = estimate_splits(n, visible_keys(s, mod, T), (int64_t)total_q * Hq * c.head_dim,
+                                false, room > 1 ? room : 1, sms);
+  return c.head_dim == 256 ? launch_d<256>(c, s, q, nullptr, T, total_q, T, Hq, sm_scale, out, S,
+                                           ws_o, ws_lse, stream, mod)
+                           : launch_d<128>(c, s, q, nullptr, T, total_q, T, Hq, sm_scale, out, S,
+                                           ws_o, ws_lse, stream, mod);
 }
 
 }  // namespace nvkv

@@ -21,7 +21,7 @@ def slopes(h):
 # what a kernel rounds, by the kernel the step's shape runs on
 def decode_slack(case, T):
     name = nv.nvkv_decode_mod_kernel_name(case.cache, T, case.Hq)
-    return "fp32" if name == "decode_simt" else "f16 weights"
+    return {"decode_simt": "fp32", "decode_qk4": "f16 weights", "prefill_mod": "f16 scores"}[name]
 
 
 DECODE = [
