@@ -1097,11 +1097,11 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
               }
             }
             if constexpr (Mod::kOn) {
-              if (mod.cap2 > 0.f) {
+              if constexpr (Mod::kCap) {
 #pragma unroll
                 for (int j = 0; j < RM; ++j) x[j] = mod.cap(x[j]);
               }
-              if (mod.slopes) {
+              if constexpr (Mod::kBias) {
 #pragma unroll
                 for (int j = 0; j < RM; ++j) {
                   const int4 row = sh.row_s[j];
@@ -1390,9 +1390,11 @@ cudaError_t launch_decode_qk4(const nvkv_cache &c, const nvkv_seqs &s, const voi
     return c.head_dim == 256 ? launch_fmt<256, false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse,
                                                       stream, NoMod{})
                              : cudaErrorNotSupported;
-  return c.head_dim == 256
-             ? launch_fmt<256, false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod)
-             : launch_fmt<128, false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod);
+  return with_mod(*mod, [&](const auto &m) {
+    return c.head_dim == 256
+               ? launch_fmt<256, false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, m)
+               : launch_fmt<128, false>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, m);
+  });
 }
 
 // The same kernel over a K8V4 cache (E4M3 K rows with an fp32 row scale,
@@ -1400,8 +1402,11 @@ cudaError_t launch_decode_qk4(const nvkv_cache &c, const nvkv_seqs &s, const voi
 cudaError_t launch_decode_qk4_k8v4(const nvkv_cache &c, const nvkv_seqs &s, const void *q, int T,
                                    int Hq, float sm_scale, int S, float *ws_o, float *ws_lse,
                                    cudaStream_t stream, const ScoreMod *mod) {
-  return mod ? launch_fmt<256, true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, *mod)
-             : launch_fmt<256, true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, NoMod{});
+  if (!mod)
+    return launch_fmt<256, true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, NoMod{});
+  return with_mod(*mod, [&](const auto &m) {
+    return launch_fmt<256, true>(c, s, q, T, Hq, sm_scale, S, ws_o, ws_lse, stream, m);
+  });
 }
 
 }  // namespace nvkv

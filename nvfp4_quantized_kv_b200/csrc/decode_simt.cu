@@ -183,11 +183,11 @@ decode_simt_kernel(const uint8_t *__restrict__ pool, int num_pages, int Hkv, int
     const int kv_len = kv_lens[b];
     int tok_begin = (int)(u - pair_start) * kUnitTokens;
     int tok_end = min((int)(seg_end - pair_start) * kUnitTokens, kv_len);
-    if constexpr (Mod::kOn) {  // the segment's units, newest first
+    if constexpr (Mod::kOn) {
       int lo, first, n;
       visible_units(kv_len, T, mod.start(b), mod.window, lo, first, n);
-      tok_begin = unit_token<Mod>(first, n, pair_start, seg_end - 1);
-      tok_end = min(unit_token<Mod>(first, n, pair_start, u) + kUnitTokens, kv_len);
+      tok_begin = unit_token<Mod>(first, n, pair_start, u);
+      tok_end = min(unit_token<Mod>(first, n, pair_start, seg_end - 1) + kUnitTokens, kv_len);
     }
     const size_t slot = (size_t)c + (size_t)b * Hkv + h;
     const bool bad_len = kv_len > max_kv_len || kv_len > max_pages * kPageTokens;

@@ -7,10 +7,10 @@
 // of its interval (score_mod.cuh); softmax; times V.
 //
 // One CTA owns 128 query rows (chunk tokens x GQA heads) of one kv-head and
-// streams the 64-token key tiles that any of its rows sees, from the newest
-// to the oldest: with a distance bias the largest scores come first, so the
-// running maximum is found in the first tile instead of being raised in every
-// one. Q (128 x D, f16, scaled to base-2 scores) sits in Tensor Memory as the
+// streams the 64-token key tiles that any of its rows sees; with a distance
+// bias from the newest to the oldest, so that the largest scores come first
+// and the running maximum is found in the first tile instead of being raised
+// in every one. Q (128 x D, f16, scaled to base-2 scores) sits in Tensor Memory as the
 // A operand of S = Q K^T (N = 64), S is double-buffered there, P (f16)
 // overwrites its own S slot as the A operand of O += P V (N = D), O stays in
 // Tensor Memory.
@@ -121,9 +121,9 @@ struct Args {
   int32_t *err;
 };
 
-template <int D>
+template <int D, class Mod>
 __global__ void __launch_bounds__(kThreads, 1)
-prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const ScoreMod mod) {
+prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const Mod mod) {
   using C = Cfg<D>;
   constexpr int kPagePitch = C::kPagePitch, kStageBytes = C::kStageBytes,
                 kKTileBytes = C::kKTileBytes, kVTileBytes = C::kVTileBytes;
@@ -191,11 +191,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   if (key_lo >= key_hi) key_lo = key_hi = 0;  // nothing is seen
   const int tile_lo = key_lo / kTileTokens;
   const int ntiles_all = (key_hi + kTileTokens - 1) / kTileTokens - tile_lo;
-  // This CTA's key tiles j0 .. j0 + ntiles - 1, counted from the newest; every
-  // ring and barrier below counts from its first tile.
+  // This CTA's key tiles j0 .. j0 + ntiles - 1, with a bias counted from the
+  // newest; every ring and barrier below counts from its first tile.
   const int j0 = (int)((int64_t)split * ntiles_all / a.num_splits);
   const int ntiles = (int)((int64_t)(split + 1) * ntiles_all / a.num_splits) - j0;
-  auto tile_key = [&](int j) { return (tile_lo + ntiles_all - 1 - (j0 + j)) * kTileTokens; };
+  auto tile_key = [&](int j) {
+    return (tile_lo + (Mod::kBias ? ntiles_all - 1 - (j0 + j) : j0 + j)) * kTileTokens;
+  };
 
   if (bad && threadIdx.x == 0) report(a.err, NVKV_DEVERR_LENGTH);
   if (threadIdx.x == 0) {
@@ -534,7 +536,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       load_scores();
       const int key0 = tile_key(j) + kHalf * hf;
       float above;  // no visible score is larger
-      if (mod.cap2 > 0.f) {
+      if constexpr (Mod::kCap) {
         // A polynomial, good for scores of at most 0.75 caps and increasing
         // beyond: its own values tell whether all of them are. Where one is
         // not, the exact form (two special functions a score).
@@ -560,7 +562,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       } else {
         above = top_score();
       }
-      if (mod.slopes) {
+      if constexpr (Mod::kBias) {
         // (distances are exact; with a prefix a key may lie ahead)
         const float d0 = (float)(pos - key0);
 #pragma unroll
@@ -787,17 +789,17 @@ prefill_mod_merge_kernel(const float *__restrict__ ws_o, const float *__restrict
     *reinterpret_cast<uint2 *>(dst) = make_uint2(ow[0], ow[1]);
 }
 
-template <int D>
+template <int D, class Mod>
 cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, const int32_t *cu_q,
                      int T, int total_q, int max_q, int Hq, float sm_scale, void *out,
                      int num_splits, float *ws_o, float *ws_lse, cudaStream_t stream,
-                     const ScoreMod &mod) {
+                     const Mod &mod) {
   CUtensorMap map;
   if (!make_pool_tmap(c, &map)) return cudaErrorNotSupported;
   const int G = Hq / c.num_kv_heads;
   const int mtiles = (int)(((int64_t)max_q * G + 127) / 128);
   constexpr int smem = Cfg<D>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(prefill_mod_kernel<D>,
+  cudaError_t e = cudaFuncSetAttribute(prefill_mod_kernel<D, Mod>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   Args a;
@@ -811,7 +813,7 @@ cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, con
   a.ws_o = num_splits > 1 ? ws_o : nullptr, a.ws_lse = ws_lse;
   a.err = s.err_word;
   const dim3 grid((unsigned)(mtiles * num_splits), (unsigned)c.num_kv_heads, (unsigned)s.batch);
-  prefill_mod_kernel<D><<<grid, kThreads, smem, stream>>>(map, a, mod);
+  prefill_mod_kernel<D, Mod><<<grid, kThreads, smem, stream>>>(map, a, mod);
   if ((e = cudaGetLastError()) != cudaSuccess || num_splits == 1) return e;
   const int per_block = num_splits > 8 ? 1 : kMergeThreads / 32;
   cudaLaunchConfig_t cfg = {};
@@ -874,10 +876,12 @@ cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, const vo
                                float *ws_lse, cudaStream_t stream, const ScoreMod &mod) {
   if (num_splits < 1 || num_splits > kMaxSplits || (num_splits > 1 && (!ws_o || !ws_lse)))
     return cudaErrorInvalidValue;
-  return c.head_dim == 256 ? launch_d<256>(c, s, q, cu_q, 0, total_q, max_q, Hq, sm_scale, out,
-                                           num_splits, ws_o, ws_lse, stream, mod)
-                           : launch_d<128>(c, s, q, cu_q, 0, total_q, max_q, Hq, sm_scale, out,
-                                           num_splits, ws_o, ws_lse, stream, mod);
+  return with_mod(mod, [&](const auto &m) {
+    return c.head_dim == 256 ? launch_d<256>(c, s, q, cu_q, 0, total_q, max_q, Hq, sm_scale, out,
+                                             num_splits, ws_o, ws_lse, stream, m)
+                             : launch_d<128>(c, s, q, cu_q, 0, total_q, max_q, Hq, sm_scale, out,
+                                             num_splits, ws_o, ws_lse, stream, m);
+  });
 }
 
 // A decode step of T queries per sequence (T * Hq/Hkv <= 128 rows, one query
@@ -891,10 +895,12 @@ cudaError_t launch_decode_rows(const nvkv_cache &c, const nvkv_seqs &s, const vo
   const int room = (int)(slots / n < kMaxStepSplits ? slots / n : kMaxStepSplits);
   const int S = estimate_splits(n, visible_keys(s, mod, T), (int64_t)total_q * Hq * c.head_dim,
                                 false, room > 1 ? room : 1, sms);
-  return c.head_dim == 256 ? launch_d<256>(c, s, q, nullptr, T, total_q, T, Hq, sm_scale, out, S,
-                                           ws_o, ws_lse, stream, mod)
-                           : launch_d<128>(c, s, q, nullptr, T, total_q, T, Hq, sm_scale, out, S,
-                                           ws_o, ws_lse, stream, mod);
+  return with_mod(mod, [&](const auto &m) {
+    return c.head_dim == 256 ? launch_d<256>(c, s, q, nullptr, T, total_q, T, Hq, sm_scale, out, S,
+                                             ws_o, ws_lse, stream, m)
+                             : launch_d<128>(c, s, q, nullptr, T, total_q, T, Hq, sm_scale, out, S,
+                                             ws_o, ws_lse, stream, m);
+  });
 }
 
 }  // namespace nvkv
