@@ -213,12 +213,15 @@ nvkv_status check_mod(const nvkv_score_mod *mod, ScoreMod &m) {
     return NVKV_ERR_INVALID_ARG;
   m.cap2 = mod->softcap * kLog2e;
   m.cap_in = mod->softcap > 0.f ? 2.f * kLog2e / m.cap2 : 0.f;
-  m.cap_u = mod->softcap > 0.f ? 1.f / m.cap2 : 0.f;
-  // kCapSmall's polynomial of tanh
-  const double tanh_poly[5] = {0.9999972283, -0.3332307647, 0.1322609151, -0.04928044419, 0.01231882928};
-  for (int i = 0; i < 5; ++i) m.poly[i] = (float)(tanh_poly[i] * m.cap2);
-  if (!std::isfinite(m.cap2) || !std::isfinite(m.cap_in) || !std::isfinite(m.cap_u * 16384.f))
-    return NVKV_ERR_INVALID_ARG;
+  // kCapSmall's polynomial of tanh, in the score instead of score / cap2
+  const double tanh_poly[5] = {0.9999972283, -0.3332307647, 0.1322609151, -0.04928044419,
+                               0.01231882928};
+  double scale = 1.0;
+  for (int i = 0; i < 5; ++i) {
+    m.poly[i] = (float)(tanh_poly[i] * scale);
+    if (m.cap2 > 0.f) scale /= (double)m.cap2 * (double)m.cap2;
+  }
+  if (!std::isfinite(m.cap2) || !std::isfinite(m.cap_in)) return NVKV_ERR_INVALID_ARG;
   m.window = mod->window;
   m.slopes = mod->alibi_slopes;
   m.prefix = mod->prefix_lens;

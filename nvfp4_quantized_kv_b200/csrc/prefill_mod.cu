@@ -15,21 +15,32 @@
 // overwrites its own S slot as the A operand of O += P V (N = D), O stays in
 // Tensor Memory.
 //
-// The tile's time is set by the softmax: with one thread for a row's 64
-// scores and one such warp on each SM sub-partition, the tile took 3,900
-// cycles of that warp (a clock64 trace), while K (1,000), V (1,000 with 8
-// warps, 2,700 with 4) and the MMAs (1,800) waited. So two warpgroups share
-// every tile, 32 keys each; the two threads of a row agree on its running
-// maximum only when a score may pass it by 2^8, which one barrier of their
-// two warps detects (it also keeps P from overwriting scores not yet read).
+// Roles, and what set the pace before each of them (clock64 traces, cycles a
+// tile at head_dim 256 with a cap):
+//  * With one thread for a row's 64 scores, and one such warp on each SM
+//    sub-partition, the softmax took 3,900. Two warpgroups share every tile,
+//    32 keys each; the two threads of a row agree on its running maximum only
+//    when a score may pass it by 2^8, which one barrier of their two warps
+//    detects (it also keeps P from overwriting scores not yet read).
+//  * K and V have warps of their own (4 and 8: V's 8 take 1,100, 4 took
+//    2,700).
+//  * One thread for all MMAs, polling for whichever could go, held a tile's
+//    value MMAs back behind the next tile's scores (issuing a batch blocks
+//    until it has nearly executed), and with them the S slot that the scores
+//    after those wait for: 3,200. Two issuing threads: 2,700, of which the
+//    softmax is busy 2,400.
+// Not faster: four softmax warpgroups, on one tile or in pairs on two; 8 warps
+// for K; integer instead of converting dequantisation.
 //   warps  0.. 3  K tile: a token a thread, D/64 chunks of 32 elements
 //   warps  4..11  V^T tile: a head_dim row a thread, D/64 pages
 //   warps 12..15  softmax of the tile's keys  0..31: a query row a thread
 //   warps 16..19  softmax of the tile's keys 32..63
 //   warp  20      TMA: the tile's 4 page blocks into a 4-stage ring
-//   warp  21      issues the MMAs (one thread, event-driven)
+//   warps 21, 22  issue the score and the value MMAs (one thread each)
 // Warps 4..19 write the output. Every wait is bounded; a timeout sets
-// NVKV_DEVERR_TIMEOUT and drains.
+// NVKV_DEVERR_TIMEOUT and drains. The long prefill (65,536 + 2,048 tokens,
+// 24/4 heads, head_dim 256, cap 50): 4.01 ms = 836 TFLOP/s, 0.50 of the
+// measured matrix rate.
 #include "score_mod.cuh"
 #include "sm100.cuh"
 
@@ -49,12 +60,12 @@ constexpr int kVWarps = 8;        // warps 4..11
 constexpr int kDeqWarps = kKWarps + kVWarps;
 constexpr int kSmxWarps = 8;      // two warpgroups: warps 12..15 and 16..19
 constexpr int kProducerWarp = 20;
-constexpr int kMmaWarp = 21;
-constexpr int kThreads = 22 * 32;
+constexpr int kMmaWarp = 21;      // issues the score MMAs
+constexpr int kPvWarp = 22;       // issues the value MMAs
+constexpr int kThreads = 23 * 32;
 constexpr int kHalf = kTileTokens / 2;  // keys of a softmax thread
 constexpr uint32_t kTmemCols = 512;
 constexpr long long kWaitBudget = 2000000000LL;
-constexpr unsigned kPollSleepNs = 100;  // of the MMA thread after an idle poll
 constexpr float kLazyRescale = 8.0f;
 
 // Tensor Memory columns (head_dim 128 uses half of Q's and O's).
@@ -84,13 +95,16 @@ struct Cfg {
   static constexpr int kOffPres = kOffPages + kStages * kTilePages * 4;  // u32[4]
   static constexpr int kOffFlags = kOffPres + 16;
   static constexpr int kOffBars = kOffFlags + 16;
-  // full, empty; kready, vready, sready, pready, pvdone; qready, final, lready
-  static constexpr int kNumBars = 2 * kStages + 2 * 5 + 3;
+  // full, empty; kready, vready, sready, pready, pvdone; qready, final, lready, final_qk
+  static constexpr int kNumBars = 2 * kStages + 2 * 5 + 4;
   static constexpr int kOffTmem = kOffBars + kNumBars * 8;
   static constexpr int kSmemBytes = kOffTmem + 16 + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(kOffK % 1024 == 0 && kOffPages % 16 == 0 && kOffBars % 8 == 0, "alignment");
 };
+
+// Keeps what follows out of the way of the instructions that always run.
+__device__ __forceinline__ bool rare(bool b) { return __builtin_expect(b, 0); }
 
 __device__ __forceinline__ int swz(int off) { return off ^ ((off >> 3) & 0x70); }
 
@@ -167,7 +181,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   uint64_t *full = bars, *empty = bars + kStages;
   uint64_t *kready = bars + 2 * kStages, *vready = kready + 2, *sready = kready + 4,
            *pready = kready + 6, *pvdone = kready + 8, *qready = kready + 10,
-           *final_bar = kready + 11, *lready = kready + 12;
+           *final_bar = kready + 11, *lready = kready + 12, *final_qk = kready + 13;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffTmem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -214,6 +228,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     }
     mbar_init(qready, 4);
     mbar_init(final_bar, 1);
+    mbar_init(final_qk, 1);
     mbar_init(lready, kSmxWarps);
     fence_mbar_init();
   }
@@ -269,58 +284,60 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
           mbar_wait(&full[k % kStages], (k / kStages) & 1, kWaitBudget);
       }
       __syncwarp();
-    } else if (warp == kMmaWarp && lane == 0 && ntiles > 0) {
+    } else if (lane == 0 && ntiles > 0) {
       // ---------------------------------------------------------------- MMA
-      const uint32_t idesc_qk = idesc_f16_f32(128, kTileTokens, false, false);
-      const uint32_t idesc_pv = idesc_f16_f32(128, D, false, false);
-      const uint32_t kb = smem_u32(ktiles), vb = smem_u32(vtiles);
-      wait_bar(qready, 0, flags, a.err);
-      tc_fence_after();
-      int qk = 0, pv = 0;
-      bool issued = false;
-      long long t_last = clock64();
-      while (pv < ntiles && !flags[2]) {
-        bool progress = false;
-        if (pv < qk && mbar_test(&pready[pv & 1], (pv >> 1) & 1) &&
-            mbar_test(&vready[pv & 1], (pv >> 1) & 1)) {
+      // Two issuing threads: issuing a batch of tcgen05.mma blocks the thread
+      // until it has nearly executed, so a single one held the value MMAs of
+      // a tile back behind the next tile's scores, and with them the S slot
+      // that the scores after those wait for.
+      if (warp == kMmaWarp) {
+        const uint32_t idesc_qk = idesc_f16_f32(128, kTileTokens, false, false);
+        const uint32_t kb = smem_u32(ktiles);
+        bool issued = false;
+        wait_bar(qready, 0, flags, a.err);
+        for (int j = 0; j < ntiles && !flags[2]; ++j) {
+          const int slot = j & 1;
+          wait_bar(&kready[slot], (j >> 1) & 1, flags, a.err);
+          // the S slot: P of tile j-2 there has been used
+          if (j >= 2) wait_bar(&pvdone[slot], ((j >> 1) + 1) & 1, flags, a.err);
           tc_fence_after();
-          const uint32_t pcol = tmem + kColS + (pv & 1) * 64;  // P: first 32 columns of the slot
-          const uint32_t vt = vb + (pv & 1) * kVTileBytes;
-#pragma unroll
-          for (int ks = 0; ks < kTileTokens / 16; ++ks) {
-            const uint64_t bd = smem_desc(vt + ks * 2 * (D * 16), D * 16, 128);
-            mma_f16_ts(tmem + kColO, pcol + ks * 8, bd, idesc_pv, (pv > 0 || ks > 0) ? 1u : 0u);
-          }
-          mma_commit(&pvdone[pv & 1]);
-          ++pv;
-          progress = issued = true;
-        } else if (qk < ntiles && (qk < 2 || mbar_test(&pvdone[qk & 1], ((qk >> 1) + 1) & 1)) &&
-                   mbar_test(&kready[qk & 1], (qk >> 1) & 1)) {
-          tc_fence_after();
-          const uint32_t kt = kb + (qk & 1) * kKTileBytes;
-          const uint32_t scol = tmem + kColS + (qk & 1) * 64;
+          const uint32_t kt = kb + slot * kKTileBytes;
+          const uint32_t scol = tmem + kColS + slot * 64;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint64_t bd = smem_desc(kt + ks * 2 * 1024, 1024, 128);
             mma_f16_ts(scol, tmem + kColQ + ks * 8, bd, idesc_qk, ks > 0 ? 1u : 0u);
           }
-          mma_commit(&sready[qk & 1]);
-          ++qk;
-          progress = issued = true;
+          mma_commit(&sready[slot]);
+          issued = true;
         }
-        if (progress) {
-          t_last = clock64();
-        } else {
-          if (clock64() - t_last > kWaitBudget) {
-            flags[2] = 1;
-            report(a.err, NVKV_DEVERR_TIMEOUT);
+        if (issued) {
+          mma_commit(final_qk);
+          mbar_wait(final_qk, 0, kWaitBudget);
+        }
+      } else {
+        const uint32_t idesc_pv = idesc_f16_f32(128, D, false, false);
+        const uint32_t vb = smem_u32(vtiles);
+        bool issued = false;
+        for (int j = 0; j < ntiles && !flags[2]; ++j) {
+          const int slot = j & 1;
+          wait_bar(&vready[slot], (j >> 1) & 1, flags, a.err);
+          wait_bar(&pready[slot], (j >> 1) & 1, flags, a.err);
+          tc_fence_after();
+          const uint32_t pcol = tmem + kColS + slot * 64;  // P: first 32 columns of the slot
+          const uint32_t vt = vb + slot * kVTileBytes;
+#pragma unroll
+          for (int ks = 0; ks < kTileTokens / 16; ++ks) {
+            const uint64_t bd = smem_desc(vt + ks * 2 * (D * 16), D * 16, 128);
+            mma_f16_ts(tmem + kColO, pcol + ks * 8, bd, idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
           }
-          __nanosleep(kPollSleepNs);
+          mma_commit(&pvdone[slot]);
+          issued = true;
         }
-      }
-      if (issued) {
-        mma_commit(final_bar);
-        mbar_wait(final_bar, 0, kWaitBudget);
+        if (issued) {
+          mma_commit(final_bar);
+          mbar_wait(final_bar, 0, kWaitBudget);
+        }
       }
     }
   } else if (warp < kDeqWarps) {
@@ -434,7 +451,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
           const int ptok = tok0 + p * kPageTokens;
           const int mine = p == 0 ? pg4.x : p == 1 ? pg4.y : p == 2 ? pg4.z : pg4.w;
           uint32_t o8[8];
-          if (mine >= 0) {
+          if (!rare(mine < 0)) {
             const uint4 *tb = reinterpret_cast<const uint4 *>(
                 vsc + ((slot * kTilePages + p) * (D / 16) + g) * 8);
             const uint4 sa = tb[0], sb = tb[1];
@@ -444,7 +461,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
             e2m1x8_to_f16x2x4(cw[pp].y, c1);
 #pragma unroll
             for (int e = 0; e < 8; ++e) o8[e] = hmul2_u32(e < 4 ? c0[e] : c1[e - 4], sp[e]);
-            if (ptok < key_lo || ptok + kPageTokens > key_hi) {
+            if (rare(ptok < key_lo || ptok + kPageTokens > key_hi)) {
               // tokens that no row sees are zero, whatever their bytes
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -540,10 +557,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         // A polynomial, good for scores of at most 0.75 caps and increasing
         // beyond: its own values tell whether all of them are. Where one is
         // not, the exact form (two special functions a score).
-        const float2 us = make_float2(mod.cap_u, mod.cap_u);
 #pragma unroll
         for (int e = 0; e < kHalf; e += 2) {
-          const float2 v = cap_small(mod, mul_f32x2(make_float2(x[e], x[e + 1]), us));
+          const float2 v = cap_small(mod, make_float2(x[e], x[e + 1]));
           x[e] = v.x, x[e + 1] = v.y;
         }
         float t0 = max3_abs(x[0], x[1], x[2]), t1 = max3_abs(x[3], x[4], x[5]);
@@ -553,7 +569,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
           t1 = max3_abs(t1, x[e + 2], x[e + 3]);
         }
         above = max3_abs(t0, t1, max3_abs(x[30], x[31], 0.f));
-        if (__any_sync(0xffffffffu, !(above <= kCapSmallTanh * mod.cap2))) {  // (a NaN too)
+        if (rare(__any_sync(0xffffffffu, !(above <= kCapSmallTanh * mod.cap2)))) {  // (a NaN too)
           load_scores();
 #pragma unroll
           for (int e = 0; e < kHalf; ++e) x[e] = mod.cap(x[e]);
@@ -569,13 +585,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         for (int e = 0; e < kHalf; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), x[e]);
         above = top_score();
       }
-      if (key0 < row_lo || key0 + kHalf > row_hi) {
+      if (rare(key0 < row_lo || key0 + kHalf > row_hi)) {
 #pragma unroll
         for (int e = 0; e < kHalf; ++e)
           if (key0 + e < row_lo || key0 + e >= row_hi) x[e] = -INFINITY;
       }
       const uint32_t here = present[j & 3] >> (2 * hf);
-      if ((here & 3u) != 3u) {
+      if (rare((here & 3u) != 3u)) {
 #pragma unroll
         for (int e = 0; e < kHalf; ++e)
           if (!((here >> (e / kPageTokens)) & 1u)) x[e] = -INFINITY;
@@ -583,7 +599,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       // One barrier of the two warps that share these rows: may any score
       // pass its row's running maximum by 2^8? (Every score of the tile has
       // been read once it is passed.)
-      if (named_barrier_or(2 + lq, 64, above > m + kLazyRescale)) {
+      if (rare(named_barrier_or(2 + lq, 64, above > m + kLazyRescale))) {
         // The exact maximum of the row's visible scores decides; both threads
         // of the row come to the same result.
         red_s[128 * hf + r] = top_score();
@@ -617,9 +633,11 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         }
         named_barrier(2 + lq, 64);  // the maxima have been read
       }
-      // Weights in f16, two per exponential instruction; masked keys are
-      // -inf and give 0 (a row with no visible key yet keeps m = -inf: it
-      // subtracts 0 instead). The denominator sums the same f16 weights.
+      // Weights from an fp32 exponential (as fast here as the f16 pair form,
+      // whose results have to be widened again for the sum), rounded to f16
+      // for the value MMAs; masked keys are -inf and give 0 (a row with no
+      // visible key yet keeps m = -inf: it subtracts 0 instead). The
+      // denominator sums the weights before their rounding, in fp32.
       const float ms = m == -INFINITY ? 0.f : m;
       uint32_t pw[kHalf / 2];
       float2 lv0 = make_float2(0.f, 0.f), lv1 = make_float2(0.f, 0.f);

@@ -59,8 +59,7 @@ struct ScoreMod {
   static constexpr bool kOn = true, kCap = true, kBias = false;
   float cap2;             // cap * log2 e; 0 = no cap
   float cap_in;           // 2 log2 e / cap2: the exponent of exp(2 x / cap2), base 2
-  float cap_u;            // 1 / cap2
-  float poly[5];          // cap_small's coefficients, times cap2
+  float poly[5];          // cap_small's coefficients, times cap2^(-2i)
   int window;             // 0 = none
   const float *slopes;    // [Hq] or null
   const int32_t *prefix;  // [batch] or null
@@ -91,18 +90,18 @@ struct ScoreMod {
 // tanh(u) = u P(u^2) for |u| <= kCapSmall, off by at most 1.9e-7 (a degree-9
 // odd polynomial, least maximum error by reweighted least squares over the
 // interval), and increasing for every u, so that a result of at most
-// kCapSmallTanh * cap2 shows that u was in the interval: 3.5 packed multiply-adds a score and none of the two special
+// kCapSmallTanh * cap2 shows that u was in the interval: 3 packed multiply-adds a score and none of the two special
 // functions of cap(), which take 16 issue cycles a warp.
 constexpr float kCapSmall = 0.75f;
 constexpr float kCapSmallTanh = 0.635148f;  // tanh(0.75), rounded down
 
-// cap() of two scores given u = score / cap2, |u| <= kCapSmall.
-__device__ __forceinline__ float2 cap_small(const ScoreMod &m, float2 u) {
-  const float2 v = mul_f32x2(u, u);
+// cap() of two scores x with |x| <= kCapSmall * cap2: x P((x / cap2)^2).
+__device__ __forceinline__ float2 cap_small(const ScoreMod &m, float2 x) {
+  const float2 v = mul_f32x2(x, x);
   float2 p = make_float2(m.poly[4], m.poly[4]);
 #pragma unroll
   for (int i = 3; i >= 0; --i) p = fma_f32x2(p, v, make_float2(m.poly[i], m.poly[i]));
-  return mul_f32x2(p, u);
+  return mul_f32x2(p, x);
 }
 
 // A ScoreMod whose call is known to cap, or to bias, its scores or not to. The
