@@ -461,9 +461,9 @@ def _arg(t: torch.Tensor, dtype: torch.dtype, device: int, n: int, name: str) ->
 def _on(cache: Cache, seqs: Seqs) -> int:
     """The device index of a call's cache and sequences."""
     device = cache.pool.get_device()
-    for t, name in ((seqs.page_table, "page_table"), (seqs.kv_lens, "kv_lens")):
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {cache.pool.device}")
+    if seqs.page_table.get_device() != device or seqs.kv_lens.get_device() != device:
+        raise ValueError(f"the page table is on {seqs.page_table.device}, kv_lens on "
+                         f"{seqs.kv_lens.device}, the cache on {cache.pool.device}")
     return device
 
 
@@ -525,7 +525,7 @@ def nvkv_decode_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, T: int, num_
     """Decode attention of T queries per sequence with the scores and masks of
     mod, merged into out (bf16 [batch*T][Hq][D]); workspace as for
     nvkv_decode_attn.  For caches of either format."""
-    device, L = _on(cache, seqs), library()
+    device, L = _on(cache, seqs), _lib or library()
     n = seqs.batch * T * num_q_heads * cache.head_dim
     fn = L.nvkv_decode_attn_mod_k8v4 if cache.kv_format == "k8v4" else L.nvkv_decode_attn_mod
     _call(device, fn, "nvkv_decode_attn_mod", stream, ctypes.byref(cache._c),
@@ -543,7 +543,7 @@ def nvkv_prefill_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, cu_q: torch
     workspace as for nvkv_prefill_attn_split (0 splits: as many of the
     automatic count as the workspace has room for).  For caches of either
     format."""
-    device, L = _on(cache, seqs), library()
+    device, L = _on(cache, seqs), _lib or library()
     n = total_q * num_q_heads * cache.head_dim
     fn = L.nvkv_prefill_attn_mod_k8v4 if cache.kv_format == "k8v4" else L.nvkv_prefill_attn_mod
     ws, size = None, 0
@@ -567,30 +567,32 @@ def nvkv_append_rope_axes(cache: Cache, seqs: Seqs, k_new: torch.Tensor, v_new: 
     (bf16 [total_new][Hq][D]) is rotated into q_out in the same launch."""
     _fmt(cache, "nvfp4", "nvkv_append_rope_axes")
     device = _on(cache, seqs)
-    if positions.dim() != 2 or positions.shape[1] != total_new:
+    pos_shape, cs_shape = positions.shape, rope_cs.shape
+    if len(pos_shape) != 2 or pos_shape[1] != total_new:
         raise ValueError("positions must be [num_axes][total_new]")
-    if rope_cs.dim() != 3 or rope_cs.shape[1] * 2 != rotary_dim or rope_cs.shape[2] != 2:
+    if len(cs_shape) != 3 or cs_shape[1] * 2 != rotary_dim or cs_shape[2] != 2:
         raise ValueError("rope_cs must be [max_pos][rotary_dim/2][2]")
     if len(axis_of_pair) * 2 != rotary_dim:
         raise ValueError("axis_of_pair must have rotary_dim/2 entries")
     n = total_new * cache.num_kv_heads * cache.head_dim
     hq, qp, qo = 0, None, None
     if q is not None and q_out is not None:
-        if q.dim() != 3 or q.shape[0] != total_new or q.shape[2] != cache.head_dim:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != total_new or q_shape[2] != cache.head_dim:
             raise ValueError("q must be [total_new][Hq][D]")
-        if q_out.shape != q.shape:
+        if q_out.shape != q_shape:
             raise ValueError("q_out must have the shape of q")
-        hq = q.shape[1]
+        hq = q_shape[1]
         qp, qo = _arg(q, torch.bfloat16, device, 0, "q"), _arg(q_out, torch.bfloat16, device, 0, "q_out")
     elif q is not None or q_out is not None:
         raise ValueError("q and q_out go together")
-    _call(device, library().nvkv_append_rope_axes, "nvkv_append_rope_axes", stream,
+    _call(device, (_lib or library()).nvkv_append_rope_axes, "nvkv_append_rope_axes", stream,
           ctypes.byref(cache._c), ctypes.byref(seqs._c),
           _arg(k_new, torch.bfloat16, device, n, "k_new"),
           _arg(v_new, torch.bfloat16, device, n, "v_new"),
           _arg(cu_new, torch.int32, device, seqs.batch + 1, "cu_new"), total_new, max_new,
-          _arg(rope_cs, torch.float32, device, 0, "rope_cs"), rope_cs.shape[0], rotary_dim,
-          _arg(positions, torch.int32, device, 0, "positions"), positions.shape[0],
+          _arg(rope_cs, torch.float32, device, 0, "rope_cs"), cs_shape[0], rotary_dim,
+          _arg(positions, torch.int32, device, 0, "positions"), pos_shape[0],
           bytes(axis_of_pair), qp, hq, qo)
 
 
@@ -600,7 +602,7 @@ def nvkv_read_rows(cache: Cache, seqs: Seqs, starts: torch.Tensor, cu_rows: torc
     """The cached K and V rows of positions starts[b] .. of every sequence as
     bf16, rows cu_rows[b] .. cu_rows[b+1]-1 of k_out and v_out
     ([total_rows][Hkv][D]).  For caches of either format."""
-    device, L = _on(cache, seqs), library()
+    device, L = _on(cache, seqs), _lib or library()
     n = total_rows * cache.num_kv_heads * cache.head_dim
     _call(device, L.nvkv_read_rows_k8v4 if cache.kv_format == "k8v4" else L.nvkv_read_rows,
           "nvkv_read_rows", stream, ctypes.byref(cache._c), ctypes.byref(seqs._c),

@@ -97,7 +97,7 @@ cudaError_t launch_combine(const nvkv_seqs &s, const void *ws_o, const void *ws_
 // arithmetic, over the units that the queries can see.  kW warps share a row:
 // a row of a single long sequence is cut into as many as half the splits of
 // the GPU, and one warp walking them, one dependent load after the other,
-// took 27 us where 8 warps take 4 (64 splits of 4,096 tokens, head_dim 128).
+// took 27 us (32 ranges of 4,096 tokens, head_dim 128).
 // Few splits a row (a batch) leave each warp a row of its own.  Each warp
 // sums the splits w, w + kW, ...; the warps' sums are added in order, so the
 // result does not depend on timing.  Started while the attention kernel
@@ -135,41 +135,45 @@ combine_mod_kernel(const int32_t *__restrict__ kv_lens, int B, int Hkv, int T, i
   U *= Hkv;
   const int units = live ? mod.units(kv_lens, b, T) : 0;
   const int64_t pair_start = before * Hkv + (int64_t)h * units;
+  // (the masked attention deals U units to min(S, U) ranges: none is empty)
+  const int64_t Se = split_ranges(U, S);
   int64_t c0 = 0, c1 = -1;
   if (units > 0) {
-    c0 = range_of_unit(pair_start, U, S);
-    c1 = range_of_unit(pair_start + units - 1, U, S);
+    c0 = range_of_unit(pair_start, U, Se);
+    c1 = range_of_unit(pair_start + units - 1, U, Se);
   }
-  // A range that owns no unit (possible only when U < S) wrote nothing.
-  auto owns = [&](int64_t c) {
-    return U >= S || range_begin(c, U, S) != range_begin(c + 1, U, S);
-  };
   sm100::grid_dependency_wait();
 
+  const float *lse = ws_lse + (size_t)bh * R + r;
   float mx = -INFINITY;
-  for (int64_t c = c0 + lane; c <= c1; c += 32)
-    if (owns(c)) mx = fmaxf(mx, ws_lse[(size_t)(c + bh) * R + r]);
+  for (int64_t c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, lse[(size_t)c * R]);
   mx = warp_max(mx);
   const int dpl = D / 32;  // channels of a lane: 4 or 8
   float acc[8], wsum = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   if (mx > -INFINITY) {
+    // 32 of this warp's ranges at a time, their weights one a lane
+    for (int64_t cb = c0 + sub; cb <= c1; cb += 32 * kW) {
+      const int64_t mine = cb + (int64_t)lane * kW;
+      const float my = mine <= c1 ? exp2f(lse[(size_t)mine * R] - mx) : 0.f;  // (2^-inf = 0)
+      const int n = (int)min((int64_t)32, (c1 - cb) / kW + 1);
 #pragma unroll 4
-    for (int64_t c = c0 + sub; c <= c1; c += kW) {  // warp-uniform
-      const float lse = owns(c) ? ws_lse[(size_t)(c + bh) * R + r] : -INFINITY;
-      if (lse == -INFINITY) continue;
-      const float w = exp2f(lse - mx);
-      const float *o = ws_o + ((size_t)(c + bh) * R + r) * (size_t)D + lane * dpl;
-      const float4 a = *reinterpret_cast<const float4 *>(o);
-      acc[0] = fmaf(w, a.x, acc[0]), acc[1] = fmaf(w, a.y, acc[1]);
-      acc[2] = fmaf(w, a.z, acc[2]), acc[3] = fmaf(w, a.w, acc[3]);
-      if (dpl == 8) {
-        const float4 e = *reinterpret_cast<const float4 *>(o + 4);
-        acc[4] = fmaf(w, e.x, acc[4]), acc[5] = fmaf(w, e.y, acc[5]);
-        acc[6] = fmaf(w, e.z, acc[6]), acc[7] = fmaf(w, e.w, acc[7]);
+      for (int k = 0; k < n; ++k) {  // warp-uniform
+        const float w = __shfl_sync(0xffffffffu, my, k);
+        const float *o =
+            ws_o + ((size_t)(cb + k * kW + bh) * R + r) * (size_t)D + lane * dpl;
+        // (a range that saw no key of the row wrote zeros)
+        const float4 a = *reinterpret_cast<const float4 *>(o);
+        acc[0] = fmaf(w, a.x, acc[0]), acc[1] = fmaf(w, a.y, acc[1]);
+        acc[2] = fmaf(w, a.z, acc[2]), acc[3] = fmaf(w, a.w, acc[3]);
+        if (dpl == 8) {
+          const float4 e = *reinterpret_cast<const float4 *>(o + 4);
+          acc[4] = fmaf(w, e.x, acc[4]), acc[5] = fmaf(w, e.y, acc[5]);
+          acc[6] = fmaf(w, e.z, acc[6]), acc[7] = fmaf(w, e.w, acc[7]);
+        }
+        wsum += w;
       }
-      wsum += w;
     }
   }
   if constexpr (kW > 1) {

@@ -272,7 +272,10 @@ __device__ void list_segments(const Mod &mod, const int32_t *kv_lens, int B, int
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
   U *= Hkv;
-  const int64_t u0 = U > 0 ? range_begin(c, U, S) : 0, u1 = U > 0 ? range_begin(c + 1, U, S) : 0;
+  // (splits past the last range have nothing to do)
+  const int64_t Se = plan_ranges<Mod>(U, S);
+  const int64_t u0 = c < Se ? range_begin(c, U, Se) : 0;
+  const int64_t u1 = c < Se ? range_begin(c + 1, U, Se) : 0;
   if (lane == 0) head->u0 = u0, head->u1 = u1;
   int64_t acc = 0;  // first unit of sequence b0
   int count = 0;

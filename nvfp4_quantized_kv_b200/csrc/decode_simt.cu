@@ -173,7 +173,9 @@ decode_simt_kernel(const uint8_t *__restrict__ pool, int num_pages, int Hkv, int
 
   const int64_t U = total_units(mod, kv_lens, B, Hkv, T);
   if (U == 0) return;
-  const int64_t u0 = range_begin(c, U, S), u1 = range_begin(c + 1, U, S);
+  const int64_t Se = plan_ranges<Mod>(U, S);
+  if (c >= Se) return;
+  const int64_t u0 = range_begin(c, U, Se), u1 = range_begin(c + 1, U, Se);
   int64_t u = u0;
   while (u < u1) {
     int b, h, units;

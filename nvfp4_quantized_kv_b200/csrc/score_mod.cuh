@@ -126,6 +126,17 @@ auto with_mod(const ScoreMod &m, F &&f) {
   return m.slopes ? as(ScoreModOf<false, true>{}) : as(ScoreModOf<false, false>{});
 }
 
+// Ranges that the split plan of U units really has: the masked attention deals
+// them to at most U of the S splits, so that every range owns a unit and the
+// merge meets no empty one; the plain plan has S.
+template <class Mod>
+__host__ __device__ __forceinline__ int64_t plan_ranges(int64_t U, int64_t S) {
+  return Mod::kOn && U < S ? U : S;
+}
+__host__ __device__ __forceinline__ int64_t split_ranges(int64_t U, int64_t S) {
+  return plan_ranges<ScoreMod>(U, S);
+}
+
 // locate_pair over the units that a Mod's queries can see (T: queries per
 // sequence of the whole step).
 template <class Mod>
