@@ -139,8 +139,8 @@ combine_mod_kernel(const int32_t *__restrict__ kv_lens, int B, int Hkv, int T, i
   const int64_t Se = split_ranges(U, S);
   int64_t c0 = 0, c1 = -1;
   if (units > 0) {
-    c0 = range_of_unit(pair_start, U, Se);
-    c1 = range_of_unit(pair_start + units - 1, U, Se);
+    c0 = range_of_unit_mod(pair_start, U, Se);
+    c1 = range_of_unit_mod(pair_start + units - 1, U, Se);
   }
   sm100::grid_dependency_wait();
 

@@ -274,8 +274,8 @@ __device__ void list_segments(const Mod &mod, const int32_t *kv_lens, int B, int
   U *= Hkv;
   // (splits past the last range have nothing to do)
   const int64_t Se = plan_ranges<Mod>(U, S);
-  const int64_t u0 = c < Se ? range_begin(c, U, Se) : 0;
-  const int64_t u1 = c < Se ? range_begin(c + 1, U, Se) : 0;
+  const int64_t u0 = c < Se ? range_begin_mod(c, U, Se) : 0;
+  const int64_t u1 = c < Se ? range_begin_mod(c + 1, U, Se) : 0;
   if (lane == 0) head->u0 = u0, head->u1 = u1;
   int64_t acc = 0;  // first unit of sequence b0
   int count = 0;
@@ -293,8 +293,13 @@ __device__ void list_segments(const Mod &mod, const int32_t *kv_lens, int B, int
     // heads h0 .. h1 of this sequence have units in [u0, u1)
     int h0 = 0, h1 = -1;
     if (n > 0 && start < u1 && start + (int64_t)n * Hkv > u0) {
-      h0 = start < u0 ? (int)((u0 - start) / n) : 0;
-      h1 = (int)((min(u1, start + (int64_t)n * Hkv) - 1 - start) / n);
+      // (a range's share of one sequence: below 2^31 units unless the batch's
+      // keys pass 2^38)
+      auto head = [&](int64_t at) {
+        return at >> 31 ? (int)(at / n) : (int)((uint32_t)at / (uint32_t)n);
+      };
+      h0 = start < u0 ? head(u0 - start) : 0;
+      h1 = head(min(u1, start + (int64_t)n * Hkv) - 1 - start);
     }
     int at = h1 - h0 + 1;  // inclusive scan of the counts
 #pragma unroll
@@ -846,7 +851,12 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           const uint32_t sb = (uint32_t)__nv_cvt_float_to_fp8(ga * (1.0f / 6.0f), __NV_SATFINITE,
                                                               __NV_E4M3);
           const float sv = e4m3_to_float((uint8_t)sb);
-          const float rs = sv > 0.f ? 1.0f / sv : 0.f;
+          float rs;
+          if constexpr (Mod::kOn)  // (it only picks the codes; a division's chain is 100 cycles)
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(sv));
+          else
+            rs = 1.0f / sv;
+          rs = sv > 0.f ? rs : 0.f;
           uint32_t codes = 0;
 #pragma unroll
           for (int i = 0; i < kE / 2; ++i) {

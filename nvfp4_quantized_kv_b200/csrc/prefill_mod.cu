@@ -100,6 +100,7 @@ struct Cfg {
   static constexpr int kOffTmem = kOffBars + kNumBars * 8;
   static constexpr int kSmemBytes = kOffTmem + 16 + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(128 * (4 * D + 16) <= kOffVsc, "the output rows fit below the tables");
   static_assert(kOffK % 1024 == 0 && kOffPages % 16 == 0 && kOffBars % 8 == 0, "alignment");
 };
 
@@ -226,7 +227,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       mbar_init(&pready[i], kSmxWarps);
       mbar_init(&pvdone[i], 1);
     }
-    mbar_init(qready, 4);
+    mbar_init(qready, 16);
     mbar_init(final_bar, 1);
     mbar_init(final_qk, 1);
     mbar_init(lready, kSmxWarps);
@@ -241,6 +242,42 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+
+  if (warp >= kKWarps && warp < kProducerWarp) {
+    // Q row -> Tensor Memory (A operand), f16, scaled to base-2 scores: 16
+    // warps, lane quarter warp % 4, a quarter of the columns each, so that a
+    // thread's loads are one latency. (Four warps with all columns had Q ready
+    // 3,000 to 6,000 cycles later.)
+    const int lq = warp & 3, part = (warp - kKWarps) >> 2;
+    const int gr = 128 * mt + 32 * lq + lane;
+    const bool valid = gr < rows && !bad;
+    const __nv_bfloat16 *qr =
+        a.q + ((size_t)(q0 + gr / G) * a.Hq + h * G + gr % G) * D + part * (D / 4);
+    uint4 raw[D / 32];
+#pragma unroll
+    for (int v = 0; v < D / 32; ++v)
+      raw[v] = valid ? __ldg(reinterpret_cast<const uint4 *>(qr) + v) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int c16 = 0; c16 < D / 128; ++c16) {
+      uint32_t w[16];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const uint4 r4 = raw[4 * c16 + v];
+        const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 hh = __floats2half2_rn(__uint_as_float(rw[e] << 16) * a.qscale,
+                                               __uint_as_float(rw[e] & 0xffff0000u) * a.qscale);
+          w[4 * v + e] = *reinterpret_cast<const uint32_t *>(&hh);
+        }
+      }
+      tmem_st16(tmem + ((uint32_t)(32 * lq) << 16) + kColQ + part * (D / 8) + c16 * 16, w);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(qready);
+  }
 
   if (warp >= kProducerWarp) {
     if (warp == kProducerWarp) {
@@ -501,32 +538,6 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       key_range(pos, kv_len, start_of(i), mod.window, prefix, row_lo, row_hi);
       slope2 = mod.slope2(h * G + g);
     }
-    // Q row -> Tensor Memory (A operand), f16, pre-scaled to base-2 scores.
-    if (hf == 0) {
-      const __nv_bfloat16 *qr = a.q + ((size_t)(q0 + i) * a.Hq + h * G + g) * D;
-#pragma unroll
-      for (int c32 = 0; c32 < D / 64; ++c32) {
-        uint32_t w[32];
-#pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          uint4 raw = make_uint4(0, 0, 0, 0);
-          if (valid) raw = *reinterpret_cast<const uint4 *>(qr + c32 * 64 + v * 8);
-          const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            __half2 hh = __floats2half2_rn(__uint_as_float(rw[e] << 16) * a.qscale,
-                                           __uint_as_float(rw[e] & 0xffff0000u) * a.qscale);
-            w[4 * v + e] = *reinterpret_cast<uint32_t *>(&hh);
-          }
-        }
-        tmem_st16(tl + kColQ + c32 * 32, w);
-        tmem_st16(tl + kColQ + c32 * 32 + 16, w + 16);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qready);
-    }
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < ntiles; ++j) {
       const int slot = j & 1;
@@ -691,7 +702,12 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     const size_t orow = (size_t)(q0 + i) * a.Hq + h * G + g2;
     const size_t plane = (size_t)split * a.total_q * a.Hq;
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16) + kColO + part * (D / 4);
-#pragma unroll
+    // The rows go through shared memory (nothing else uses it any more), 16
+    // bytes apart from a multiple of 128 so that the lanes' stores meet no
+    // bank conflict, and leave as one bulk copy a row.
+    const int bytes = a.ws_o ? D * 4 : D * 2;
+    uint8_t *srow = smem + r * (bytes + 16);
+#pragma unroll 1
     for (int c16 = 0; c16 < D / 64; ++c16) {
       uint32_t rr[16];
       if (ntiles > 0) {
@@ -702,10 +718,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
 #pragma unroll
         for (int e = 0; e < 16; ++e) rr[e] = 0u;
       }
-      if (!write) continue;
       const int col = part * (D / 4) + c16 * 16;
       if (a.ws_o) {
-        float4 *dst = reinterpret_cast<float4 *>(a.ws_o + (plane + orow) * D + col);
+        float4 *dst = reinterpret_cast<float4 *>(srow + 4 * col);
 #pragma unroll
         for (int e4 = 0; e4 < 4; ++e4)
           dst[e4] = make_float4(__uint_as_float(rr[4 * e4]) * inv,
@@ -720,10 +735,22 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
                                                     __uint_as_float(rr[2 * e + 1]) * inv);
           ow[e] = *reinterpret_cast<uint32_t *>(&b2);
         }
-        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + col);
+        uint4 *dst = reinterpret_cast<uint4 *>(srow + 2 * col);
         dst[0] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
         dst[1] = make_uint4(ow[4], ow[5], ow[6], ow[7]);
       }
+    }
+    fence_proxy_async_smem();
+    named_barrier(6 + lq, 128);  // the four warps of these rows
+    if (part == 0) {
+      if (write) {
+        void *dst = a.ws_o ? (void *)(a.ws_o + (plane + orow) * D) : (void *)(a.out + orow * D);
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                     "r"(smem_u32(srow)), "r"(bytes)
+                     : "memory");
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
 
