@@ -464,6 +464,8 @@ def _on(cache: Cache, seqs: Seqs) -> int:
     if seqs.page_table.get_device() != device or seqs.kv_lens.get_device() != device:
         raise ValueError(f"the page table is on {seqs.page_table.device}, kv_lens on "
                          f"{seqs.kv_lens.device}, the cache on {cache.pool.device}")
+    if seqs.err_word is not None and seqs.err_word.get_device() != device:
+        raise ValueError(f"err_word is on {seqs.err_word.device}, the cache on {cache.pool.device}")
     return device
 
 
@@ -486,28 +488,27 @@ class ScoreMod:
     tanh, a bias -alibi_slopes[head] * |distance| (float32 [Hq]), a sliding
     window of that many keys, a prefix of prefix_lens[b] tokens (int32
     [batch]) whose queries see all of it, and the first visible key key_starts
-    (int32, [batch] for decode, [total_q] for prefill).  The tensors are kept
-    and read by every call, so their contents may change between calls."""
+    (int32, [batch] for decode, [total_q] for prefill).  Every call takes the
+    attributes as they are then, and its kernels read the tensors."""
 
     def __init__(self, softcap: float = 0.0, window: int = 0,
                  alibi_slopes: torch.Tensor | None = None, prefix_lens: torch.Tensor | None = None,
                  key_starts: torch.Tensor | None = None):
         self.softcap, self.window = float(softcap), int(window)
         self.alibi_slopes, self.prefix_lens, self.key_starts = alibi_slopes, prefix_lens, key_starts
-        self._c = _ScoreModC(
-            self.softcap, self.window,
-            _dev(alibi_slopes, torch.float32, "alibi_slopes") if alibi_slopes is not None else None,
-            _dev(prefix_lens, torch.int32, "prefix_lens") if prefix_lens is not None else None,
-            _dev(key_starts, torch.int32, "key_starts") if key_starts is not None else None)
+        for t, dtype, name in ((alibi_slopes, torch.float32, "alibi_slopes"),
+                               (prefix_lens, torch.int32, "prefix_lens"),
+                               (key_starts, torch.int32, "key_starts")):
+            if t is not None:
+                _dev(t, dtype, name)
 
-    def _ref(self, device: int, num_q_heads: int, batch: int, starts: int):
-        if self.alibi_slopes is not None:
-            _arg(self.alibi_slopes, torch.float32, device, num_q_heads, "alibi_slopes")
-        if self.prefix_lens is not None:
-            _arg(self.prefix_lens, torch.int32, device, batch, "prefix_lens")
-        if self.key_starts is not None:
-            _arg(self.key_starts, torch.int32, device, starts, "key_starts")
-        return ctypes.byref(self._c)
+    def _struct(self, device: int, num_q_heads: int, batch: int, starts: int) -> _ScoreModC:
+        a, p, k = self.alibi_slopes, self.prefix_lens, self.key_starts
+        return _ScoreModC(
+            self.softcap, self.window,
+            None if a is None else _arg(a, torch.float32, device, num_q_heads, "alibi_slopes"),
+            None if p is None else _arg(p, torch.int32, device, batch, "prefix_lens"),
+            None if k is None else _arg(k, torch.int32, device, starts, "key_starts"))
 
 
 def nvkv_decode_mod_kernel_name(cache: Cache, T: int, num_q_heads: int) -> str:
@@ -530,7 +531,7 @@ def nvkv_decode_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, T: int, num_
     fn = L.nvkv_decode_attn_mod_k8v4 if cache.kv_format == "k8v4" else L.nvkv_decode_attn_mod
     _call(device, fn, "nvkv_decode_attn_mod", stream, ctypes.byref(cache._c),
           ctypes.byref(seqs._c), _arg(q, torch.bfloat16, device, n, "q"), T, num_q_heads, sm_scale,
-          mod._ref(device, num_q_heads, seqs.batch, seqs.batch), num_splits,
+          ctypes.byref(mod._struct(device, num_q_heads, seqs.batch, seqs.batch)), num_splits,
           _arg(workspace, torch.uint8, device, 0, "workspace"), workspace.numel(),
           _arg(out, torch.bfloat16, device, n, "out"))
 
@@ -552,7 +553,8 @@ def nvkv_prefill_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, cu_q: torch
     _call(device, fn, "nvkv_prefill_attn_mod", stream, ctypes.byref(cache._c),
           ctypes.byref(seqs._c), _arg(q, torch.bfloat16, device, n, "q"),
           _arg(cu_q, torch.int32, device, seqs.batch + 1, "cu_q"), total_q, max_q, num_q_heads,
-          sm_scale, mod._ref(device, num_q_heads, seqs.batch, total_q), num_splits, ws, size,
+          sm_scale, ctypes.byref(mod._struct(device, num_q_heads, seqs.batch, total_q)),
+          num_splits, ws, size,
           _arg(out, torch.bfloat16, device, n, "out"))
 
 
