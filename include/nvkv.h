@@ -406,7 +406,7 @@ nvkv_status nvkv_pages_restore_k8v4(const nvkv_cache *cache, const int32_t *page
  * reused by another sequence) as long as no query of the call sees a key of
  * the page, and no bad page id is reported for them.  The keys of a bad page
  * that a query does see are left out (and reported).
- *   softcap:      > 0 and finite, or 0 for none.
+ *   softcap:      > 0 and finite (at least 1e-38), or 0 for none.
  *   window:       > 0: that many keys up to the query's own; 0: none.
  *   alibi_slopes: device float [Hq], or NULL.
  *   prefix_lens:  device int32 [batch], or NULL (values <= 0: no prefix).

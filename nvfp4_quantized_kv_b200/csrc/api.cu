@@ -212,16 +212,15 @@ nvkv_status check_mod(const nvkv_score_mod *mod, ScoreMod &m) {
   if (!mod || !std::isfinite(mod->softcap) || mod->softcap < 0.f || mod->window < 0)
     return NVKV_ERR_INVALID_ARG;
   m.cap2 = mod->softcap * kLog2e;
-  m.cap_in = mod->softcap > 0.f ? 2.f * kLog2e / m.cap2 : 0.f;
-  // kCapSmall's polynomial of tanh, in the score instead of score / cap2
-  const double tanh_poly[5] = {0.9999972283, -0.3332307647, 0.1322609151, -0.04928044419,
-                               0.01231882928};
+  m.inv_cap = mod->softcap > 0.f ? 1.f / m.cap2 : 0.f;
+  if (!std::isfinite(m.cap2) || !std::isfinite(m.inv_cap)) return NVKV_ERR_INVALID_ARG;
+  const bool fits = m.cap2 >= 1e-4f && m.cap2 <= 3e4f;  // see cap_small
+  m.cap_top = fits ? kCapSmallTanh * m.cap2 : -1.f;
   double scale = 1.0;
   for (int i = 0; i < 5; ++i) {
-    m.poly[i] = (float)(tanh_poly[i] * scale);
-    if (m.cap2 > 0.f) scale /= (double)m.cap2 * (double)m.cap2;
+    m.poly[i] = fits ? (float)(tanh_coefficient(i) * scale) : 0.f;
+    scale /= (double)m.cap2 * (double)m.cap2;
   }
-  if (!std::isfinite(m.cap2) || !std::isfinite(m.cap_in)) return NVKV_ERR_INVALID_ARG;
   m.window = mod->window;
   m.slopes = mod->alibi_slopes;
   m.prefix = mod->prefix_lens;

@@ -1112,7 +1112,10 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if constexpr (Mod::kOn) {
               if constexpr (Mod::kCap) {
 #pragma unroll
-                for (int j = 0; j < RM; ++j) x[j] = mod.cap(x[j]);
+                for (int j = 0; j < RM; j += 2) {
+                  const float2 v = mod.cap(make_float2(x[j], x[j + 1]));
+                  x[j] = v.x, x[j + 1] = v.y;
+                }
               }
               if constexpr (Mod::kBias) {
 #pragma unroll

@@ -117,7 +117,7 @@ __device__ __forceinline__ void attend_rows_simt(const uint8_t *__restrict__ poo
     float s = k_half_score(L{}, blk, D, slot, half, qr);
     s += __shfl_xor_sync(0xffffffffu, s, 16);
     if constexpr (Mod::kOn) {
-      if (mod.cap2 > 0.f) s = mod.cap(s);
+      if (mod.cap2 > 0.f) s = mod.cap(make_float2(s, 0.f)).x;
       s = fmaf(-slope2, fabsf((float)(pos - (p0 + slot))), s);
     }
     const float s_eff = valid ? s : -INFINITY;

@@ -580,10 +580,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
           t1 = max3_abs(t1, x[e + 2], x[e + 3]);
         }
         above = max3_abs(t0, t1, max3_abs(x[30], x[31], 0.f));
-        if (rare(__any_sync(0xffffffffu, !(above <= kCapSmallTanh * mod.cap2)))) {  // (a NaN too)
+        if (rare(__any_sync(0xffffffffu, !(above <= mod.cap_top)))) {  // (a NaN too)
           load_scores();
 #pragma unroll
-          for (int e = 0; e < kHalf; ++e) x[e] = mod.cap(x[e]);
+          for (int e = 0; e < kHalf; e += 2) {
+            const float2 v = mod.cap(make_float2(x[e], x[e + 1]));
+            x[e] = v.x, x[e + 1] = v.y;
+          }
           above = mod.cap2;
         }
       } else {

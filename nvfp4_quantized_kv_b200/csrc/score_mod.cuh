@@ -12,10 +12,24 @@ namespace nvkv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// tanh(u) = u P(u^2) for |u| <= kCapSmall, off by at most 1.9e-7, and by 2.8e-6
+// of its value (a degree-9 odd polynomial, least maximum error by reweighted
+// least squares over the interval); increasing for every u.
+__host__ __device__ constexpr float tanh_coefficient(int i) {
+  return i == 0   ? 0.9999972283f
+         : i == 1 ? -0.3332307647f
+         : i == 2 ? 0.1322609151f
+         : i == 3 ? -0.04928044419f
+                  : 0.01231882928f;
+}
+constexpr float kCapSmall = 0.75f;
+constexpr float kCapSmallTanh = 0.635148f;  // tanh(0.75), rounded down
+
 // Visible keys [lo, hi) of a query at position p of a sequence of kv_len
 // tokens: lo = max(0, start, p - W + 1), hi = p + 1, or p + min(P - p, W)
 // when p lies inside the prefix P; at most kv_len.  W <= 0: no window.
-// Always an interval; empty (hi <= lo) when start > p, or p < 0.
+// Always an interval; empty (hi <= lo) when p < 0, or when nothing from
+// start on is below hi.
 __host__ __device__ inline void key_range(int p, int kv_len, int start, int window, int prefix,
                                           int &lo, int &hi) {
   lo = start > 0 ? start : 0;
@@ -58,8 +72,9 @@ struct NoMod {
 struct ScoreMod {
   static constexpr bool kOn = true, kCap = true, kBias = false;
   float cap2;             // cap * log2 e; 0 = no cap
-  float cap_in;           // 2 log2 e / cap2: the exponent of exp(2 x / cap2), base 2
-  float poly[5];          // cap_small's coefficients, times cap2^(-2i)
+  float inv_cap;          // 1 / cap2
+  float cap_top;          // see cap_small
+  float poly[5];          // tanh's coefficients times cap2^(-2i)
   int window;             // 0 = none
   const float *slopes;    // [Hq] or null
   const int32_t *prefix;  // [batch] or null
@@ -73,29 +88,39 @@ struct ScoreMod {
     visible_units(kv_lens[b], T, start(b), window, lo, first, n);
     return n;
   }
-  // cap2 * tanh(x / cap2) = cap2 - 2 cap2 / (2^(x * cap_in) + 1): one base-2
-  // exponential and one reciprocal.  Each approximation is good to a few
-  // 2^-23, so the result is off by at most about 2^-20 * cap2 whatever x
-  // (tanh.approx would be off by 2^-11 * cap2, several per cent of a softmax
-  // weight at a cap of 50).  The exponential's overflow to infinity gives
-  // +cap2, its underflow -cap2.
-  __device__ __forceinline__ float cap(float x) const {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * cap_in));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
-    return fmaf(-2.f * cap2, r, cap2);
+  // cap2 * tanh(u), u = x / cap2, of two scores, off by at most about 3e-6
+  // times the result (2^-18) at any cap and any x: near 0 the polynomial,
+  // beyond it 1 - 2 / (exp(2 u) + 1) from one base-2 exponential and one
+  // reciprocal, whose error of some 2^-21 of a cap would be whole units of a
+  // score at a cap of 1e6.  (tanh.approx would be off by 2^-11 of a cap,
+  // several per cent of a softmax weight at a cap of 50.)  The exponential's
+  // overflow to infinity gives +cap2, its underflow -cap2.
+  __device__ __forceinline__ float2 cap(float2 x) const {
+    const float2 u = mul_f32x2(x, make_float2(inv_cap, inv_cap));
+    const float2 v = mul_f32x2(u, u);
+    float2 p = make_float2(tanh_coefficient(4), tanh_coefficient(4));
+#pragma unroll
+    for (int i = 3; i >= 0; --i)
+      p = fma_f32x2(p, v, make_float2(tanh_coefficient(i), tanh_coefficient(i)));
+    p = mul_f32x2(p, u);
+    auto far = [](float a) {
+      float e, r;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * (2.f * kLog2e)));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
+      return fmaf(-2.f, r, 1.f);
+    };
+    const float tx = fabsf(u.x) <= kCapSmall ? p.x : far(u.x);
+    const float ty = fabsf(u.y) <= kCapSmall ? p.y : far(u.y);
+    return mul_f32x2(make_float2(tx, ty), make_float2(cap2, cap2));
   }
 };
 
-// tanh(u) = u P(u^2) for |u| <= kCapSmall, off by at most 1.9e-7 (a degree-9
-// odd polynomial, least maximum error by reweighted least squares over the
-// interval), and increasing for every u, so that a result of at most
-// kCapSmallTanh * cap2 shows that u was in the interval: 3 packed multiply-adds a score and none of the two special
-// functions of cap(), which take 16 issue cycles a warp.
-constexpr float kCapSmall = 0.75f;
-constexpr float kCapSmallTanh = 0.635148f;  // tanh(0.75), rounded down
-
-// cap() of two scores x with |x| <= kCapSmall * cap2: x P((x / cap2)^2).
+// cap() of two scores x with |x| <= kCapSmall * cap2, x P((x / cap2)^2) with
+// the powers of cap2 in the coefficients: 5 packed instructions a pair.  The
+// result is increasing in x for every x, so one of at most cap_top =
+// kCapSmallTanh * cap2 shows that x was in the interval.  Caps whose powers
+// leave fp32 (cap2 outside [1e-4, 3e4]) have a cap_top of -1: no result
+// passes.
 __device__ __forceinline__ float2 cap_small(const ScoreMod &m, float2 x) {
   const float2 v = mul_f32x2(x, x);
   float2 p = make_float2(m.poly[4], m.poly[4]);

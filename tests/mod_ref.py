@@ -186,7 +186,8 @@ def attend(q, k, v, seen, p, j, scale, cap, slope, slack):
     eps = (k.shape[1] + 4) * 2.0 ** -24 + (2.0 ** -11 if slack == "f16 scores" else 1e-6)
     off = absqk * eps
     if cap:
-        off = torch.minimum(off, torch.full_like(off, 2 * cap)) + cap * 2.0 ** -19
+        # the cap itself is good to 2^-18 of its result
+        off = torch.minimum(off, torch.full_like(off, 2 * cap)) + x.abs() * 2.0 ** -18
     if slope:
         # slope * log2e rounded once, the product with the distance rounded,
         # the sum rounded: 3 roundings of 2^-24 of the bias

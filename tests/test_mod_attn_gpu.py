@@ -366,3 +366,25 @@ def test_prefill_cap_from_linear_to_saturated(D, Hq, Hkv):
         m = Mod(cap=cap)
         ref, tol = case.reference(m, D ** -0.5, False, "f16 scores")
         assert_within(run_prefill(case, m, D ** -0.5), ref, tol, f"{gain}/{cap}")
+
+
+@pytest.mark.parametrize("kernel", ["default", "simt"])
+@pytest.mark.parametrize("cap", [1e-30, 1e-5, 1e-3, 3e3, 2e4, 3e4, 1e7, 1e30])
+@pytest.mark.parametrize("D,Hq,Hkv", [(256, 24, 4), (128, 8, 2)])
+def test_caps_of_any_size(D, Hq, Hkv, cap, kernel, monkeypatch):
+    """Caps far below and far above the scores; a cap above all of them
+    leaves the scores as they are."""
+    if kernel != "default":
+        monkeypatch.setenv("NVKV_DECODE_KERNEL", kernel)
+    for T in (1, 5):
+        case = Case(Hq, Hkv, D, [300, 77], [T, T], seed=31, q_gain=3.0).device()
+        case.q_dev[0, 0] = 0.0  # scores of exactly 0
+        case.q[0, 0] = 0
+        m = Mod(cap=cap)
+        ref, tol = case.reference(m, D ** -0.5, True, decode_slack(case, T))
+        assert_within(run_decode(case, m, T, D ** -0.5), ref, tol, f"decode of {T}")
+    case = Case(Hq, Hkv, D, [200], [100], seed=32, q_gain=3.0).device()
+    case.q_dev[0] = 0.0
+    case.q[0] = 0
+    ref, tol = case.reference(m, D ** -0.5, False, prefill_slack(case, kernel))
+    assert_within(run_prefill(case, m, D ** -0.5), ref, tol, "prefill")
