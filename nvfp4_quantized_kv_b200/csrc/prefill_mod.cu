@@ -783,7 +783,10 @@ prefill_mod_merge_kernel(const float *__restrict__ ws_o, const float *__restrict
   __shared__ float s_acc[kW > 1 ? kMergeThreads / 32 : 1][D], s_w[kMergeThreads / 32];
   const int b = blockIdx.y;
   const int q0 = T > 0 ? b * T : cu_q[b], n_b = T > 0 ? T : cu_q[b + 1] - q0;
-  if (n_b <= 0 || q0 < 0 || q0 + n_b > total_q) return;  // no output rows (as in the attention)
+  if (n_b <= 0 || q0 < 0 || q0 + n_b > total_q) {  // no output rows (as in the attention)
+    grid_dependency_wait();  // (a grid of such blocks alone must not end before the attention)
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kW;
   const int64_t idx = (int64_t)blockIdx.x * kRows + warp / kW;  // token idx / Hq, head idx % Hq
   // only the rows the attention grid covers (tile rows i*G + g < row_cap)
