@@ -435,7 +435,8 @@ typedef struct nvkv_score_mod {
  *   "prefill_mod" (more rows): the kernel of nvkv_prefill_attn_mod, the keys
  *                 of each (sequence, kv-head) split over as many CTAs as the
  *                 workspace has room for; q * sm_scale * log2(e) enters as one
- *                 f16 (11 significant bits; |q * sm_scale| below about 45000).
+ *                 f16 (11 significant bits; |q * sm_scale| below about 45000);
+ *                 at most 65535 sequences.
  *   "decode_simt" (NVKV_DECODE_KERNEL=simt).
  *
  * nvkv_decode_attn_mod_k8v4: the same over a K8V4 cache, on the kernels of
@@ -458,6 +459,7 @@ nvkv_status nvkv_decode_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs *
  * sum, which accumulates in fp32.
  * num_splits = 0 takes the automatic count that the workspace has room for
  * (1 for a NULL one; nvkv_prefill_workspace_bytes(..., 0) is enough for any).
+ * |q * sm_scale| below about 45000 (f16), at most 65535 sequences.
  * A prefix is seen in both directions as far as it is cached: put it into one
  * chunk.
  *
@@ -490,7 +492,7 @@ nvkv_status nvkv_prefill_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs 
  *   q:            device bf16 [total_new][Hq][D], rotated into q_out (same
  *                 shape; q_out = q is allowed) and rounded once to bf16, or
  *                 NULL (then q_out and num_q_heads are not used).
- * The rotation is that of nvkv_append_rope.  A row with a position outside
+ * The rotation is that of nvkv_append_rope; at most 65535 sequences.  A row with a position outside
  * the table on any axis sets NVKV_DEVERR_LENGTH and is left out: none of its
  * K, V and q_out is written.  A row on a bad page sets NVKV_DEVERR_PAGE_ID;
  * its K and V are left out, its query is rotated all the same. */
@@ -512,7 +514,7 @@ nvkv_status nvkv_append_rope_axes(const nvkv_cache *cache, const nvkv_seqs *seqs
  *   total_rows: cu_rows[batch] (host copy); max_rows >= every n_b (host bound).
  * A sequence whose rows are not all cached (starts[b] < 0 or starts[b] + n_b
  * > kv_lens[b]) sets NVKV_DEVERR_LENGTH, a bad page NVKV_DEVERR_PAGE_ID; the
- * rows concerned are left as they were.
+ * rows concerned are left as they were.  At most 65535 sequences.
  * nvkv_read_rows_k8v4: the same from a K8V4 cache. */
 nvkv_status nvkv_read_rows(const nvkv_cache *cache, const nvkv_seqs *seqs, const int32_t *starts,
                            const int32_t *cu_rows, int32_t total_rows, int32_t max_rows,

@@ -504,6 +504,8 @@ class ScoreMod:
 
     def _struct(self, device: int, num_q_heads: int, batch: int, starts: int) -> _ScoreModC:
         a, p, k = self.alibi_slopes, self.prefix_lens, self.key_starts
+        if not 0 <= self.window < 2 ** 31:
+            raise ValueError(f"window is {self.window}, must be 0 .. 2^31 - 1")
         return _ScoreModC(
             self.softcap, self.window,
             None if a is None else _arg(a, torch.float32, device, num_q_heads, "alibi_slopes"),

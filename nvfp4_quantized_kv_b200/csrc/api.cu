@@ -238,6 +238,11 @@ bool force_kernel(const char *name) {
 }
 bool force_simt() { return force_kernel("simt"); }
 
+// Whether sequences and kv-heads fit the y and z sides of a launch grid.
+bool grid_holds(const nvkv_cache &c, const nvkv_seqs &s) {
+  return s.batch <= 65535 && c.num_kv_heads <= 65535;
+}
+
 nvkv_status decode_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const void *q, int32_t T,
                        int32_t num_q_heads, float sm_scale, const nvkv_score_mod *mod,
                        int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
@@ -258,6 +263,7 @@ nvkv_status decode_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const voi
   } else if (!simt && !k8 && !force_kernel("tc") && decode_qk4_supported(c, T, num_q_heads, true)) {
     e = launch_decode_qk4(c, *seqs, q, T, num_q_heads, sm_scale, a.S, a.ws_o, a.ws_lse, s, &m);
   } else if (!simt && !k8) {
+    if (!grid_holds(c, *seqs)) return NVKV_ERR_UNSUPPORTED;
     return cuda_status(launch_decode_rows(c, *seqs, q, T, num_q_heads, sm_scale,
                                           (int64_t)a.S + (int64_t)seqs->batch * c.num_kv_heads - 1,
                                           a.ws_o, a.ws_lse, out, nvkv_default_num_splits(), s, m));
@@ -279,7 +285,9 @@ nvkv_status prefill_mod(const nvkv_cache *cache, const nvkv_seqs *seqs, const vo
   ScoreMod m;
   if ((st = check_mod(mod, m)) != NVKV_OK) return st;
   if (num_splits < 0 || num_splits > prefill_max_splits()) return NVKV_ERR_INVALID_ARG;
-  if (total_q == 0) return NVKV_OK;
+  if (total_q == 0 || max_q == 0) return NVKV_OK;
+  if (!grid_holds(*cache, *seqs)) return NVKV_ERR_UNSUPPORTED;
+  if (max_q > total_q) max_q = total_q;  // (no chunk is longer)
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (k8)
     return cuda_status(launch_prefill_simt(*cache, *seqs, q, cu_q, total_q, num_q_heads, sm_scale,
@@ -317,7 +325,7 @@ nvkv_status read_rows(const nvkv_cache *cache, const nvkv_seqs *seqs, const int3
   if (total_rows == 0 || max_rows == 0) return NVKV_OK;
   if (!starts || !cu_rows || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
     return NVKV_ERR_INVALID_ARG;
-  if (!read_rows_fits(*cache, max_rows)) return NVKV_ERR_UNSUPPORTED;
+  if (!grid_holds(*cache, *seqs) || !read_rows_fits(*cache, max_rows)) return NVKV_ERR_UNSUPPORTED;
   return cuda_status(launch_read_rows(*cache, *seqs, starts, cu_rows, total_rows, max_rows, k_out,
                                       v_out, reinterpret_cast<cudaStream_t>(stream), k8));
 }
@@ -654,7 +662,8 @@ nvkv_status nvkv_append_rope_axes(const nvkv_cache *cache, const nvkv_seqs *seqs
     return NVKV_ERR_INVALID_ARG;
   if (q && (!q_out || !aligned16(q) || !aligned16(q_out) || num_q_heads <= 0))
     return NVKV_ERR_INVALID_ARG;
-  if (!append_axes_fits(*cache, max_new, num_q_heads, q != nullptr)) return NVKV_ERR_UNSUPPORTED;
+  if (!grid_holds(*cache, *seqs) || !append_axes_fits(*cache, max_new, num_q_heads, q != nullptr))
+    return NVKV_ERR_UNSUPPORTED;
   return cuda_status(launch_append_axes(*cache, *seqs, k_new, v_new, cu_new, total_new, max_new,
                                         rope_cs, max_pos, rotary_dim, positions, num_axes,
                                         axis_of_pair, q, num_q_heads, q_out,

@@ -388,3 +388,16 @@ def test_caps_of_any_size(D, Hq, Hkv, cap, kernel, monkeypatch):
     case.q[0] = 0
     ref, tol = case.reference(m, D ** -0.5, False, prefill_slack(case, kernel))
     assert_within(run_prefill(case, m, D ** -0.5), ref, tol, "prefill")
+
+
+def test_a_loose_bound_of_the_chunk_lengths():
+    """max_q is only an upper bound: the largest int32 gives the same rows."""
+    case = Case(24, 4, 256, [200, 90], [40, 9], seed=33).device()
+    m = Mod(cap=20.0, window=64).device("cuda")
+    outs = []
+    for max_q in (40, 2 ** 31 - 1):
+        out = torch.full((49, 24, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
+        nv.nvkv_prefill_attn_mod(case.cache, case.seqs, case.q_dev, case.cu_dev, 49, max_q, 24, 1 / 16, m, 1, None, out)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert torch.isfinite(outs[0]).all() and torch.equal(*outs)

@@ -110,6 +110,29 @@ def test_read_refusals(lib, fn):
     assert call(total=0, starts=None) == nv.OK
 
 
+def test_more_sequences_than_a_grid_holds(lib):
+    """Calls that launch a grid with a side of sequences refuse the count
+    that does not fit (the K8V4 prefill's check comes first too)."""
+    many = seqs(batch=65536)
+    need = lib.nvkv_decode_workspace_bytes(65536, 2, 24, 4, 256, 8)
+    assert lib.nvkv_decode_attn_mod(B(cache()), B(many), 0x100, 2, 24, 0.1, B(mod()), 8, 0x1000, need, 0x100,
+                                    None) == nv.ERR_UNSUPPORTED
+    for f in (lib.nvkv_prefill_attn_mod, lib.nvkv_prefill_attn_mod_k8v4):
+        assert f(B(cache()), B(many), 0x100, 0x200, 10, 10, 24, 0.1, B(mod()), 1, None, 0, 0x300,
+                 None) == nv.ERR_UNSUPPORTED
+        assert f(B(cache()), B(seqs()), 0x100, 0x200, 10, 0, 24, 0.1, B(mod()), 1, None, 0, 0x300, None) == nv.OK
+    for f in (lib.nvkv_read_rows, lib.nvkv_read_rows_k8v4):
+        assert f(B(cache()), B(many), 0x100, 0x200, 3, 3, 0x300, 0x400, None) == nv.ERR_UNSUPPORTED
+    assert lib.nvkv_append_rope_axes(B(cache()), B(many), 0x100, 0x200, 0x300, 3, 3, 0x400, 64, 256, 0x500, 3,
+                                     bytes(128), None, 0, None, None) == nv.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("window", [-1, 2 ** 31, 2 ** 32 + 5])
+def test_a_window_that_is_no_int32_is_refused(window):
+    with pytest.raises(ValueError, match="window"):
+        nv.ScoreMod(window=window)._struct(0, 8, 1, 1)
+
+
 def test_python_checks():
     import torch
     with pytest.raises(ValueError, match="CUDA"):
