@@ -1,6 +1,6 @@
 // decode_qk4.cu -- split-K GQA decode attention over the NVFP4 paged pool,
-// head_dim 256, up to 6 query rows per (sequence, kv-head): the scores on
-// the NVFP4 block-scaled tensor-core MMA, straight from the cached codes.
+// head_dim 256 (masked also 128), up to 6 query rows per (sequence, kv-head):
+// the scores on the NVFP4 block-scaled tensor-core MMA, straight from the cached codes.
 //
 // What it computes is the decode half of the path in the "knoopx/ninfer"
 // README, "Capabilities and limits" (batched decode, MTP verify), over the
@@ -70,6 +70,24 @@
 //  * warp 13 issues the score MMAs, warp 14 the value MMAs (one thread each).
 //  * Every wait is bounded; a timeout sets NVKV_DEVERR_TIMEOUT, turns later
 //    waits into no-ops and lets the kernel drain and free its Tensor Memory.
+//
+// Masked attention (nvkv_decode_attn_mod; Mod = ScoreModOf<cap, bias>), also
+// at head_dim 128: the softmax caps the recombined scores, adds the distance
+// bias and masks each row's key interval, all between the recombination and
+// the running maximum; units that no query sees are in no range.  Every step
+// that needs no mask (a unit inside all rows' intervals) takes a
+// warp-uniform branch past it.  One warp lists the CTA's range and segments
+// before the roles start (every role walking the sequences cost microseconds
+// at a batch of 64), and kernels are instances by cap and bias because the
+// roles share the instruction caches.  Measured (nvkv_decode_attn_mod with
+// its merge): 4 x 32k tokens, cap, 24/4 heads, head_dim 256: 351 us, 0.61 of
+// the time that the cache bytes need at the copy rate; 64 windows of 4,096
+// tokens: 104 us, 0.43; one sequence of 4,097 tokens, 8/2 heads, head_dim
+// 128: 14.4 us, which is the launch of two kernels, the set-up (about 7,000
+// cycles before the first unit) and one drain.  What bounds it per unit is
+// the plain kernel's hand-off from the V^T writers to the value MMAs (about
+// 2,000 cycles a unit); a segment's end costs some 7,000 cycles more, which
+// many short windows feel.
 #include <cfloat>
 
 #include "score_mod.cuh"

@@ -538,7 +538,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       key_range(pos, kv_len, start_of(i), mod.window, prefix, row_lo, row_hi);
       slope2 = mod.slope2(h * G + g);
     }
-    float m = -INFINITY, l = 0.f;
+    // (a row that is none has scores of 0 and a maximum of 0: it never asks
+    // for a new one)
+    float m = valid ? -INFINITY : 0.f, l = 0.f;
     for (int j = 0; j < ntiles; ++j) {
       const int slot = j & 1;
       wait_bar(&sready[slot], (j >> 1) & 1, flags, a.err);
@@ -603,6 +605,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
 #pragma unroll
         for (int e = 0; e < kHalf; ++e)
           if (key0 + e < row_lo || key0 + e >= row_hi) x[e] = -INFINITY;
+        if (valid && (key0 >= row_hi || key0 + kHalf <= row_lo)) above = -INFINITY;
       }
       const uint32_t here = present[j & 3] >> (2 * hf);
       if (rare((here & 3u) != 3u)) {
