@@ -41,6 +41,8 @@
 // NVKV_DEVERR_TIMEOUT and drains. The long prefill (65,536 + 2,048 tokens,
 // 24/4 heads, head_dim 256, cap 50): 4.01 ms = 836 TFLOP/s, 0.50 of the
 // measured matrix rate.
+#include <type_traits>
+
 #include "score_mod.cuh"
 #include "sm100.cuh"
 
@@ -136,10 +138,20 @@ struct Args {
   int32_t *err;
 };
 
-template <int D, class Mod>
+// kCopies = 4 or 2: tiles of at most 32 or 64 rows (a verify step, a decode
+// step of a wide group, a short chunk).  The MMA has 128 rows anyway, so the
+// rows stand in every (every other) 32-lane quarter of the tile, and each
+// copy of a row weighs its own quarter (half) of every tile's keys, with a
+// running maximum of its own and weights of 0 elsewhere; the copies are added
+// at the end as key splits are.  The softmax of a tile then takes a quarter
+// (half) of the instructions.
+template <int D, int kCopies, class Mod>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const Mod mod) {
   using C = Cfg<D>;
+  constexpr int kTileRows = 128 / kCopies;
+  constexpr int kQuarters = 4 / kCopies;    // 32-lane quarters of one copy
+  constexpr int kKeys = kHalf / kCopies;    // keys of a softmax thread
   constexpr int kPagePitch = C::kPagePitch, kStageBytes = C::kStageBytes,
                 kKTileBytes = C::kKTileBytes, kVTileBytes = C::kVTileBytes;
   // blockIdx.x = m-tile * num_splits + split: split s of an m-tile takes the
@@ -155,7 +167,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   auto start_of = [&](int i) { return mod.start(a.T > 0 ? b : q0 + i); };
   const int prefix = mod.prefix_of(b);
   const int rows = n_b * G;
-  if (128 * mt >= rows) return;  // uniform: this tile has no query row
+  if (kTileRows * mt >= rows) return;  // uniform: this tile has no query row
   // (a decode step may have more queries than tokens: the first see nothing)
   const bool bad = n_b < 0 || q0 < 0 || q0 + n_b > a.total_q || (a.T == 0 && kv_len < n_b) ||
                    kv_len > a.max_kv_len || kv_len > a.max_pages * kPageTokens;
@@ -191,8 +203,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   // the tile's tokens.
   int key_lo = 0x7fffffff, key_hi = 0;
   if (!bad) {
-    const int i_last = min(n_b - 1, (128 * mt + 127) / G);
-    for (int i = (128 * mt) / G + lane; i <= i_last; i += 32) {
+    const int i_last = min(n_b - 1, (kTileRows * mt + kTileRows - 1) / G);
+    for (int i = (kTileRows * mt) / G + lane; i <= i_last; i += 32) {
       int lo, hi;
       key_range(kv_len - n_b + i, kv_len, start_of(i), mod.window, prefix, lo, hi);
       if (lo < hi) key_lo = min(key_lo, lo), key_hi = max(key_hi, hi);
@@ -249,7 +261,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     // thread's loads are one latency. (Four warps with all columns had Q ready
     // 3,000 to 6,000 cycles later.)
     const int lq = warp & 3, part = (warp - kKWarps) >> 2;
-    const int gr = 128 * mt + 32 * lq + lane;
+    const int gr = kTileRows * mt + 32 * (lq % kQuarters) + lane;
     const bool valid = gr < rows && !bad;
     const __nv_bfloat16 *qr =
         a.q + ((size_t)(q0 + gr / G) * a.Hq + h * G + gr % G) * D + part * (D / 4);
@@ -526,9 +538,11 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     // ------------------------------------------------------------- softmax
     const int hf = warp >= kDeqWarps + 4;     // keys 32 * hf .. of every tile
     const int lq = warp & 3;
-    const int r = 32 * lq + lane;             // query row of the tile
+    const int copy = lq / kQuarters;
+    const int koff = kHalf * hf + kKeys * copy;  // first key of this thread in a tile
+    const int r = 32 * lq + lane;             // row of the MMA
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
-    const int gr = 128 * mt + r;
+    const int gr = kTileRows * mt + 32 * (lq % kQuarters) + lane;
     const bool valid = gr < rows && !bad;
     const int i = gr / G, g = gr % G;
     const int pos = kv_len - n_b + i;
@@ -547,45 +561,50 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       __syncwarp();  // the Tensor Memory loads below are warp-collective
       tc_fence_after();
       const uint32_t scol = tl + kColS + slot * 64;
-      float x[kHalf];
+      float x[kKeys];
       auto load_scores = [&]() {
-        uint32_t(&xr)[kHalf] = reinterpret_cast<uint32_t(&)[kHalf]>(x);
-        tmem_ld16(scol + kHalf * hf, reinterpret_cast<uint32_t(&)[16]>(xr[0]));
-        tmem_ld16(scol + kHalf * hf + 16, reinterpret_cast<uint32_t(&)[16]>(xr[16]));
+        uint32_t(&xr)[kKeys] = reinterpret_cast<uint32_t(&)[kKeys]>(x);
+        if constexpr (kKeys == 8) {
+          tmem_ld8(scol + koff, xr);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kKeys; e += 16)
+            tmem_ld16(scol + koff + e, reinterpret_cast<uint32_t(&)[16]>(xr[e]));
+        }
         tmem_wait_ld();
       };
       auto top_score = [&]() {
         float t0 = max3(x[0], x[1], x[2]), t1 = max3(x[3], x[4], x[5]);
 #pragma unroll
-        for (int e = 6; e < 30; e += 4) {
+        for (int e = 6; e + 4 <= kKeys; e += 4) {
           t0 = max3(t0, x[e], x[e + 1]);
           t1 = max3(t1, x[e + 2], x[e + 3]);
         }
-        return max3(t0, t1, fmaxf(x[30], x[31]));
+        return max3(t0, t1, fmaxf(x[kKeys - 2], x[kKeys - 1]));
       };
       load_scores();
-      const int key0 = tile_key(j) + kHalf * hf;
+      const int key0 = tile_key(j) + koff;
       float above;  // no visible score is larger
       if constexpr (Mod::kCap) {
         // A polynomial, good for scores of at most 0.75 caps and increasing
         // beyond: its own values tell whether all of them are. Where one is
         // not, the exact form (two special functions a score).
 #pragma unroll
-        for (int e = 0; e < kHalf; e += 2) {
+        for (int e = 0; e < kKeys; e += 2) {
           const float2 v = cap_small(mod, make_float2(x[e], x[e + 1]));
           x[e] = v.x, x[e + 1] = v.y;
         }
         float t0 = max3_abs(x[0], x[1], x[2]), t1 = max3_abs(x[3], x[4], x[5]);
 #pragma unroll
-        for (int e = 6; e < 30; e += 4) {
+        for (int e = 6; e + 4 <= kKeys; e += 4) {
           t0 = max3_abs(t0, x[e], x[e + 1]);
           t1 = max3_abs(t1, x[e + 2], x[e + 3]);
         }
-        above = max3_abs(t0, t1, max3_abs(x[30], x[31], 0.f));
+        above = max3_abs(t0, t1, max3_abs(x[kKeys - 2], x[kKeys - 1], 0.f));
         if (rare(__any_sync(0xffffffffu, !(above <= mod.cap_top)))) {  // (a NaN too)
           load_scores();
 #pragma unroll
-          for (int e = 0; e < kHalf; e += 2) {
+          for (int e = 0; e < kKeys; e += 2) {
             const float2 v = mod.cap(make_float2(x[e], x[e + 1]));
             x[e] = v.x, x[e + 1] = v.y;
           }
@@ -598,19 +617,20 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         // (distances are exact; with a prefix a key may lie ahead)
         const float d0 = (float)(pos - key0);
 #pragma unroll
-        for (int e = 0; e < kHalf; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), x[e]);
+        for (int e = 0; e < kKeys; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), x[e]);
         above = top_score();
       }
-      if (rare(key0 < row_lo || key0 + kHalf > row_hi)) {
+      if (rare(key0 < row_lo || key0 + kKeys > row_hi)) {
 #pragma unroll
-        for (int e = 0; e < kHalf; ++e)
+        for (int e = 0; e < kKeys; ++e)
           if (key0 + e < row_lo || key0 + e >= row_hi) x[e] = -INFINITY;
-        if (valid && (key0 >= row_hi || key0 + kHalf <= row_lo)) above = -INFINITY;
+        if (valid && (key0 >= row_hi || key0 + kKeys <= row_lo)) above = -INFINITY;
       }
-      const uint32_t here = present[j & 3] >> (2 * hf);
-      if (rare((here & 3u) != 3u)) {
+      const uint32_t here = present[j & 3] >> (koff / kPageTokens);
+      constexpr uint32_t kHere = kKeys > kPageTokens ? 3u : 1u;  // their pages
+      if (rare((here & kHere) != kHere)) {
 #pragma unroll
-        for (int e = 0; e < kHalf; ++e)
+        for (int e = 0; e < kKeys; ++e)
           if (!((here >> (e / kPageTokens)) & 1u)) x[e] = -INFINITY;
       }
       // One barrier of the two warps that share these rows: may any score
@@ -656,10 +676,10 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       // visible key yet keeps m = -inf: it subtracts 0 instead). The
       // denominator sums the weights before their rounding, in fp32.
       const float ms = m == -INFINITY ? 0.f : m;
-      uint32_t pw[kHalf / 2];
+      uint32_t pw[kKeys / 2];
       float2 lv0 = make_float2(0.f, 0.f), lv1 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < kHalf / 2; ++e) {
+      for (int e = 0; e < kKeys / 2; ++e) {
         float2 w;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.x) : "f"(x[2 * e] - ms));
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.y) : "f"(x[2 * e + 1] - ms));
@@ -668,18 +688,28 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       }
       l += (lv0.x + lv0.y) + (lv1.x + lv1.y);
       // P overwrites the first 32 columns of its own S slot.
-      tmem_st16(scol + kHalf / 2 * hf, pw);
+      if constexpr (kCopies == 1) {
+        tmem_st16(scol + kHalf / 2 * hf, pw);
+      } else {
+        uint32_t all[kHalf / 2];
+#pragma unroll
+        for (int e = 0; e < kHalf / 2; ++e)
+          all[e] = e / (kKeys / 2) == copy ? pw[e % (kKeys / 2)] : 0u;
+        tmem_st16(scol + kHalf / 2 * hf, all);
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&pready[slot]);
     }
     l_s[128 * hf + r] = l;
+    // (the maxima of the last tile that asked for one have been read)
+    if (kCopies > 1 && hf == 0) red_s[r] = m;
     __syncwarp();
     if (lane == 0) mbar_arrive(lready);
     // Split partial: O / l (fp32) and lse = m + log2(l), -inf without a
     // visible key, in the split's plane of total_q * Hq rows.
-    if (a.ws_o && hf == 0) {
+    if (kCopies == 1 && a.ws_o && hf == 0) {
       wait_bar(lready, 0, flags, a.err);
       const float both = l_s[r] + l_s[128 + r];
       if (gr < rows && rows_ok)
@@ -700,18 +730,33 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     wait_bar(lready, 0, flags, a.err);
     const int lq = warp & 3, part = (warp - kKWarps) >> 2;
     const int r = 32 * lq + lane;
-    const int gr = 128 * mt + r;
-    const int i = gr / G, g2 = gr % G;
-    const bool write = gr < rows && rows_ok;
-    const float l = l_s[r] + l_s[128 + r];
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const size_t orow = (size_t)(q0 + i) * a.Hq + h * G + g2;
     const size_t plane = (size_t)split * a.total_q * a.Hq;
+    auto out_row = [&](int gr) { return (size_t)(q0 + gr / G) * a.Hq + h * G + gr % G; };
+    float inv;  // times O: 1 / l, with copies their share 2^(m - max) / sum 2^(m - max) l
+    if constexpr (kCopies == 1) {
+      const float l = l_s[r] + l_s[128 + r];
+      inv = l > 0.f ? 1.f / l : 0.f;
+    } else {
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) top = fmaxf(top, red_s[32 * (lq % kQuarters + kQuarters * c) + lane]);
+      if (top == -INFINITY) top = 0.f;  // (no key seen)
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) {
+        const int rc = 32 * (lq % kQuarters + kQuarters * c) + lane;
+        sum = fmaf(exp2f(red_s[rc] - top), l_s[rc] + l_s[128 + rc], sum);
+      }
+      inv = sum > 0.f ? exp2f(red_s[r] - top) / sum : 0.f;
+      const int gr = kTileRows * mt + 32 * lq + lane;
+      if (a.ws_o && lq < kQuarters && part == 0 && gr < rows && rows_ok)
+        a.ws_lse[plane + out_row(gr)] = sum > 0.f ? top + log2f(sum) : -INFINITY;
+    }
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16) + kColO + part * (D / 4);
     // The rows go through shared memory (nothing else uses it any more), 16
     // bytes apart from a multiple of 128 so that the lanes' stores meet no
     // bank conflict, and leave as one bulk copy a row.
-    const int bytes = a.ws_o ? D * 4 : D * 2;
+    const bool wide = kCopies > 1 || a.ws_o;
+    const int bytes = wide ? D * 4 : D * 2;
     uint8_t *srow = smem + r * (bytes + 16);
 #pragma unroll 1
     for (int c16 = 0; c16 < D / 64; ++c16) {
@@ -725,7 +770,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         for (int e = 0; e < 16; ++e) rr[e] = 0u;
       }
       const int col = part * (D / 4) + c16 * 16;
-      if (a.ws_o) {
+      if (wide) {
         float4 *dst = reinterpret_cast<float4 *>(srow + 4 * col);
 #pragma unroll
         for (int e4 = 0; e4 < 4; ++e4)
@@ -746,10 +791,39 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         dst[1] = make_uint4(ow[4], ow[5], ow[6], ow[7]);
       }
     }
+    if constexpr (kCopies > 1) {
+      // The copies' shares of a row added in order, a warp a row.
+      named_barrier(10, 16 * 32);
+      for (int rr = warp - kKWarps; rr < kTileRows; rr += 16) {
+        const int gr = kTileRows * mt + rr;
+        if (gr >= rows || !rows_ok) break;  // warp-uniform
+        const size_t orow = out_row(gr);
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 128) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < kCopies; ++c) {
+            const float4 o = *reinterpret_cast<const float4 *>(
+                smem + (rr + kTileRows * c) * (bytes + 16) + 4 * c0 + 16 * lane);
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+          }
+          const size_t at = orow * D + c0 + 4 * lane;
+          if (a.ws_o) {
+            *reinterpret_cast<float4 *>(a.ws_o + plane * D + at) = v;
+          } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2 *>(a.out + at) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+          }
+        }
+      }
+    } else {
     fence_proxy_async_smem();
     named_barrier(6 + lq, 128);  // the four warps of these rows
     if (part == 0) {
-      if (write) {
+      const int gr = 128 * mt + r;
+      if (gr < rows && rows_ok) {
+        const size_t orow = out_row(gr);
         void *dst = a.ws_o ? (void *)(a.ws_o + (plane + orow) * D) : (void *)(a.out + orow * D);
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
                      "r"(smem_u32(srow)), "r"(bytes)
@@ -757,6 +831,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
     }
   }
 
@@ -843,7 +918,7 @@ prefill_mod_merge_kernel(const float *__restrict__ ws_o, const float *__restrict
     *reinterpret_cast<uint2 *>(dst) = make_uint2(ow[0], ow[1]);
 }
 
-template <int D, class Mod>
+template <int D, int kCopies, class Mod>
 cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, const int32_t *cu_q,
                      int T, int total_q, int max_q, int Hq, float sm_scale, void *out,
                      int num_splits, float *ws_o, float *ws_lse, cudaStream_t stream,
@@ -851,9 +926,10 @@ cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, con
   CUtensorMap map;
   if (!make_pool_tmap(c, &map)) return cudaErrorNotSupported;
   const int G = Hq / c.num_kv_heads;
-  const int mtiles = (int)(((int64_t)max_q * G + 127) / 128);
+  constexpr int kTileRows = 128 / kCopies;
+  const int mtiles = (int)(((int64_t)max_q * G + kTileRows - 1) / kTileRows);
   constexpr int smem = Cfg<D>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(prefill_mod_kernel<D, Mod>,
+  cudaError_t e = cudaFuncSetAttribute(prefill_mod_kernel<D, kCopies, Mod>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   Args a;
@@ -867,7 +943,7 @@ cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, con
   a.ws_o = num_splits > 1 ? ws_o : nullptr, a.ws_lse = ws_lse;
   a.err = s.err_word;
   const dim3 grid((unsigned)(mtiles * num_splits), (unsigned)c.num_kv_heads, (unsigned)s.batch);
-  prefill_mod_kernel<D, Mod><<<grid, kThreads, smem, stream>>>(map, a, mod);
+  prefill_mod_kernel<D, kCopies, Mod><<<grid, kThreads, smem, stream>>>(map, a, mod);
   if ((e = cudaGetLastError()) != cudaSuccess || num_splits == 1) return e;
   const int per_block = num_splits > 8 ? 1 : kMergeThreads / 32;
   cudaLaunchConfig_t cfg = {};
@@ -883,7 +959,33 @@ cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, con
   return cudaLaunchKernelEx(
       &cfg, num_splits > 8 ? prefill_mod_merge_kernel<D, 8> : prefill_mod_merge_kernel<D, 1>,
       (const float *)ws_o, (const float *)ws_lse, num_splits, cu_q, T, total_q, Hq, G,
-      128 * mtiles, static_cast<__nv_bfloat16 *>(out));
+      kTileRows * mtiles, static_cast<__nv_bfloat16 *>(out));
+}
+
+// Copies of the query rows in a tile: as many as fit when a sequence has one
+// tile at most.
+int copies_of(int max_q, int G) {
+  const int64_t rows = (int64_t)max_q * G;
+  return rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+}
+
+template <class Mod>
+cudaError_t launch_rows(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
+                        const int32_t *cu_q, int T, int total_q, int max_q, int Hq, float sm_scale,
+                        void *out, int num_splits, float *ws_o, float *ws_lse, cudaStream_t stream,
+                        const Mod &mod) {
+  auto go = [&](auto copies) {
+    constexpr int kCopies = decltype(copies)::value;
+    return c.head_dim == 256
+               ? launch_d<256, kCopies>(c, s, q, cu_q, T, total_q, max_q, Hq, sm_scale, out,
+                                        num_splits, ws_o, ws_lse, stream, mod)
+               : launch_d<128, kCopies>(c, s, q, cu_q, T, total_q, max_q, Hq, sm_scale, out,
+                                        num_splits, ws_o, ws_lse, stream, mod);
+  };
+  const int copies = copies_of(max_q, Hq / c.num_kv_heads);
+  if (copies == 4) return go(std::integral_constant<int, 4>{});
+  if (copies == 2) return go(std::integral_constant<int, 2>{});
+  return go(std::integral_constant<int, 1>{});
 }
 
 }  // namespace
@@ -931,10 +1033,8 @@ cudaError_t launch_prefill_mod(const nvkv_cache &c, const nvkv_seqs &s, const vo
   if (num_splits < 1 || num_splits > kMaxSplits || (num_splits > 1 && (!ws_o || !ws_lse)))
     return cudaErrorInvalidValue;
   return with_mod(mod, [&](const auto &m) {
-    return c.head_dim == 256 ? launch_d<256>(c, s, q, cu_q, 0, total_q, max_q, Hq, sm_scale, out,
-                                             num_splits, ws_o, ws_lse, stream, m)
-                             : launch_d<128>(c, s, q, cu_q, 0, total_q, max_q, Hq, sm_scale, out,
-                                             num_splits, ws_o, ws_lse, stream, m);
+    return launch_rows(c, s, q, cu_q, 0, total_q, max_q, Hq, sm_scale, out, num_splits, ws_o,
+                       ws_lse, stream, m);
   });
 }
 
@@ -950,10 +1050,8 @@ cudaError_t launch_decode_rows(const nvkv_cache &c, const nvkv_seqs &s, const vo
   const int S = estimate_splits(n, visible_keys(s, mod, T), (int64_t)total_q * Hq * c.head_dim,
                                 false, room > 1 ? room : 1, sms);
   return with_mod(mod, [&](const auto &m) {
-    return c.head_dim == 256 ? launch_d<256>(c, s, q, nullptr, T, total_q, T, Hq, sm_scale, out, S,
-                                             ws_o, ws_lse, stream, m)
-                             : launch_d<128>(c, s, q, nullptr, T, total_q, T, Hq, sm_scale, out, S,
-                                             ws_o, ws_lse, stream, m);
+    return launch_rows(c, s, q, nullptr, T, total_q, T, Hq, sm_scale, out, S, ws_o, ws_lse, stream,
+                       m);
   });
 }
 
