@@ -628,7 +628,14 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // factors, query terms and S^T slot are ready; the other issues the
     // value MMAs of each unit once its V^T and P are ready.  Each commits
     // its own MMAs; the tensor pipe runs both streams.
-    if (lane == 0) {
+    {
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+      const uint32_t n = __reduce_max_sync(0xffffffffu, n_units);
+      auto aborted = [&]() { return __any_sync(0xffffffffu, sh.flags[2]); };
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        wait_bar(bar, parity, sh.flags, err);
+        __syncwarp();
+      };
       int64_t seg_end = segment(0, u0).seg_end;
       uint32_t seg_idx = 0;
       bool issued = false;
@@ -636,84 +643,84 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // NVFP4: E2M1 x E2M1 block-scaled; K8V4: E4M3 x E4M3 (kind::f8f6f4,
         // format 0 = E4M3), the same descriptor layout as the f16 kind.
         const uint32_t idesc_qk = K8 ? idesc_f16_f32(128, NS, false, false) : idesc_nvf4(128, NS);
-        const uint32_t qb = smem_u32(sh.qtile);
+        const uint64_t qd = smem_desc_rows<K8 ? 128 : D / 2>(smem_u32(sh.qtile));
         const uint32_t kt0 = smem_u32(sh.stages);
-        for (uint32_t qk = 0; qk < n_units && !sh.flags[2]; ++qk) {
+        for (uint32_t qk = 0; qk < n && !aborted(); ++qk) {
           const int64_t uu = u0 + qk;
           const bool opens = qk == 0 || uu >= seg_end;
           if (uu >= seg_end) {
             seg_end = segment(++seg_idx, uu).seg_end;
           }
-          if (opens) wait_bar(sh.qready, seg_idx & 1, sh.flags, err);
+          if (opens) wait(sh.qready, seg_idx & 1);
           const int stage = qk % kStages;
-          wait_bar(&sh.full[stage], (qk / kStages) & 1, sh.flags, err);
-          if (!K8) wait_bar(&sh.sfa_ready[qk & 1], (qk >> 1) & 1, sh.flags, err);
+          wait(&sh.full[stage], (qk / kStages) & 1);
+          if (!K8) wait(&sh.sfa_ready[qk & 1], (qk >> 1) & 1);
           // S^T was read by the softmax of unit qk-1
-          if (qk > 0) wait_bar(sh.sfree, (qk - 1) & 1, sh.flags, err);
+          if (qk > 0) wait(sh.sfree, (qk - 1) & 1);
           tc_fence_after();
-          const uint32_t sslot = tmem + kColS;
-          const uint32_t sfa = tmem + kColSFA + (qk & 1) * 16;
-          const uint32_t kt = kt0 + stage * kStageBytes;
+          const uint32_t sslot = tm + kColS;
+          const uint32_t sfa = tm + kColSFA + (qk & 1) * 16;
+          constexpr int kSwz = K8 ? 128 : D / 2;
+          const uint64_t kd = smem_desc_rows<kSwz>(kt0 + stage * kStageBytes);
           if constexpr (K8) {
             // two head_dim halves of 128 bytes, 4 K steps of 32 elements each
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                mma_f8_ss(sslot, smem_desc_sw128(kt + hf * kUnitPages * kKPageBytes + 32 * ks),
-                          smem_desc_sw128(qb + hf * kNSMax * 128 + 32 * ks), idesc_qk,
-                          (hf | ks) > 0);
+                mma_f8_ss_warp(sslot, desc_at(kd, hf * kUnitPages * kKPageBytes + 32 * ks),
+                               desc_at(qd, hf * kNSMax * 128 + 32 * ks), idesc_qk, (hf | ks) > 0);
           } else {
 #pragma unroll
             for (int ks = 0; ks < D / 64; ++ks)
-              mma_nvf4_ss(sslot, smem_desc_rows<D / 2>(kt + 32 * ks),
-                          smem_desc_rows<D / 2>(qb + 32 * ks), idesc_qk, ks > 0, sfa + 4 * ks,
-                          tmem + kColSFB + 4 * ks);
+              mma_nvf4_ss_warp(sslot, desc_at(kd, 32 * ks), desc_at(qd, 32 * ks), idesc_qk, ks > 0,
+                               sfa + 4 * ks, tm + kColSFB + 4 * ks);
           }
-          mma_commit(sh.sready);
-          mma_commit(&sh.empty[stage]);  // the K tile has been read
+          mma_commit_warp(sh.sready);
+          mma_commit_warp(&sh.empty[stage]);  // the K tile has been read
           // the last score MMA of a segment that another follows: the V^T
           // writers may build the next pair's query terms
-          if (uu + 1 >= seg_end && uu + 1 < u1) mma_commit(sh.qfree);
+          if (__any_sync(0xffffffffu, uu + 1 >= seg_end && uu + 1 < u1)) mma_commit_warp(sh.qfree);
           issued = true;
         }
         if (issued) {
-          mma_commit(sh.final_bar);
+          mma_commit_warp(sh.final_bar);
           mbar_wait(sh.final_bar, 0, kWaitBudget);
         }
       } else {
         const uint32_t idesc_pv = idesc_f16_f32(128, kNP, false, true);
         const uint32_t pb = smem_u32(sh.ptile);
-        for (uint32_t pv = 0; pv < n_units && !sh.flags[2]; ++pv) {
+        for (uint32_t pv = 0; pv < n && !aborted(); ++pv) {
           const int64_t uu = u0 + pv;
-          const bool first = pv == 0 || uu >= seg_end;  // O^T starts from zero
+          // O^T starts from zero
+          const bool first = __any_sync(0xffffffffu, pv == 0 || uu >= seg_end);
           if (uu >= seg_end)
             seg_end = segment(++seg_idx, uu).seg_end;
           const int ps = pv % kPSlots;
-          wait_bar(&sh.pready[ps], (pv / kPSlots) & 1, sh.flags, err);
-          const uint32_t pslot = pb + ps * kPSlotBytes;
+          wait(&sh.pready[ps], (pv / kPSlots) & 1);
+          const uint64_t pd = smem_desc(pb + ps * kPSlotBytes, 128, 2048);
           const int vs = pv % kVSlots;
-          const uint32_t vslot = tmem + kColV + vs * (D / 2);
+          const uint32_t vslot = tm + kColV + vs * (D / 2);
           // One half at a time (of head_dim; at head_dim 128 of the tokens):
           // each half's V^T is released as soon as its MMAs complete.
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            wait_bar(&sh.vready[vs * 2 + hf], (pv / kVSlots) & 1, sh.flags, err);
+            wait(&sh.vready[vs * 2 + hf], (pv / kVSlots) & 1);
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4 * kHalves; ++k) {
               const int ks = kHalves == 2 ? k : 4 * hf + k;  // K step: 16 tokens
-              mma_f16_ts(tmem + kColO + (kHalves == 2 ? hf * kNP : 0),
-                         vslot + (kHalves == 2 ? 64 * hf : 0) + ks * 8,
-                         smem_desc(pslot + ks * 256, 128, 2048), idesc_pv, (!first) || ks > 0);
+              mma_f16_ts_warp(tm + kColO + (kHalves == 2 ? hf * kNP : 0),
+                              vslot + (kHalves == 2 ? 64 * hf : 0) + ks * 8, desc_at(pd, ks * 256),
+                              idesc_pv, (!first) || ks > 0);
             }
-            mma_commit(&sh.pvdone[vs * 2 + hf]);
+            mma_commit_warp(&sh.pvdone[vs * 2 + hf]);
           }
-          mma_commit(&sh.pfree[ps]);
+          mma_commit_warp(&sh.pfree[ps]);
           issued = true;
         }
         if (issued) {
-          mma_commit(sh.final_pv);
+          mma_commit_warp(sh.final_pv);
           mbar_wait(sh.final_pv, 0, kWaitBudget);
         }
       }

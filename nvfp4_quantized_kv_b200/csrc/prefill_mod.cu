@@ -63,7 +63,7 @@ constexpr int kDeqWarps = kKWarps + kVWarps;
 constexpr int kSmxWarps = 8;      // two warpgroups: warps 12..15 and 16..19
 constexpr int kProducerWarp = 20;
 constexpr int kMmaWarp = 21;      // issues the score MMAs
-constexpr int kPvWarp = 22;       // issues the value MMAs
+                                  // (warp 22 the value MMAs)
 constexpr int kThreads = 23 * 32;
 constexpr int kHalf = kTileTokens / 2;  // keys of a softmax thread
 constexpr uint32_t kTmemCols = 512;
@@ -333,61 +333,66 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
           mbar_wait(&full[k % kStages], (k / kStages) & 1, kWaitBudget);
       }
       __syncwarp();
-    } else if (lane == 0 && ntiles > 0) {
+    } else if (ntiles > 0) {
       // ---------------------------------------------------------------- MMA
-      // Two issuing threads: issuing a batch of tcgen05.mma blocks the thread
+      // Two issuing warps: issuing a batch of tcgen05.mma blocks the thread
       // until it has nearly executed, so a single one held the value MMAs of
       // a tile back behind the next tile's scores, and with them the S slot
-      // that the scores after those wait for.
+      // that the scores after those wait for. The whole warp walks the loop
+      // and one lane issues (see mma_f16_ts_warp).
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+      const int nt = (int)__reduce_max_sync(0xffffffffu, (uint32_t)ntiles);
+      auto aborted = [&]() { return __any_sync(0xffffffffu, flags[2]); };
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        wait_bar(bar, parity, flags, a.err);
+        __syncwarp();
+      };
+      bool issued = false;
       if (warp == kMmaWarp) {
         const uint32_t idesc_qk = idesc_f16_f32(128, kTileTokens, false, false);
         const uint32_t kb = smem_u32(ktiles);
-        bool issued = false;
-        wait_bar(qready, 0, flags, a.err);
-        for (int j = 0; j < ntiles && !flags[2]; ++j) {
+        wait(qready, 0);
+        for (int j = 0; j < nt && !aborted(); ++j) {
           const int slot = j & 1;
-          wait_bar(&kready[slot], (j >> 1) & 1, flags, a.err);
+          wait(&kready[slot], (j >> 1) & 1);
           // the S slot: P of tile j-2 there has been used
-          if (j >= 2) wait_bar(&pvdone[slot], ((j >> 1) + 1) & 1, flags, a.err);
+          if (j >= 2) wait(&pvdone[slot], ((j >> 1) + 1) & 1);
           tc_fence_after();
-          const uint32_t kt = kb + slot * kKTileBytes;
-          const uint32_t scol = tmem + kColS + slot * 64;
+          const uint64_t kd = smem_desc(kb + slot * kKTileBytes, 1024, 128);
+          const uint32_t scol = tm + kColS + slot * 64;
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t bd = smem_desc(kt + ks * 2 * 1024, 1024, 128);
-            mma_f16_ts(scol, tmem + kColQ + ks * 8, bd, idesc_qk, ks > 0 ? 1u : 0u);
-          }
-          mma_commit(&sready[slot]);
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_f16_ts_warp(scol, tm + kColQ + ks * 8, desc_at(kd, ks * 2 * 1024), idesc_qk, ks > 0);
+          mma_commit_warp(&sready[slot]);
           issued = true;
         }
         if (issued) {
-          mma_commit(final_qk);
+          mma_commit_warp(final_qk);
           mbar_wait(final_qk, 0, kWaitBudget);
         }
       } else {
         const uint32_t idesc_pv = idesc_f16_f32(128, D, false, false);
         const uint32_t vb = smem_u32(vtiles);
-        bool issued = false;
-        for (int j = 0; j < ntiles && !flags[2]; ++j) {
+        for (int j = 0; j < nt && !aborted(); ++j) {
           const int slot = j & 1;
-          wait_bar(&vready[slot], (j >> 1) & 1, flags, a.err);
-          wait_bar(&pready[slot], (j >> 1) & 1, flags, a.err);
+          wait(&vready[slot], (j >> 1) & 1);
+          wait(&pready[slot], (j >> 1) & 1);
           tc_fence_after();
-          const uint32_t pcol = tmem + kColS + slot * 64;  // P: first 32 columns of the slot
-          const uint32_t vt = vb + slot * kVTileBytes;
+          const uint32_t pcol = tm + kColS + slot * 64;  // P: first 32 columns of the slot
+          const uint64_t vd = smem_desc(vb + slot * kVTileBytes, D * 16, 128);
 #pragma unroll
-          for (int ks = 0; ks < kTileTokens / 16; ++ks) {
-            const uint64_t bd = smem_desc(vt + ks * 2 * (D * 16), D * 16, 128);
-            mma_f16_ts(tmem + kColO, pcol + ks * 8, bd, idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
-          }
-          mma_commit(&pvdone[slot]);
+          for (int ks = 0; ks < kTileTokens / 16; ++ks)
+            mma_f16_ts_warp(tm + kColO, pcol + ks * 8, desc_at(vd, ks * 2 * (D * 16)), idesc_pv,
+                            j > 0 || ks > 0);
+          mma_commit_warp(&pvdone[slot]);
           issued = true;
         }
         if (issued) {
-          mma_commit(final_bar);
+          mma_commit_warp(final_bar);
           mbar_wait(final_bar, 0, kWaitBudget);
         }
       }
+      __syncwarp();
     }
   } else if (warp < kDeqWarps) {
     if (warp < kKWarps) {
