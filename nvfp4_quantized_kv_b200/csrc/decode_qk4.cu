@@ -1136,10 +1136,24 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             if constexpr (Mod::kOn) {
               if constexpr (Mod::kCap) {
+                float y[RM];
 #pragma unroll
                 for (int j = 0; j < RM; j += 2) {
-                  const float2 v = mod.cap(make_float2(x[j], x[j + 1]));
-                  x[j] = v.x, x[j + 1] = v.y;
+                  const float2 v = cap_small(mod, make_float2(x[j], x[j + 1]));
+                  y[j] = v.x, y[j + 1] = v.y;
+                }
+                float top = max3_abs(y[0], y[1], 0.f);
+#pragma unroll
+                for (int j = 2; j < RM; j += 2) top = max3_abs(y[j], y[j + 1], top);
+                if (__builtin_expect(__any_sync(0xffffffffu, !(top <= mod.cap_top)), 0)) {
+#pragma unroll
+                  for (int j = 0; j < RM; j += 2) {
+                    const float2 v = mod.cap(make_float2(x[j], x[j + 1]));
+                    x[j] = v.x, x[j + 1] = v.y;
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < RM; ++j) x[j] = y[j];
                 }
               }
               if constexpr (Mod::kBias) {
