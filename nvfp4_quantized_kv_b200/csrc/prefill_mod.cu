@@ -199,6 +199,35 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // The query rows, asked for before anything else is worked out: coalesced
+  // copies into the second K and V tile slots (free until the second tile),
+  // 16-byte chunks swizzled so that a row a lane reads them without bank
+  // conflicts. (Each lane loading its own row took 4,000 cycles of the
+  // load unit, and the page ids queued behind it.)
+  auto q_chunk = [&](int rr, int c) -> uint8_t * {
+    return (rr < 64 ? ktiles + kKTileBytes : vtiles + kVTileBytes) + (rr & 63) * (D * 2) +
+           ((c ^ (rr & 7)) << 4);
+  };
+  if (warp >= kKWarps && warp < kProducerWarp) {
+    constexpr int kRowChunks = D / 8, kAtOnce = 32 / kRowChunks;  // rows of an instruction
+    constexpr int kWarpRows = kTileRows / 16;
+    const int r0 = (warp - kKWarps) * kWarpRows, c = lane % kRowChunks;
+    // lane i knows where the warp's row i is (a division once)
+    const int mine = kTileRows * mt + r0 + lane % kWarpRows;
+    const int at = mine < rows && !bad ? mine / G * a.Hq + mine % G : -1;
+#pragma unroll
+    for (int i = 0; i < kWarpRows; i += kAtOnce) {
+      const int rr = i + lane / kRowChunks, from = __shfl_sync(0xffffffffu, at, rr);
+      uint8_t *dst = q_chunk(r0 + rr, c);
+      if (from >= 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+                     "l"(a.q + ((size_t)q0 * a.Hq + h * G + from) * D + 8 * c)
+                     : "memory");
+      else
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
   // The keys [key_lo, key_hi) that any row of the tile sees: every warp scans
   // the tile's tokens.
   int key_lo = 0x7fffffff, key_hi = 0;
@@ -256,25 +285,18 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= kKWarps && warp < kProducerWarp) {
-    // Q row -> Tensor Memory (A operand), f16, scaled to base-2 scores: 16
-    // warps, lane quarter warp % 4, a quarter of the columns each, so that a
-    // thread's loads are one latency. (Four warps with all columns had Q ready
-    // 3,000 to 6,000 cycles later.)
+    // Q row -> Tensor Memory (A operand), f16, scaled to base-2 scores: lane
+    // quarter warp % 4, a quarter of the columns each.
     const int lq = warp & 3, part = (warp - kKWarps) >> 2;
-    const int gr = kTileRows * mt + 32 * (lq % kQuarters) + lane;
-    const bool valid = gr < rows && !bad;
-    const __nv_bfloat16 *qr =
-        a.q + ((size_t)(q0 + gr / G) * a.Hq + h * G + gr % G) * D + part * (D / 4);
-    uint4 raw[D / 32];
-#pragma unroll
-    for (int v = 0; v < D / 32; ++v)
-      raw[v] = valid ? __ldg(reinterpret_cast<const uint4 *>(qr) + v) : make_uint4(0u, 0u, 0u, 0u);
+    const int rr = 32 * (lq % kQuarters) + lane;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    named_barrier(10, 16 * 32);  // every warp's rows are there
 #pragma unroll
     for (int c16 = 0; c16 < D / 128; ++c16) {
       uint32_t w[16];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const uint4 r4 = raw[4 * c16 + v];
+        const uint4 r4 = *reinterpret_cast<const uint4 *>(q_chunk(rr, part * (D / 32) + 4 * c16 + v));
         const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -428,7 +450,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);  // this warp's reads of the stage are done
-        // K tile slot: its previous tile's scores must be done.
+        // K tile slot: its previous tile's scores must be done (the second
+        // slot holds Q at first).
+        if (j == 1) wait_bar(qready, 0, flags, a.err);
         if (j >= 2) {
           wait_bar(&sready[slot], ((j >> 1) + 1) & 1, flags, a.err);
           tc_fence_after();
@@ -494,6 +518,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         named_barrier(1, kVWarps * 32);
         if (lane == 0) mbar_arrive(&empty[stage]);  // (the barrier follows every read)
         // V^T tile slot: its previous tile's value MMAs must be done.
+        if (j == 1) wait_bar(qready, 0, flags, a.err);
         if (j >= 2) {
           wait_bar(&pvdone[slot], ((j >> 1) + 1) & 1, flags, a.err);
           tc_fence_after();
@@ -727,6 +752,12 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     // ------------------------------------------------------------- epilogue
     // O / l -> out (or the split's plane), 16 warps: lane quarter warp % 4,
     // quarter warp / 4 of the columns.
+    // lane i knows where row 32 * lq + i goes (-1: nowhere)
+    int at = -1;
+    if (kCopies == 1) {
+      const int mine = 128 * mt + 32 * (warp & 3) + lane;
+      if (mine < rows && rows_ok) at = mine / G * a.Hq + mine % G;
+    }
     if (ntiles > 0) {
       wait_bar(final_bar, 0, flags, a.err);
       __syncwarp();
@@ -759,7 +790,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16) + kColO + part * (D / 4);
     // The rows go through shared memory (nothing else uses it any more), 16
     // bytes apart from a multiple of 128 so that the lanes' stores meet no
-    // bank conflict, and leave as one bulk copy a row.
+    // bank conflict, and leave coalesced.
     const bool wide = kCopies > 1 || a.ws_o;
     const int bytes = wide ? D * 4 : D * 2;
     uint8_t *srow = smem + r * (bytes + 16);
@@ -823,20 +854,20 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         }
       }
     } else {
-    fence_proxy_async_smem();
-    named_barrier(6 + lq, 128);  // the four warps of these rows
-    if (part == 0) {
-      const int gr = 128 * mt + r;
-      if (gr < rows && rows_ok) {
-        const size_t orow = out_row(gr);
-        void *dst = a.ws_o ? (void *)(a.ws_o + (plane + orow) * D) : (void *)(a.out + orow * D);
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                     "r"(smem_u32(srow)), "r"(bytes)
-                     : "memory");
+      named_barrier(6 + lq, 128);  // the four warps of these rows
+      // Eight rows a warp, 16 bytes a lane.
+      const int shift = __ffs(bytes / 16) - 1;  // (row bytes are a power of two)
+      const size_t row0 = (size_t)q0 * a.Hq + h * G;
+      uint8_t *first = a.ws_o ? (uint8_t *)(a.ws_o + (plane + row0) * D)
+                              : (uint8_t *)(a.out + row0 * D);
+#pragma unroll 4
+      for (int k = lane; k < 8 << shift; k += 32) {
+        const int i = 8 * part + (k >> shift), off = (k & ((1 << shift) - 1)) * 16;
+        const int to = __shfl_sync(0xffffffffu, at, i);
+        if (to >= 0)
+          *reinterpret_cast<uint4 *>(first + (size_t)to * bytes + off) =
+              *reinterpret_cast<const uint4 *>(smem + (32 * lq + i) * (bytes + 16) + off);
       }
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    }
     }
   }
 
