@@ -66,12 +66,13 @@ DATASHEET_BF16_TFLOPS = 2250.0  # dense
 DECODE_CAPTURE = {
     "kernel": "decode_qk4",
     "sources": ["nvfp4_quantized_kv_b200/csrc/decode_qk4.cu",
+                "nvfp4_quantized_kv_b200/csrc/score_mod.cuh",
                 "nvfp4_quantized_kv_b200/csrc/sm100.cuh",
                 "nvfp4_quantized_kv_b200/csrc/nvkv_common.cuh",
                 "include/nvkv.h"],
-    "sha256": "cc497b3949b877049093e0c373fdab8f332cd7d4eeca000e7c4e2d88e85a02cb",
-    "dram_bytes_read": 207595776,
-    "dram_bytes_write": 3718912,
+    "sha256": "4ede9dc008e72d56fde350202eac42f1e622186f46c10154edcf29db2815aae2",
+    "dram_bytes_read": 207596288,
+    "dram_bytes_write": 3389440,
     "kv_bytes": 207363456,
 }
 

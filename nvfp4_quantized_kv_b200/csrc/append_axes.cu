@@ -24,6 +24,11 @@
 //    written (the other nibble of such a byte is kept).  They come first in
 //    the grid and load their 8 rows at once: one warp for a whole page, row
 //    after row, at the grid's end, made the launch twice as long.
+//
+// Measured (24/4 heads, head_dim 256, queries included): 2,048 rows, rotary
+// width 128: 15.2 us, 61 MB = 4,020 GB/s, 0.61 of the measured copy rate (4
+// blocks an SM are one wave and a half of dependent loads); one row for each
+// of 64 sequences: 6.6 us, the launch and four dependent loads.
 #include "nvkv_common.cuh"
 
 namespace nvkv {

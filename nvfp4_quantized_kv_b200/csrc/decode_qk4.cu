@@ -67,7 +67,7 @@
 //    2^8, detected by a vote), fp32 exp2, P to a 4-slot ring in shared
 //    memory, the denominator from the same f16 weights; at a segment start
 //    they build the query terms.
-//  * warp 13 issues the score MMAs, warp 14 the value MMAs (one thread each).
+//  * warp 13 issues the score MMAs, warp 14 the value MMAs.
 //  * Every wait is bounded; a timeout sets NVKV_DEVERR_TIMEOUT, turns later
 //    waits into no-ops and lets the kernel drain and free its Tensor Memory.
 //
@@ -80,9 +80,9 @@
 // before the roles start (every role walking the sequences cost microseconds
 // at a batch of 64), and kernels are instances by cap and bias because the
 // roles share the instruction caches.  Measured (nvkv_decode_attn_mod with
-// its merge): 4 x 32k tokens, cap, 24/4 heads, head_dim 256: 351 us, 0.61 of
-// the time that the cache bytes need at the copy rate; 64 windows of 4,096
-// tokens: 104 us, 0.43; one sequence of 4,097 tokens, 8/2 heads, head_dim
+// its merge): 3 x {330k, 420k, 470k} tokens, cap, 24/4 heads, head_dim 256:
+// 338 us, 0.63 of the measured copy rate; 64 windows of 4,096 tokens: 94 us,
+// 0.47; one sequence of 4,097 tokens, 8/2 heads, head_dim
 // 128: 14.4 us, which is the launch of two kernels, the set-up (about 7,000
 // cycles before the first unit) and one drain.  What bounds it per unit is
 // the plain kernel's hand-off from the V^T writers to the value MMAs (about
@@ -621,10 +621,12 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kPvWarp) {
     // ------------------------------------------------------------------ MMA
-    // Two issuing threads: issuing a batch of tcgen05.mma blocks the thread
-    // until the batch has nearly executed, so a single thread would leave
-    // the tensor pipe idle while it waits for the next step's inputs.  One
-    // thread issues the scores of each unit as soon as its tiles, scale
+    // Two issuing warps: issuing a batch of tcgen05.mma blocks the thread
+    // until the batch has nearly executed, so a single one would leave the
+    // tensor pipe idle while it waits for the next step's inputs.  Each walks
+    // its loop converged and one lane issues (see mma_f16_ts_warp: 2 % of the
+    // plain step, 3 % of the masked one, 12 % of one of many windows).  One
+    // issues the scores of each unit as soon as its tiles, scale
     // factors, query terms and S^T slot are ready; the other issues the
     // value MMAs of each unit once its V^T and P are ready.  Each commits
     // its own MMAs; the tensor pipe runs both streams.

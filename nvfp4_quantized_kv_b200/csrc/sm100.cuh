@@ -245,38 +245,13 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uin
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
       : "memory");
 }
-// D[tmem] (+)= (A[smem] x SFA[tmem]) * (B[smem] x SFB[tmem]): the NVFP4
-// block-scaled MMA (kind::mxf4nvf4, one UE4M3 scale per 16 E2M1 elements
-// along K, K = 64 per instruction), fp32 accumulate.
-__device__ __forceinline__ void mma_nvf4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate,
-                                            uint32_t sfa_tmem, uint32_t sfb_tmem) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], "
-      "p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
-      : "memory");
-}
-// D[tmem] (+)= A[smem] * B[smem], kind::f8f6f4 (8-bit A and B, K = 32 per
-// instruction), f32 accumulate; the instruction descriptor gives the types
-// (idesc_f16_f32's layout, where format 0 means E4M3 for this kind).
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// The same MMA and its commit for a converged warp, issued by its elected lane
-// (always the same one).  Operands that are the same in all lanes for the
-// compiler to see stay in uniform registers, so an MMA is one or two
-// instructions; in a branch that one thread takes they have to be moved there
-// one by one (the prefill's 16 score MMAs: 1,850 cycles instead of the 800
-// that the tensor pipe needs).
+// D[tmem] (+)= A[tmem] * B[smem] for a converged warp, issued by its elected lane
+// (always the same one).  The instruction takes its operands from uniform
+// registers: where the compiler can see that all lanes hold the same, they are
+// there already, while a branch that one thread takes has to move them, one
+// by one, for every MMA (the masked prefill's 16 score MMAs of a tile took
+// 1,850 cycles to issue that way and take 900 this way; the tensor pipe needs
+// 800).
 __device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                                 uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -287,6 +262,9 @@ __device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// D[tmem] (+)= (A[smem] x SFA[tmem]) * (B[smem] x SFB[tmem]): the NVFP4
+// block-scaled MMA (kind::mxf4nvf4, one UE4M3 scale per 16 E2M1 elements
+// along K, K = 64 per instruction), fp32 accumulate; converged warp.
 __device__ __forceinline__ void mma_nvf4_ss_warp(uint32_t d_tmem, uint64_t a_desc,
                                                  uint64_t b_desc, uint32_t idesc,
                                                  uint32_t accumulate, uint32_t sfa_tmem,
@@ -300,6 +278,10 @@ __device__ __forceinline__ void mma_nvf4_ss_warp(uint32_t d_tmem, uint64_t a_des
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
       : "memory");
 }
+// D[tmem] (+)= A[smem] * B[smem], kind::f8f6f4 (8-bit A and B, K = 32 per
+// instruction), f32 accumulate; the instruction descriptor gives the types
+// (idesc_f16_f32's layout, where format 0 means E4M3 for this kind);
+// converged warp.
 __device__ __forceinline__ void mma_f8_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                                uint32_t idesc, uint32_t accumulate) {
   asm volatile(
