@@ -401,3 +401,46 @@ def test_a_loose_bound_of_the_chunk_lengths():
         outs.append(out)
     torch.cuda.synchronize()
     assert torch.isfinite(outs[0]).all() and torch.equal(*outs)
+
+
+FEW = [  # rows of a kv-head: n * Hq / Hkv at most 32, and at most 64
+    (24, 4, 256, [300, 77, 6], [5, 1, 3]),
+    (24, 4, 256, [300, 77, 130], [10, 2, 9]),
+    (16, 2, 128, [300, 77, 4], [4, 3, 4]),
+    (16, 2, 128, [200, 65, 129], [8, 1, 7]),
+    (12, 1, 256, [190], [1]),
+    (4, 4, 128, [700, 64], [32, 31]),
+    (4, 4, 256, [140, 900], [64, 33]),
+]
+
+
+@pytest.mark.parametrize("masks", ["none", "window", "all"])
+@pytest.mark.parametrize("c", FEW, ids=[f"{c[0]}_{c[1]}_{c[2]}_{max(c[4])}" for c in FEW])
+def test_prefill_of_few_rows(c, masks):
+    """Chunks short enough for a tile to hold several copies of its rows."""
+    Hq, Hkv, D, lens, n = c
+    case = Case(Hq, Hkv, D, lens, n, seed=41).device()
+    m = {"none": Mod(), "window": Mod(window=50, cap=12.0),
+         "all": Mod(cap=20.0, window=77, slopes=slopes(Hq), prefix=[l - 2 for l in lens],
+                    starts=[i * 5 % 90 for i in range(sum(n))])}[masks]
+    ref, tol = case.reference(m, D ** -0.5, False, "f16 scores")
+    for splits in (0, 1, 3):
+        assert_within(run_prefill(case, m, D ** -0.5, splits), ref, tol, f"S{splits}")
+    assert int(case.err.item()) == 0
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(256, 24, 4), (128, 16, 2)])
+@pytest.mark.parametrize("n", [1, 2, 4, 8, 150])
+def test_the_same_call_gives_the_same_bits(D, Hq, Hkv, n):
+    """Sums have a fixed order: 40 calls, one after another, agree."""
+    case = Case(Hq, Hkv, D, [900, 333, 257], [min(n, 16)] * 3 if n <= 16 else [n, 90, 120], seed=43).device()
+    m = Mod(cap=15.0, window=300, slopes=slopes(Hq))
+    run = (lambda: run_decode(case, m, n, D ** -0.5)) if n <= 16 else (lambda: run_prefill(case, m, D ** -0.5))
+    first = run()
+    assert torch.isfinite(first).all()
+    for _ in range(40):
+        assert torch.equal(run(), first)
+    if n <= 16:
+        first = run_prefill(case, m, D ** -0.5)
+        for _ in range(40):
+            assert torch.equal(run_prefill(case, m, D ** -0.5), first)
