@@ -33,7 +33,8 @@
 //    MMAs themselves need 800 (scores: 48 cycles an instruction is the least
 //    at N = 64) and 512.
 // Not faster: four softmax warpgroups, on one tile or in pairs on two; 8 warps
-// for K; integer instead of converting dequantisation; rolled issue loops.
+// for K; integer instead of converting dequantisation; rolled issue loops;
+// rolled conversion loops.
 //   warps  0.. 3  K tile: a token a thread, D/64 chunks of 32 elements
 //   warps  4..11  V^T tile: a head_dim row a thread, D/64 pages
 //   warps 12..15  softmax of the tile's keys  0..31: a query row a thread
@@ -52,8 +53,9 @@
 // the next CTA's start on the SM. Packed documents of 1,500 tokens (8,192 +
 // 2,048): 82.7 us = 492 TFLOP/s; windows of 1,024 in chunks of 512, 301, 777
 // and 65 tokens: 79 us, 2.16 waves of such CTAs. A verify step of 24 rows
-// over 2 x 32,768 tokens, 18 CTAs a pair: 46 us, bound by one tile's chain
-// of waits in the V^T warps (2,130 cycles).
+// over 2 x 32,768 tokens, 18 CTAs a pair: 47 us; its K and V^T warps are busy
+// 2,000 of the 2,130 cycles a tile. (Reading a tile's bytes while the tile
+// before is converted gained nothing there and cost the long prefill 11 %.)
 #include <type_traits>
 
 #include "score_mod.cuh"
@@ -212,6 +214,31 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (bad && threadIdx.x == 0) report(a.err, NVKV_DEVERR_LENGTH);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kDeqWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kready[i], kKWarps);
+      mbar_init(&vready[i], kVWarps);
+      mbar_init(&sready[i], 1);
+      mbar_init(&pready[i], kSmxWarps);
+      mbar_init(&pvdone[i], 1);
+    }
+    mbar_init(qready, 16);
+    mbar_init(final_bar, 1);
+    mbar_init(final_qk, 1);
+    mbar_init(lready, kSmxWarps);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 4) flags[threadIdx.x] = 0;
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+
   // The query rows, asked for before anything else is worked out: coalesced
   // copies into the second K and V tile slots (free until the second tile),
   // 16-byte chunks swizzled so that a row a lane reads them without bank
@@ -268,29 +295,23 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     return (tile_lo + (Mod::kBias ? ntiles_all - 1 - (j0 + j) : j0 + j)) * kTileTokens;
   };
 
-  if (bad && threadIdx.x == 0) report(a.err, NVKV_DEVERR_LENGTH);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kDeqWarps);
+  // (the TMA warp) pages of the tiles: lane p's of every four
+  const int32_t *pt = a.page_table + (size_t)b * a.max_pages;
+  const int p = lane & 3;
+  auto page_for = [&](int j) -> int {
+    const int tok = tile_key(j) + p * kPageTokens;
+    if (tok >= key_hi || tok + kPageTokens <= key_lo) return -1;  // nobody sees it
+    const int pg = pt[tok / kPageTokens];
+    if (pg < 0 || pg >= a.num_pages) {
+      if (lane < kTilePages) report(a.err, NVKV_DEVERR_PAGE_ID);
+      return -1;
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&kready[i], kKWarps);
-      mbar_init(&vready[i], kVWarps);
-      mbar_init(&sready[i], 1);
-      mbar_init(&pready[i], kSmxWarps);
-      mbar_init(&pvdone[i], 1);
-    }
-    mbar_init(qready, 16);
-    mbar_init(final_bar, 1);
-    mbar_init(final_qk, 1);
-    mbar_init(lready, kSmxWarps);
-    fence_mbar_init();
-  }
-  if (threadIdx.x < 4) flags[threadIdx.x] = 0;
-  if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+    return pg;
+  };
+  int first_page = -1;
+  if (warp == kProducerWarp) {
+    prefetch_tmap(&tmap);
+    if (ntiles > 0) first_page = page_for(0);
   }
   tc_fence_before();
   __syncthreads();
@@ -329,20 +350,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   if (warp >= kProducerWarp) {
     if (warp == kProducerWarp) {
       // ---------------------------------------------------------------- TMA
-      prefetch_tmap(&tmap);
-      const int32_t *pt = a.page_table + (size_t)b * a.max_pages;
-      const int p = lane & 3;
-      auto page_for = [&](int j) -> int {
-        const int tok = tile_key(j) + p * kPageTokens;
-        if (tok >= key_hi || tok + kPageTokens <= key_lo) return -1;  // nobody sees it
-        const int pg = pt[tok / kPageTokens];
-        if (pg < 0 || pg >= a.num_pages) {
-          if (lane < kTilePages) report(a.err, NVKV_DEVERR_PAGE_ID);
-          return -1;
-        }
-        return pg;
-      };
-      int cur = ntiles > 0 ? page_for(0) : -1;
+      int cur = first_page;
       for (int j = 0; j < ntiles; ++j) {
         const int stage = j % kStages;
         const int nxt = j + 1 < ntiles ? page_for(j + 1) : -1;
