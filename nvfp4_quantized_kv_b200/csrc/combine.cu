@@ -144,6 +144,7 @@ combine_mod_kernel(const int32_t *__restrict__ kv_lens, int B, int Hkv, int T, i
     c1 = range_of_unit_mod(pair_start + units - 1, U, Se);
   }
   sm100::grid_dependency_wait();
+  sm100::launch_dependents();  // (not before: the attention's SMs are free now)
 
   const float *lse = ws_lse + (size_t)bh * R + r;
   float mx = -INFINITY;
@@ -212,16 +213,9 @@ cudaError_t launch_combine_mod(const nvkv_seqs &s, const float *ws_o, const floa
   // ranges a pair can span: its share of the splits and one at either end
   const bool shared = S / ((int64_t)s.batch * Hkv) + 2 > 4;
   const int per_block = shared ? 1 : kMergeThreads / 32;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((rows + per_block - 1) / per_block));
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared ? combine_mod_kernel<8> : combine_mod_kernel<1>,
+  const DependentLaunch launch(dim3((unsigned)((rows + per_block - 1) / per_block)), kMergeThreads,
+                               0, stream, true);
+  return cudaLaunchKernelEx(&launch.cfg, shared ? combine_mod_kernel<8> : combine_mod_kernel<1>,
                             s.kv_lens, s.batch, Hkv, T, Hq, D, S, ws_o, ws_lse,
                             static_cast<__nv_bfloat16 *>(out), mod);
 }

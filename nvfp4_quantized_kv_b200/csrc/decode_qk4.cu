@@ -504,7 +504,12 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
   SegList *seg_head = reinterpret_cast<SegList *>(smem + F::kOffSegs);
   Seg *segs = reinterpret_cast<Seg *>(smem + F::kOffSegs + 16);
   if constexpr (Mod::kOn) {
-    launch_dependents();  // the merge may be set up while this kernel runs
+    // The kernel before may still be running (programmatic dependent launch):
+    // nothing of global memory is touched before it has ended.  The merge in
+    // turn may be set up while this kernel runs, but not earlier: it reads the
+    // lengths ahead of its own wait.
+    grid_dependency_wait();
+    launch_dependents();
     if (warp == kPvWarp)
       list_segments(mod, kv_lens, B, Hkv, T, c, S, max_kv_len, max_pages, seg_head, segs);
   }
@@ -1421,11 +1426,12 @@ cudaError_t launch_fmt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, i
   const int smem = Fmt<D, K8>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<S, kThreads, smem, stream>>>(
-      map_k, map_ks, map_v, c.num_pages, c.num_kv_heads, s.page_table, s.max_pages_per_seq,
-      s.kv_lens, s.batch, s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), T, Hq, qscale, S,
-      ws_o, ws_lse, s.err_word, mod);
-  return cudaGetLastError();
+  const DependentLaunch launch(S, kThreads, smem, stream, Mod::kOn);
+  return cudaLaunchKernelEx(
+      &launch.cfg, kernel, map_k, map_ks, map_v, c.num_pages, c.num_kv_heads,
+      (const int32_t *)s.page_table, s.max_pages_per_seq, (const int32_t *)s.kv_lens, s.batch,
+      s.max_kv_len, static_cast<const __nv_bfloat16 *>(q), T, Hq, qscale, S, ws_o, ws_lse,
+      s.err_word, mod);
 }
 
 }  // namespace

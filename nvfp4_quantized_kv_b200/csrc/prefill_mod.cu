@@ -172,6 +172,10 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   // blockIdx.x = m-tile * num_splits + split: split s of an m-tile takes the
   // s-th of num_splits equal runs of its key tiles and, when num_splits > 1,
   // leaves O / l and log2(l) + m of its rows in the workspace for the merge.
+  // The kernel before may still be running (programmatic dependent launch). The
+  // merge in turn may be set up while this one runs, but not earlier: it reads
+  // the chunk bounds ahead of its own wait.
+  grid_dependency_wait();
   launch_dependents();
   const int mt = blockIdx.x / a.num_splits, split = blockIdx.x % a.num_splits;
   const int h = blockIdx.y, b = blockIdx.z;
@@ -929,6 +933,7 @@ prefill_mod_merge_kernel(const float *__restrict__ ws_o, const float *__restrict
   const size_t row = (size_t)q0 * Hq + (live ? idx : 0);
   const size_t plane = (size_t)total_q * Hq;
   grid_dependency_wait();
+  launch_dependents();  // (not before: the attention's SMs are free now)
   const float my_lse = live && lane < num_splits ? ws_lse[lane * plane + row] : -INFINITY;
   const float mx = warp_max(my_lse);
   const float my_w = my_lse > -INFINITY ? exp2f(my_lse - mx) : 0.f;
@@ -1000,21 +1005,15 @@ cudaError_t launch_d(const nvkv_cache &c, const nvkv_seqs &s, const void *q, con
   a.ws_o = num_splits > 1 ? ws_o : nullptr, a.ws_lse = ws_lse;
   a.err = s.err_word;
   const dim3 grid((unsigned)(mtiles * num_splits), (unsigned)c.num_kv_heads, (unsigned)s.batch);
-  prefill_mod_kernel<D, kCopies, Mod><<<grid, kThreads, smem, stream>>>(map, a, mod);
-  if ((e = cudaGetLastError()) != cudaSuccess || num_splits == 1) return e;
+  const DependentLaunch launch(grid, kThreads, smem, stream, true);
+  e = cudaLaunchKernelEx(&launch.cfg, prefill_mod_kernel<D, kCopies, Mod>, map, (const Args)a, mod);
+  if (e != cudaSuccess || num_splits == 1) return e;
   const int per_block = num_splits > 8 ? 1 : kMergeThreads / 32;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((int64_t)max_q * Hq + per_block - 1) / per_block),
-                     (unsigned)s.batch);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  const DependentLaunch merge(
+      dim3((unsigned)(((int64_t)max_q * Hq + per_block - 1) / per_block), (unsigned)s.batch),
+      kMergeThreads, 0, stream, true);
   return cudaLaunchKernelEx(
-      &cfg, num_splits > 8 ? prefill_mod_merge_kernel<D, 8> : prefill_mod_merge_kernel<D, 1>,
+      &merge.cfg, num_splits > 8 ? prefill_mod_merge_kernel<D, 8> : prefill_mod_merge_kernel<D, 1>,
       (const float *)ws_o, (const float *)ws_lse, num_splits, cu_q, T, total_q, Hq, G,
       kTileRows * mtiles, static_cast<__nv_bfloat16 *>(out));
 }

@@ -151,6 +151,26 @@ auto with_mod(const ScoreMod &m, F &&f) {
   return m.slopes ? as(ScoreModOf<false, true>{}) : as(ScoreModOf<false, false>{});
 }
 
+// A launch that, with `dependent`, may start while the kernel before it in the
+// stream ends (programmatic dependent launch): the masked attention kernels and
+// their merges wait for that kernel in the device code before they touch
+// global memory, so the launches' latencies lie behind one another's work.
+struct DependentLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  DependentLaunch(dim3 grid, int threads, int smem, cudaStream_t stream, bool dependent) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+  }
+  DependentLaunch(const DependentLaunch &) = delete;  // cfg points into it
+};
+
 // Ranges that the split plan of U units really has: the masked attention deals
 // them to at most U of the S splits, so that every range owns a unit and the
 // merge meets no empty one; the plain plan has S.

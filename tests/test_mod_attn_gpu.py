@@ -408,7 +408,7 @@ FEW = [  # rows of a kv-head: n * Hq / Hkv at most 32, and at most 64
     (24, 4, 256, [300, 77, 130], [10, 2, 9]),
     (16, 2, 128, [300, 77, 4], [4, 3, 4]),
     (16, 2, 128, [200, 65, 129], [8, 1, 7]),
-    (12, 1, 256, [190], [1]),
+    (10, 1, 256, [190], [1]),
     (4, 4, 128, [700, 64], [32, 31]),
     (4, 4, 256, [140, 900], [64, 33]),
 ]

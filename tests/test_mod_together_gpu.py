@@ -229,3 +229,58 @@ def test_score_mod_attributes_may_change():
     mod.key_starts = torch.zeros(1, dtype=torch.int64, device=dev)
     with pytest.raises(TypeError, match="key_starts"):
         run(mod)
+
+
+@pytest.mark.parametrize("kind", ["decode", "verify", "prefill", "prefill split"])
+def test_back_to_back_calls_see_what_the_kernel_before_wrote(kind):
+    """The attention kernels may be set up while the kernel before them ends:
+    lengths, queries and rows written just before a call, by kernels that take
+    their time, and a workspace still being merged, are waited for."""
+    dev = torch.device("cuda")
+    Hq, Hkv, D, L = 24, 4, 256, 2000
+    g = torch.Generator(device=dev).manual_seed(11)
+    cache = nv.Cache.allocate(130, Hkv, D, dev, fill=0)
+    lens = torch.tensor([L], dtype=torch.int32, device=dev)
+    seqs = nv.Seqs(torch.arange(128, dtype=torch.int32, device=dev)[None], lens, 2048)
+    kv = [torch.randn((L, Hkv, D), generator=g, device=dev).bfloat16() for _ in range(2)]
+    nv.nvkv_append(cache, seqs, kv[0], kv[1], torch.tensor([0, L], dtype=torch.int32, device=dev), L, L)
+    n = {"decode": 1, "verify": 4, "prefill": 100, "prefill split": 100}[kind]
+    size = max(nv.nvkv_decode_workspace_bytes(1, min(n, 16), Hq, Hkv, D, 0),
+               nv.nvkv_prefill_workspace_bytes(n, Hq, D, 4))
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    q, cu = torch.zeros((n, Hq, D), dtype=torch.bfloat16, device=dev), torch.zeros(2, dtype=torch.int32, device=dev)
+    mod = nv.ScoreMod(softcap=20.0, window=700)
+    busy = torch.randn((4096, 4096), generator=g, device=dev)
+    steps = [(L - 50 * i, torch.randn((n, Hq, D), generator=g, device=dev).bfloat16()) for i in range(12)]
+    cu_new = torch.tensor([0, n], dtype=torch.int32, device=dev)
+
+    def call(out):
+        if n <= 16:
+            nv.nvkv_decode_attn_mod(cache, seqs, q, n, Hq, 1 / 16, mod, 0, ws, out)
+        else:
+            nv.nvkv_prefill_attn_mod(cache, seqs, q, cu, n, n, Hq, 1 / 16, mod, 4 if "split" in kind else 1, ws, out)
+
+    def run(wait):
+        outs = []
+        for length, query in steps:
+            q.fill_(float("nan"))
+            lens.zero_()
+            cu.zero_()
+            out = torch.full_like(q, float("nan"))
+            torch.cuda.synchronize()
+            x = busy @ busy  # keeps the stream busy before the values arrive
+            q.copy_(query + (x[0, 0] * 0).bfloat16())
+            cu.copy_(cu_new)
+            lens.fill_(length)
+            if wait:
+                torch.cuda.synchronize()
+            call(out)
+            outs.append(out)
+            again = torch.empty_like(out)  # the workspace is still being merged
+            call(again)
+            torch.cuda.synchronize()
+            assert torch.equal(again, out)
+        return outs
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
