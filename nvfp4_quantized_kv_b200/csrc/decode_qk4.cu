@@ -81,10 +81,10 @@
 // at a batch of 64), and kernels are instances by cap and bias because the
 // roles share the instruction caches.  Measured (nvkv_decode_attn_mod with
 // its merge): 3 x {330k, 420k, 470k} tokens, cap, 24/4 heads, head_dim 256:
-// 338 us, 0.63 of the measured copy rate; 64 windows of 4,096 tokens: 94 us,
-// 0.47; one sequence of 4,097 tokens, 8/2 heads, head_dim
-// 128: 14.4 us, which is the launch of two kernels, the set-up (about 7,000
-// cycles before the first unit) and one drain.  What bounds it per unit is
+// 335 us, 0.64 of the measured copy rate; 64 windows of 4,096 tokens: 91.6 us,
+// 0.49; one sequence of 4,097 tokens, 8/2 heads, head_dim 128: 12.8 us, which
+// is two kernels' launches (each partly behind the kernel before), the set-up
+// (about 7,000 cycles before the first unit) and one drain.  What bounds it per unit is
 // the plain kernel's hand-off from the V^T writers to the value MMAs (about
 // 2,000 cycles a unit); a segment's end costs some 7,000 cycles more, which
 // many short windows feel.

@@ -51,9 +51,9 @@
 // barriers, 2,800 to the first page block and Q, 4,000 for K and its scores,
 // 2,400 for the first softmax, 3,600 for the output, 2,900 from its end to
 // the next CTA's start on the SM. Packed documents of 1,500 tokens (8,192 +
-// 2,048): 82.7 us = 492 TFLOP/s; windows of 1,024 in chunks of 512, 301, 777
-// and 65 tokens: 79 us, 2.16 waves of such CTAs. A verify step of 24 rows
-// over 2 x 32,768 tokens, 18 CTAs a pair: 47 us; its K and V^T warps are busy
+// 2,048): 82.3 us = 494 TFLOP/s; windows of 1,024 in chunks of 512, 301, 777
+// and 65 tokens: 77.6 us, 2.16 waves of such CTAs. A verify step of 24 rows
+// over 2 x 32,768 tokens, 18 CTAs a pair: 45 us; its K and V^T warps are busy
 // 2,000 of the 2,130 cycles a tile. (Reading a tile's bytes while the tile
 // before is converted gained nothing there and cost the long prefill 11 %.)
 #include <type_traits>
