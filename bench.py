@@ -70,9 +70,9 @@ DECODE_CAPTURE = {
                 "nvfp4_quantized_kv_b200/csrc/sm100.cuh",
                 "nvfp4_quantized_kv_b200/csrc/nvkv_common.cuh",
                 "include/nvkv.h"],
-    "sha256": "4ede9dc008e72d56fde350202eac42f1e622186f46c10154edcf29db2815aae2",
-    "dram_bytes_read": 207596288,
-    "dram_bytes_write": 3389440,
+    "sha256": "aa1322261fcec58cfdba31efd17c38f0f08d60fcc42b763bd73746fd5d9ef0db",
+    "dram_bytes_read": 207592704,
+    "dram_bytes_write": 3468032,
     "kv_bytes": 207363456,
 }
 

@@ -144,6 +144,8 @@ combine_mod_kernel(const int32_t *__restrict__ kv_lens, int B, int Hkv, int T, i
     c1 = range_of_unit_mod(pair_start + units - 1, U, Se);
   }
   sm100::grid_dependency_wait();
+  ws_o = sm100::after_wait(ws_o);
+  ws_lse = sm100::after_wait(ws_lse);
   sm100::launch_dependents();  // (not before: the attention's SMs are free now)
 
   const float *lse = ws_lse + (size_t)bh * R + r;

@@ -509,6 +509,9 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // turn may be set up while this kernel runs, but not earlier: it reads the
     // lengths ahead of its own wait.
     grid_dependency_wait();
+    kv_lens = after_wait(kv_lens);
+    page_table = after_wait(page_table);
+    q = after_wait(q);
     launch_dependents();
     if (warp == kPvWarp)
       list_segments(mod, kv_lens, B, Hkv, T, c, S, max_kv_len, max_pages, seg_head, segs);

@@ -933,6 +933,8 @@ prefill_mod_merge_kernel(const float *__restrict__ ws_o, const float *__restrict
   const size_t row = (size_t)q0 * Hq + (live ? idx : 0);
   const size_t plane = (size_t)total_q * Hq;
   grid_dependency_wait();
+  ws_o = after_wait(ws_o);
+  ws_lse = after_wait(ws_lse);
   launch_dependents();  // (not before: the attention's SMs are free now)
   const float my_lse = live && lane < num_splits ? ws_lse[lane * plane + row] : -INFINITY;
   const float mx = warp_max(my_lse);

@@ -360,6 +360,13 @@ __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
 __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// Loads through a const __restrict__ pointer may be moved ahead of the wait;
+// those through the pointer that after_wait returns may not.
+template <class T>
+__device__ __forceinline__ T *after_wait(T *p) {
+  asm volatile("" : "+l"(p)::"memory");
+  return p;
+}
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

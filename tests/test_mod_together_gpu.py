@@ -284,3 +284,37 @@ def test_back_to_back_calls_see_what_the_kernel_before_wrote(kind):
 
     for a, b in zip(run(True), run(False)):
         assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+def test_append_and_read_back_to_back():
+    """Rows appended, read and appended over again, call after call without a
+    wait in between, are those of each call."""
+    dev = torch.device("cuda")
+    Hq, Hkv, D, n = 24, 4, 256, 600
+    g = torch.Generator(device=dev).manual_seed(12)
+    cache = nv.Cache.allocate(40, Hkv, D, dev, fill=0)
+    seqs = nv.Seqs(torch.arange(40, dtype=torch.int32, device=dev)[None],
+                   torch.tensor([n], dtype=torch.int32, device=dev), 640)
+    cs = torch.empty((640, 128, 2), device=dev)
+    nv.nvkv_rope_table(cs, 256, 1e6, 1.0)
+    pos = torch.arange(n, dtype=torch.int32, device=dev)[None].expand(2, n).contiguous()
+    cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+    zero = torch.zeros(1, dtype=torch.int32, device=dev)
+    axis = [i & 1 for i in range(128)]
+    rows = [[torch.randn((n, h, D), generator=g, device=dev).bfloat16() for h in (Hkv, Hkv, Hq)] for _ in range(20)]
+
+    def run(wait):
+        outs = [[torch.empty_like(t) for t in r] for r in rows]
+        torch.cuda.synchronize()
+        for (k, v, q), (ko, vo, qo) in zip(rows, outs):
+            nv.nvkv_append_rope_axes(cache, seqs, k, v, cu, n, n, cs, 256, pos, axis, q, qo)
+            if wait:
+                torch.cuda.synchronize()
+            nv.nvkv_read_rows(cache, seqs, zero, cu, n, n, ko, vo)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+
+    for a, b in zip(run(True), run(False)):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
