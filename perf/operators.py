@@ -106,9 +106,8 @@ def draw(rng):
     else:
         batch = _log(rng, 1, 16)
         high = _log(rng, 1, 120000 // batch)
-        low = _log(rng, 1, high)
-        c = {"op": "read", "hkv": hkv, "d": d, "ctx": "%dx%d-%d" % (batch, low, high),
-             "skip": rng.randrange(0, min(100, low))}
+        c = {"op": "read", "hkv": hkv, "d": d, "ctx": "%dx%d-%d" % (batch, _log(rng, 1, high), high),
+             "skip": rng.randrange(0, min(100, high))}
     c.pop("name", None)
     return c
 
