@@ -562,6 +562,12 @@ def nvkv_prefill_attn_mod(cache: Cache, seqs: Seqs, q: torch.Tensor, cu_q: torch
           _arg(out, torch.bfloat16, device, n, "out"))
 
 
+def _axis_bytes(axes) -> bytes:
+    """One byte for each number.  Element by element: bytes() of an object with
+    a buffer (a numpy array, an array.array) would be its memory, not its numbers."""
+    return axes if type(axes) is bytes else bytes(list(axes))
+
+
 def nvkv_append_rope_axes(cache: Cache, seqs: Seqs, k_new: torch.Tensor, v_new: torch.Tensor,
                           cu_new: torch.Tensor, total_new: int, max_new: int,
                           rope_cs: torch.Tensor, rotary_dim: int, positions: torch.Tensor,
@@ -569,7 +575,8 @@ def nvkv_append_rope_axes(cache: Cache, seqs: Seqs, k_new: torch.Tensor, v_new: 
                           q_out: torch.Tensor | None = None, stream=None) -> None:
     """nvkv_append_rope with the positions of every row on several axes:
     positions int32 [num_axes][total_new], axis_of_pair the axis (a whole
-    number) of each of the rotary_dim/2 pairs, as bytes or a sequence.  q
+    number) of each of the rotary_dim/2 pairs, as bytes or any sequence of
+    whole numbers (a list, a numpy array or array.array of any integer type).  q
     (bf16 [total_new][Hq][D]) is rotated into q_out in the same launch."""
     _fmt(cache, "nvfp4", "nvkv_append_rope_axes")
     device = _on(cache, seqs)
@@ -599,7 +606,7 @@ def nvkv_append_rope_axes(cache: Cache, seqs: Seqs, k_new: torch.Tensor, v_new: 
           _arg(cu_new, torch.int32, device, seqs.batch + 1, "cu_new"), total_new, max_new,
           _arg(rope_cs, torch.float32, device, 0, "rope_cs"), cs_shape[0], rotary_dim,
           _arg(positions, torch.int32, device, 0, "positions"), pos_shape[0],
-          bytes(axis_of_pair), qp, hq, qo)
+          _axis_bytes(axis_of_pair), qp, hq, qo)
 
 
 def nvkv_read_rows(cache: Cache, seqs: Seqs, starts: torch.Tensor, cu_rows: torch.Tensor,
