@@ -501,18 +501,18 @@ class ScoreMod:
                                (key_starts, torch.int32, "key_starts")):
             if t is not None:
                 _dev(t, dtype, name)
-        self._c = _ScoreModC()
 
     def _struct(self, device: int, num_q_heads: int, batch: int, starts: int) -> _ScoreModC:
         a, p, k = self.alibi_slopes, self.prefix_lens, self.key_starts
         if not 0 <= self.window < 2 ** 31:
             raise ValueError(f"window is {self.window}, must be 0 .. 2^31 - 1")
-        c = self._c
-        c.softcap, c.window = self.softcap, self.window
-        c.alibi_slopes = None if a is None else _arg(a, torch.float32, device, num_q_heads, "alibi_slopes")
-        c.prefix_lens = None if p is None else _arg(p, torch.int32, device, batch, "prefix_lens")
-        c.key_starts = None if k is None else _arg(k, torch.int32, device, starts, "key_starts")
-        return c
+        # (a struct of its own for each call: the library reads it after the
+        # interpreter's lock is dropped, when another thread may make a call)
+        return _ScoreModC(
+            self.softcap, self.window,
+            None if a is None else _arg(a, torch.float32, device, num_q_heads, "alibi_slopes"),
+            None if p is None else _arg(p, torch.int32, device, batch, "prefix_lens"),
+            None if k is None else _arg(k, torch.int32, device, starts, "key_starts"))
 
 
 def nvkv_decode_mod_kernel_name(cache: Cache, T: int, num_q_heads: int) -> str:

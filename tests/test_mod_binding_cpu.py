@@ -57,3 +57,19 @@ def test_axes_that_are_no_bytes_are_refused(caught, axes):
     with pytest.raises((TypeError, ValueError)):
         append(axes)
     assert not caught
+
+
+def test_a_call_keeps_its_score_mod_while_another_is_made(caught):
+    """The library reads a call's struct after the interpreter's lock is
+    dropped: a call with other attributes of the same ScoreMod, made
+    meanwhile, must not change it."""
+    cache, seqs = host_cache()
+    q, ws = torch.zeros(1, 2, 128, dtype=bf16), torch.zeros(16, dtype=torch.uint8)
+    mod = nv.ScoreMod(softcap=30.0, window=64)
+    nv.nvkv_decode_attn_mod(cache, seqs, q, 1, 2, 0.1, mod, 1, ws, q)
+    starts = torch.zeros(1, dtype=torch.int32)
+    mod.softcap, mod.window, mod.key_starts = 7.0, 5, starts
+    nv.nvkv_prefill_attn_mod(cache, seqs, q, torch.tensor([0, 1], dtype=torch.int32), 1, 1, 2, 0.1, mod, 1, None, q)
+    first, second = caught[0][6]._obj, caught[1][8]._obj
+    assert (first.softcap, first.window, first.key_starts) == (30.0, 64, None)
+    assert (second.softcap, second.window, second.key_starts) == (7.0, 5, starts.data_ptr())
