@@ -432,9 +432,10 @@ typedef struct nvkv_score_mod {
  * nvkv_decode_mod_kernel_name names the kernel ("none" on invalid arguments):
  *   "decode_qk4"  (T*Hq/Hkv <= 6, head_dim 128 and 256): the arithmetic of
  *                 nvkv_decode_attn's decode_qk4.
- *   "prefill_mod" (more rows): the kernel of nvkv_prefill_attn_mod, the keys
- *                 of each (sequence, kv-head) split over as many CTAs as the
- *                 workspace has room for; q * sm_scale * log2(e) enters as one
+ *   "prefill_mod" (more rows, or a pool of more than 2^31/36 pages times
+ *                 kv-heads: 137 GB at head_dim 128): the kernel of
+ *                 nvkv_prefill_attn_mod, the keys of each (sequence, kv-head)
+ *                 split over as many CTAs as the workspace has room for; q * sm_scale * log2(e) enters as one
  *                 f16 (11 significant bits; |q * sm_scale| below about 45000);
  *                 at most 65535 sequences.
  *   "decode_simt" (NVKV_DECODE_KERNEL=simt).

@@ -1441,10 +1441,14 @@ cudaError_t launch_fmt(const nvkv_cache &c, const nvkv_seqs &s, const void *q, i
 
 // True when this kernel takes the shape: head_dim 256 and at most 6 query
 // rows (T * Hq/Hkv) per (sequence, kv-head), for both cache formats; with a
-// ScoreMod over an NVFP4 cache also head_dim 128.
+// ScoreMod over an NVFP4 cache also head_dim 128.  Not a pool whose rows
+// pass the 32-bit coordinates of its maps: a row is 64 bytes at head_dim 128,
+// so that is one of 137 GB (the other kernels count rows of 128 bytes, or
+// bytes in 64 bits).
 bool decode_qk4_supported(const nvkv_cache &c, int T, int Hq, bool mod) {
   const int R = T * (Hq / c.num_kv_heads);
   if (R < 1 || encode_fn() == nullptr) return false;
+  if ((int64_t)c.num_pages * c.num_kv_heads > INT32_MAX / kRowsPerHead) return false;
   return R <= kRowsCap && (c.head_dim == 256 || (mod && c.head_dim == 128));
 }
 
