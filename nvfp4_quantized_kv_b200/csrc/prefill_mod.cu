@@ -111,14 +111,15 @@ struct Cfg {
   static constexpr int kOffPages = kOffL + 2 * 128 * 4;             // int[stages][4]
   static constexpr int kOffPres = kOffPages + kStages * kTilePages * 4;  // u32[4]
   static constexpr int kOffFlags = kOffPres + 16;
-  static constexpr int kOffBars = kOffFlags + 16;
+  static constexpr int kOffSeen = kOffFlags + 16;                   // u64[stages]
+  static constexpr int kOffBars = kOffSeen + kStages * 8;
   // full, empty; kready, vready, sready, pready, pvdone; qready, final, lready, final_qk
   static constexpr int kNumBars = 2 * kStages + 2 * 5 + 4;
   static constexpr int kOffTmem = kOffBars + kNumBars * 8;
   static constexpr int kSmemBytes = kOffTmem + 16 + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(128 * (4 * D + 16) <= kOffVsc, "the output rows fit below the tables");
-  static_assert(kOffK % 1024 == 0 && kOffPages % 16 == 0 && kOffBars % 8 == 0, "alignment");
+  static_assert(kOffK % 1024 == 0 && kOffPages % 16 == 0 && kOffSeen % 8 == 0 && kOffBars % 8 == 0, "alignment");
 };
 
 // Keeps what follows out of the way of the instructions that always run.
@@ -209,6 +210,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   // which wait for the value MMAs of tile j.
   volatile uint32_t *present = reinterpret_cast<volatile uint32_t *>(smem + C::kOffPres);
   volatile int *flags = reinterpret_cast<volatile int *>(smem + C::kOffFlags);
+  uint64_t *seen_s = reinterpret_cast<uint64_t *>(smem + C::kOffSeen);  // with gaps: keys seen
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBars);
   uint64_t *full = bars, *empty = bars + kStages;
   uint64_t *kready = bars + 2 * kStages, *vready = kready + 2, *sready = kready + 4,
@@ -272,17 +274,32 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     }
   }
 
-  // The keys [key_lo, key_hi) that any row of the tile sees: every warp scans
-  // the tile's tokens.
+  // The keys from key_lo to key_hi - 1 hold all that any row of the tile sees:
+  // every warp scans the tile's tokens. Rows with starts of their own may
+  // leave keys unseen in between (padding between documents sees nothing):
+  // there are none when each row's interval touches the next one's. (Without
+  // starts, and in a decode step, it does: all that see a key see their own
+  // position, or the step's first key.)
   int key_lo = 0x7fffffff, key_hi = 0;
+  bool gaps = false;
+  const int i_first = kTileRows * mt / G;
+  const int i_last = min(n_b - 1, (kTileRows * mt + kTileRows - 1) / G);
+  auto range_of = [&](int i, int &lo, int &hi) {
+    key_range(kv_len - n_b + i, kv_len, start_of(i), mod.window, prefix, lo, hi);
+  };
   if (!bad) {
-    const int i_last = min(n_b - 1, (kTileRows * mt + kTileRows - 1) / G);
-    for (int i = (kTileRows * mt) / G + lane; i <= i_last; i += 32) {
+    for (int i = i_first + lane; i <= i_last; i += 32) {
       int lo, hi;
-      key_range(kv_len - n_b + i, kv_len, start_of(i), mod.window, prefix, lo, hi);
+      range_of(i, lo, hi);
       if (lo < hi) key_lo = min(key_lo, lo), key_hi = max(key_hi, hi);
+      if (mod.starts && a.T == 0 && i < i_last) {
+        int lo2, hi2;
+        range_of(i + 1, lo2, hi2);
+        gaps |= lo >= hi || lo2 >= hi2 || lo > hi2 || lo2 > hi;
+      }
     }
   }
+  gaps = __any_sync(0xffffffffu, gaps);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     key_lo = min(key_lo, __shfl_xor_sync(0xffffffffu, key_lo, o));
@@ -299,12 +316,28 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     return (tile_lo + (Mod::kBias ? ntiles_all - 1 - (j0 + j) : j0 + j)) * kTileTokens;
   };
 
-  // (the TMA warp) pages of the tiles: lane p's of every four
+  // (the TMA warp) which of tile j's 64 keys some row sees, where there may be
+  // gaps; a row of the tile at a time in every lane
+  auto seen_keys = [&](int j) -> uint64_t {
+    if (!gaps) return ~uint64_t(0);
+    const int tok = tile_key(j);
+    uint64_t seen = 0;
+    for (int i = i_first + lane; i <= i_last; i += 32) {
+      int lo, hi;
+      range_of(i, lo, hi);
+      lo = max(lo - tok, 0), hi = min(hi - tok, kTileTokens);
+      if (lo < hi) seen |= (~uint64_t(0) << lo) & (~uint64_t(0) >> (kTileTokens - hi));
+    }
+    return (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(seen >> 32)) << 32 |
+           __reduce_or_sync(0xffffffffu, (uint32_t)seen);
+  };
+  // pages of the tiles: lane p's of every four
   const int32_t *pt = a.page_table + (size_t)b * a.max_pages;
   const int p = lane & 3;
-  auto page_for = [&](int j) -> int {
+  auto page_for = [&](int j, uint64_t seen) -> int {
     const int tok = tile_key(j) + p * kPageTokens;
     if (tok >= key_hi || tok + kPageTokens <= key_lo) return -1;  // nobody sees it
+    if (((seen >> (kPageTokens * p)) & 0xffffu) == 0) return -1;
     const int pg = pt[tok / kPageTokens];
     if (pg < 0 || pg >= a.num_pages) {
       if (lane < kTilePages) report(a.err, NVKV_DEVERR_PAGE_ID);
@@ -313,9 +346,10 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     return pg;
   };
   int first_page = -1;
+  uint64_t first_seen = 0;
   if (warp == kProducerWarp) {
     prefetch_tmap(&tmap);
-    if (ntiles > 0) first_page = page_for(0);
+    if (ntiles > 0) first_page = page_for(0, first_seen = seen_keys(0));
   }
   tc_fence_before();
   __syncthreads();
@@ -355,15 +389,18 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     if (warp == kProducerWarp) {
       // ---------------------------------------------------------------- TMA
       int cur = first_page;
+      uint64_t cur_seen = first_seen;
       for (int j = 0; j < ntiles; ++j) {
         const int stage = j % kStages;
-        const int nxt = j + 1 < ntiles ? page_for(j + 1) : -1;
+        const uint64_t nxt_seen = j + 1 < ntiles ? seen_keys(j + 1) : 0;
+        const int nxt = j + 1 < ntiles ? page_for(j + 1, nxt_seen) : -1;
         if (j >= kStages) {
           if (lane == 0) wait_bar(&empty[stage], ((j / kStages) + 1) & 1, flags, a.err);
           __syncwarp();
         }
         const bool mine = lane < kTilePages && cur >= 0;
         if (lane < kTilePages) spages[stage * kTilePages + lane] = cur;
+        if (lane == 0) seen_s[stage] = cur_seen;
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * C::kHeadBytes;
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], bytes);
@@ -371,7 +408,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         if (mine)
           tma_load_2d(stages + stage * kStageBytes + lane * kPagePitch, &tmap, 0,
                       (cur * a.Hkv + h) * C::kRowsPerHead, &full[stage]);
-        cur = nxt;
+        cur = nxt, cur_seen = nxt_seen;
       }
       // Drain: every issued copy must land before the CTA may exit.
       if (lane == 0) {
@@ -519,6 +556,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
         const uint8_t *stg = stages + stage * kStageBytes;
         wait_bar(&full[stage], (j / kStages) & 1, flags, a.err);
         const int4 pg4 = *reinterpret_cast<const int4 *>(spages + stage * kTilePages);
+        const uint64_t seen = seen_s[stage];
         const int tok0 = tile_key(j);
         if (t < D) {
           // This tile's V scales, converted once (the 16 V^T rows of a group
@@ -565,13 +603,15 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
             e2m1x8_to_f16x2x4(cw[pp].y, c1);
 #pragma unroll
             for (int e = 0; e < 8; ++e) o8[e] = hmul2_u32(e < 4 ? c0[e] : c1[e - 4], sp[e]);
-            if (rare(ptok < key_lo || ptok + kPageTokens > key_hi)) {
+            if (rare(gaps || ptok < key_lo || ptok + kPageTokens > key_hi)) {
               // tokens that no row sees are zero, whatever their bytes
+              const uint32_t some = (uint32_t)(seen >> (kPageTokens * p));
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int t0 = ptok + 2 * e;
-                if (t0 < key_lo || t0 >= key_hi) o8[e] &= 0xffff0000u;
-                if (t0 + 1 < key_lo || t0 + 1 >= key_hi) o8[e] &= 0xffffu;
+                if (t0 < key_lo || t0 >= key_hi || !((some >> (2 * e)) & 1u)) o8[e] &= 0xffff0000u;
+                if (t0 + 1 < key_lo || t0 + 1 >= key_hi || !((some >> (2 * e + 1)) & 1u))
+                  o8[e] &= 0xffffu;
               }
             }
           } else {
