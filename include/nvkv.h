@@ -433,11 +433,10 @@ typedef struct nvkv_score_mod {
  *   "decode_qk4"  (T*Hq/Hkv <= 6, head_dim 128 and 256): the arithmetic of
  *                 nvkv_decode_attn's decode_qk4.
  *   "prefill_mod" (more rows, or a pool of more than 2^31/36 pages times
- *                 kv-heads: 137 GB at head_dim 128): the kernel of
- *                 nvkv_prefill_attn_mod, the keys of each (sequence, kv-head)
- *                 split over as many CTAs as the workspace has room for; q * sm_scale * log2(e) enters as one
- *                 f16 (11 significant bits; |q * sm_scale| below about 45000);
- *                 at most 65535 sequences.
+ *                 kv-heads: 137 GB at head_dim 128): the kernel and the
+ *                 arithmetic of nvkv_prefill_attn_mod, the keys of each
+ *                 (sequence, kv-head) split over as many CTAs as the workspace
+ *                 has room for; at most 65535 sequences.
  *   "decode_simt" (NVKV_DECODE_KERNEL=simt).
  *
  * nvkv_decode_attn_mod_k8v4: the same over a K8V4 cache, on the kernels of
@@ -454,13 +453,16 @@ nvkv_status nvkv_decode_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs *
                                       size_t workspace_bytes, void *out, nvkv_stream_t stream);
 
 /* nvkv_prefill_attn_split (same arguments, layouts, workspace and checks),
- * with the scores of `mod`, on the tensor cores for both head_dims: q *
- * sm_scale * log2(e) as f16, products with the exact K in fp32, the scores'
- * modifications and the softmax in fp32, weights rounded to f16 for the value
- * sum, which accumulates in fp32.
+ * with the scores of `mod`, on the tensor cores for both head_dims: q as f16
+ * after a power of two per row that puts the row's largest element into
+ * [2^14, 2^15) (exact, at any size of q, but for elements below 2^-31 of that
+ * largest one, which keep an absolute precision of 2^-39 of it), products with
+ * the exact K in fp32, times sm_scale * log2(e) and the power of two in fp32,
+ * the scores' modifications and the softmax in fp32, weights rounded to f16 for
+ * the value sum, which accumulates in fp32.
  * num_splits = 0 takes the automatic count that the workspace has room for
  * (1 for a NULL one; nvkv_prefill_workspace_bytes(..., 0) is enough for any).
- * |q * sm_scale| below about 45000 (f16), at most 65535 sequences.
+ * At most 65535 sequences.
  * A prefix is seen in both directions as far as it is cached: put it into one
  * chunk.
  *

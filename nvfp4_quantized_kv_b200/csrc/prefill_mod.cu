@@ -10,10 +10,20 @@
 // streams the 64-token key tiles that any of its rows sees; with a distance
 // bias from the newest to the oldest, so that the largest scores come first
 // and the running maximum is found in the first tile instead of being raised
-// in every one. Q (128 x D, f16, scaled to base-2 scores) sits in Tensor Memory as the
-// A operand of S = Q K^T (N = 64), S is double-buffered there, P (f16)
-// overwrites its own S slot as the A operand of O += P V (N = D), O stays in
-// Tensor Memory.
+// in every one. Q (128 x D, f16) sits in Tensor Memory as the A operand of
+// S = Q K^T (N = 64), S is double-buffered there, P (f16) overwrites its own S
+// slot as the A operand of O += P V (N = D), O stays in Tensor Memory.
+//
+// A row of Q is its bf16 values times the power of two that puts the largest
+// into [2^14, 2^15): 8 significant bits, so nothing is rounded but elements
+// below 2^-31 of that largest one (f16 subnormals; by at most 2^-39 of it), and
+// no size of q overflows. sm_scale * log2(e) and the power of two come back as
+// one fp32 factor of the row's scores. (sm_scale in Q itself took 11 bits of
+// the product, fewer than the plain verify step's two f16 terms, and ended at
+// |q * sm_scale| = 45,000.) The factor's 16 packed products a tile and thread
+// and the rows' maxima cost 1 to 2 % (long chunk 3.82 -> 3.86 ms, documents
+// 84.2 -> 86.1 us); pairs of scores, not single ones, have the running maximum
+// subtracted to make up for half of it.
 //
 // Roles, and what set the pace before each of them (clock64 traces, cycles a
 // tile at head_dim 256 with a cap):
@@ -356,26 +366,41 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  float qfac = 1.f;  // a softmax thread's row: what its products become scores by
   if (warp >= kKWarps && warp < kProducerWarp) {
-    // Q row -> Tensor Memory (A operand), f16, scaled to base-2 scores: lane
-    // quarter warp % 4, a quarter of the columns each.
+    // Q row -> Tensor Memory (A operand), f16: lane quarter warp % 4, a quarter
+    // of the columns each.
     const int lq = warp & 3, part = (warp - kKWarps) >> 2;
     const int rr = 32 * (lq % kQuarters) + lane;
     asm volatile("cp.async.wait_all;" ::: "memory");
     named_barrier(10, 16 * 32);  // every warp's rows are there
+    uint32_t qw[D / 8], top2 = 0;
+#pragma unroll
+    for (int v = 0; v < D / 32; ++v) {
+      const uint4 r4 = *reinterpret_cast<const uint4 *>(q_chunk(rr, part * (D / 32) + v));
+      qw[4 * v] = r4.x, qw[4 * v + 1] = r4.y, qw[4 * v + 2] = r4.z, qw[4 * v + 3] = r4.w;
+    }
+#pragma unroll
+    for (int v = 0; v < D / 8; ++v) top2 = __vmaxu2(top2, qw[v] & 0x7fff7fffu);
+    // the row's largest exponent, from the four quarters' maxima (where the
+    // softmax keeps its maxima and denominators later)
+    static_assert(C::kOffL == C::kOffRed + 2 * 128 * 4, "one table");
+    uint32_t *top_s = reinterpret_cast<uint32_t *>(red_s) + 32 * lq + lane;  // [part][row]
+    top_s[128 * part] = max(top2 >> 16, top2 & 0xffffu);
+    named_barrier(10, 16 * 32);
+    // (below 2^-100 a row's scores are below 2^-80 whatever the keys)
+    const uint32_t eb = max(27u, max(max(top_s[0], top_s[128]), max(top_s[256], top_s[384])) >> 7);
+    const float up = __uint_as_float((268u - eb) << 23);  // 2^(14 - e), e = eb - 127
+    qfac = a.qscale * __uint_as_float((eb - 14u) << 23);  // 2^(e - 14)
 #pragma unroll
     for (int c16 = 0; c16 < D / 128; ++c16) {
       uint32_t w[16];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const uint4 r4 = *reinterpret_cast<const uint4 *>(q_chunk(rr, part * (D / 32) + 4 * c16 + v));
-        const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __half2 hh = __floats2half2_rn(__uint_as_float(rw[e] << 16) * a.qscale,
-                                               __uint_as_float(rw[e] & 0xffff0000u) * a.qscale);
-          w[4 * v + e] = *reinterpret_cast<const uint32_t *>(&hh);
-        }
+      for (int v = 0; v < 16; ++v) {
+        const uint32_t rw = qw[16 * c16 + v];
+        const __half2 hh = __floats2half2_rn(__uint_as_float(rw << 16) * up,
+                                             __uint_as_float(rw & 0xffff0000u) * up);
+        w[v] = *reinterpret_cast<const uint32_t *>(&hh);
       }
       tmem_st16(tmem + ((uint32_t)(32 * lq) << 16) + kColQ + part * (D / 8) + c16 * 16, w);
     }
@@ -667,6 +692,11 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
             tmem_ld16(scol + koff + e, reinterpret_cast<uint32_t(&)[16]>(xr[e]));
         }
         tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < kKeys; e += 2) {
+          const float2 v = mul_f32x2(make_float2(x[e], x[e + 1]), make_float2(qfac, qfac));
+          x[e] = v.x, x[e + 1] = v.y;
+        }
       };
       auto top_score = [&]() {
         float t0 = max3(x[0], x[1], x[2]), t1 = max3(x[3], x[4], x[5]);
@@ -775,9 +805,10 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       float2 lv0 = make_float2(0.f, 0.f), lv1 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < kKeys / 2; ++e) {
+        const float2 d = add_f32x2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(-ms, -ms));
         float2 w;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.x) : "f"(x[2 * e] - ms));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.y) : "f"(x[2 * e + 1] - ms));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.x) : "f"(d.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.y) : "f"(d.y));
         asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(pw[e]) : "f"(w.x), "f"(w.y));
         (e & 1 ? lv1 : lv0) = add_f32x2(e & 1 ? lv1 : lv0, w);
       }
