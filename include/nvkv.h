@@ -405,7 +405,9 @@ nvkv_status nvkv_pages_restore_k8v4(const nvkv_cache *cache, const int32_t *page
  * looked at: their pages may be absent from the page table (-1, freed, or
  * reused by another sequence) as long as no query of the call sees a key of
  * the page, and no bad page id is reported for them.  The keys of a bad page
- * that a query does see are left out (and reported).
+ * that a query does see are left out (and reported).  A query row with an
+ * element that is not finite gives a row of NaN where it sees a key, in every
+ * kernel and at every split count, and changes no other row.
  *   softcap:      > 0 and finite (at least 1e-38), or 0 for none.
  *   window:       > 0: that many keys up to the query's own; 0: none.
  *   alibi_slopes: device float [Hq], or NULL.

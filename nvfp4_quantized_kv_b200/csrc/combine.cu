@@ -150,13 +150,19 @@ combine_mod_kernel(const int32_t *__restrict__ kv_lens, int B, int Hkv, int T, i
 
   const float *lse = ws_lse + (size_t)bh * R + r;
   float mx = -INFINITY;
-  for (int64_t c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, lse[(size_t)c * R]);
+  bool odd = false;  // a NaN among them: the row's query is not finite
+  for (int64_t c = c0 + lane; c <= c1; c += 32) {
+    const float v = lse[(size_t)c * R];
+    mx = fmaxf(mx, v);
+    odd |= isnan(v);
+  }
   mx = warp_max(mx);
+  odd = __any_sync(0xffffffffu, odd);
   const int dpl = D / 32;  // channels of a lane: 4 or 8
   float acc[8], wsum = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  if (mx > -INFINITY) {
+  if (mx > -INFINITY || odd) {
     // 32 of this warp's ranges at a time, their weights one a lane
     for (int64_t cb = c0 + sub; cb <= c1; cb += 32 * kW) {
       const int64_t mine = cb + (int64_t)lane * kW;

@@ -377,6 +377,15 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// max(a, b), NaN if either is and kNan, else the number of the two.
+template <bool kNan>
+__device__ __forceinline__ float largest(float a, float b) {
+  if constexpr (!kNan) return fmaxf(a, b);
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // The D/16 scale bytes of a row (the words past them zero).
 template <int D>
 __device__ __forceinline__ uint4 scale_bytes(const uint8_t *p) {
@@ -832,12 +841,15 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
           for (int i = 0; i < kE; ++i) y[i] = 0.f;
         }
-        float a = 0.f;
-#pragma unroll
-        for (int i = 0; i < kE; ++i) a = fmaxf(a, fabsf(y[i]));
-        a = warp_max(a);
         // A row whose largest element is below the smallest normal float
         // (2^-126) is taken as zero: its scores would be below 2^-110.
+        // (Masked: a NaN element makes it NaN, so 255 is a row that is not finite.)
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < kE; ++i) a = largest<Mod::kOn>(a, fabsf(y[i]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          a = largest<Mod::kOn>(a, __shfl_xor_sync(0xffffffffu, a, o));
         const int eb = (int)((__float_as_uint(a) >> 23) & 0xffu);  // biased exponent
         // a in [2^(eb-127), 2^(eb-126)): a * 2^k in [256, 512) (NVFP4), in
         // [128, 256) (K8V4, under the E4M3 maximum 448)
@@ -917,7 +929,13 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           }
         }
         }
-        if (lane == 0) sh.fac[r] = eb > 0 ? scale_pow2(1.f, -k) : 0.f;
+        if (lane == 0) {
+          float f = eb > 0 ? scale_pow2(1.f, -k) : 0.f;
+          if constexpr (Mod::kOn) {
+            if (eb == 255) f = NAN;  // a row that is not finite has scores of NaN
+          }
+          sh.fac[r] = f;
+        }
       }
       fence_proxy_async_smem();
       named_barrier(2, kDeqWarps * 32);
@@ -1312,6 +1330,8 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           for (int w = 0; w < 4; ++w) lv[n] += sh.red[w * kNP + n];
         }
         // The sums carry the 2^-14 of V^T: o = O * 2^14 / l, lse = m + log2(l).
+        // (Masked: only a sum of 0 is a row that saw nothing; NaN stays NaN.)
+        auto none = [](float l) { return Mod::kOn ? l == 0.f : !(l > 0.f); };
 #pragma unroll
         for (int half = 0; half < kHalves; ++half) {
           uint32_t o8[8];
@@ -1322,7 +1342,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           for (int n = 0; n < RM; ++n) {
             if (n < R) {
               const float v = __uint_as_float(o8[n]);
-              ws_o[(slot * R + n) * D + d] = lv[n] > 0.f ? v * 16384.f / lv[n] : 0.f;
+              ws_o[(slot * R + n) * D + d] = none(lv[n]) ? 0.f : v * 16384.f / lv[n];
             }
           }
         }
@@ -1330,7 +1350,7 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
           float l = 0.f;
 #pragma unroll
           for (int n = 0; n < RM; ++n) l = n == stid ? lv[n] : l;
-          ws_lse[slot * R + stid] = l > 0.f ? sh.m_s[stid] + log2f(l) : -INFINITY;
+          ws_lse[slot * R + stid] = none(l) ? -INFINITY : sh.m_s[stid] + log2f(l);
         }
         tc_fence_before();
         named_barrier(1, kSmxWarps * 32);  // the sums and maxima have been read

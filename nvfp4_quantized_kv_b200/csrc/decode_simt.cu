@@ -88,7 +88,8 @@ __device__ __forceinline__ float k_half_score(K8v4Layout, const uint8_t *blk, in
 // max m, the sum l of 2^(s - m) and, per lane, the unnormalised value sums of
 // channels [lane*D/32, (lane+1)*D/32).  With a ScoreMod the scores are capped
 // and biased by slope2 * |pos - key|; keys outside the interval are left out
-// whatever their bytes hold (weight and scale are replaced, not multiplied).
+// whatever their bytes hold (weight and scale are replaced, not multiplied),
+// and a row that is not finite gives NaN (l and acc) once it sees a key.
 template <class L, class Mod>
 __device__ __forceinline__ void attend_rows_simt(const uint8_t *__restrict__ pool, int num_pages,
                                                  int Hkv, int D, int h,
@@ -102,6 +103,11 @@ __device__ __forceinline__ void attend_rows_simt(const uint8_t *__restrict__ poo
   l = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  [[maybe_unused]] bool odd = false;
+  if constexpr (Mod::kOn) {
+    for (int d = lane; d < D; d += 32) odd |= !isfinite(qr[d]);
+    odd = __any_sync(0xffffffffu, odd);
+  }
   // pages from the one that holds jb; none for an empty interval
   const int jp = !Mod::kOn ? jb : jb < je ? jb / kPageTokens * kPageTokens : je;
   for (int p0 = jp; p0 < je; p0 += kPageTokens) {
@@ -119,6 +125,7 @@ __device__ __forceinline__ void attend_rows_simt(const uint8_t *__restrict__ poo
     if constexpr (Mod::kOn) {
       if (mod.cap2 > 0.f) s = mod.cap(make_float2(s, 0.f)).x;
       s = fmaf(-slope2, fabsf((float)(pos - (p0 + slot))), s);
+      if (odd) s = NAN;
     }
     const float s_eff = valid ? s : -INFINITY;
     const float m_new = fmaxf(m, warp_max(s_eff));
@@ -226,7 +233,8 @@ decode_simt_kernel(const uint8_t *__restrict__ pool, int num_pages, int Hkv, int
       float *o = ws_o + (slot * R + r) * (size_t)D;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       for (int i = 0; i < dpl; ++i) o[lane * dpl + i] = acc[i] * inv;
-      if (lane == 0) ws_lse[slot * R + r] = l > 0.f ? m + log2f(l) : -INFINITY;
+      const bool none = Mod::kOn ? l == 0.f : !(l > 0.f);  // (masked: NaN stays NaN)
+      if (lane == 0) ws_lse[slot * R + r] = none ? -INFINITY : m + log2f(l);
     }
     u = seg_end;
   }

@@ -390,7 +390,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     named_barrier(10, 16 * 32);
     // (below 2^-100 a row's scores are below 2^-80 whatever the keys)
     const uint32_t eb = max(27u, max(max(top_s[0], top_s[128]), max(top_s[256], top_s[384])) >> 7);
-    const float up = __uint_as_float((268u - eb) << 23);  // 2^(14 - e), e = eb - 127
+    // 2^(14 - e), e = eb - 127; a row that is not finite is NaN throughout
+    const float up = __uint_as_float(eb < 255u ? (268u - eb) << 23 : 0x7fc00000u);
     qfac = a.qscale * __uint_as_float((eb - 14u) << 23);  // 2^(e - 14)
 #pragma unroll
     for (int c16 = 0; c16 < D / 128; ++c16) {
@@ -840,7 +841,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       const float both = l_s[r] + l_s[128 + r];
       if (gr < rows && rows_ok)
         a.ws_lse[(size_t)split * a.total_q * a.Hq + (size_t)(q0 + i) * a.Hq + h * G + g] =
-            both > 0.f ? m + log2f(both) : -INFINITY;
+            both == 0.f ? -INFINITY : m + log2f(both);  // (NaN stays NaN)
     }
   }
 
@@ -881,7 +882,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       inv = sum > 0.f ? exp2f(red_s[r] - top) / sum : 0.f;
       const int gr = kTileRows * mt + 32 * lq + lane;
       if (a.ws_o && lq < kQuarters && part == 0 && gr < rows && rows_ok)
-        a.ws_lse[plane + out_row(gr)] = sum > 0.f ? top + log2f(sum) : -INFINITY;
+        a.ws_lse[plane + out_row(gr)] = sum == 0.f ? -INFINITY : top + log2f(sum);
     }
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16) + kColO + part * (D / 4);
     // The rows go through shared memory (nothing else uses it any more), 16
@@ -977,7 +978,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
 // sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M) with M the largest lse (zero
 // when no split saw a key). kW warps a row (a decode step's few rows have up
 // to 32 splits), D/32 elements a lane; the warps' sums are added in order.
-// Rows outside every sequence's chunk are left alone. Set up while the
+// A split whose lse is NaN makes the row NaN. Rows outside every sequence's
+// chunk are left alone. Set up while the
 // attention kernel runs (programmatic dependent launch).
 constexpr int kMaxSplits = 8;        // of a chunk
 constexpr int kMaxStepSplits = 32;   // of a decode step
@@ -1008,8 +1010,8 @@ prefill_mod_merge_kernel(const float *__restrict__ ws_o, const float *__restrict
   ws_lse = after_wait(ws_lse);
   launch_dependents();  // (not before: the attention's SMs are free now)
   const float my_lse = live && lane < num_splits ? ws_lse[lane * plane + row] : -INFINITY;
-  const float mx = warp_max(my_lse);
-  const float my_w = my_lse > -INFINITY ? exp2f(my_lse - mx) : 0.f;
+  const float mx = warp_max(my_lse);  // (of the numbers among them)
+  const float my_w = my_lse == -INFINITY ? 0.f : exp2f(my_lse - mx);
   float acc[kE], wsum = 0.f;
 #pragma unroll
   for (int e = 0; e < kE; ++e) acc[e] = 0.f;
