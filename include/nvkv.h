@@ -400,7 +400,9 @@ nvkv_status nvkv_pages_restore_k8v4(const nvkv_cache *cache, const int32_t *page
  *                                           prefix_lens[b] (p < P),
  *     hi = P, at most p + window            queries of the prefix see all of
  *                                           it, in both directions
- * and hi <= kv_len always.  The interval may be empty (a document that starts
+ * and hi <= kv_len always.  (A prefix reaches past a document's end, but not
+ * before its start: of several documents inside one prefix, each sees the
+ * later ones.)  The interval may be empty (a document that starts
  * after p): the row's output is then 0.  Keys outside the interval are not
  * looked at: their pages may be absent from the page table (-1, freed, or
  * reused by another sequence) as long as no query of the call sees a key of
@@ -461,7 +463,8 @@ nvkv_status nvkv_decode_attn_mod_k8v4(const nvkv_cache *cache, const nvkv_seqs *
  * largest one, which keep an absolute precision of 2^-39 of it), products with
  * the exact K in fp32, times sm_scale * log2(e) and the power of two in fp32,
  * the scores' modifications and the softmax in fp32, weights rounded to f16 for
- * the value sum, which accumulates in fp32.
+ * the value sum, which accumulates in fp32 on the tensor cores: a key of less
+ * than about 2^-24 of what its split has summed adds nothing.
  * num_splits = 0 takes the automatic count that the workspace has room for
  * (1 for a NULL one; nvkv_prefill_workspace_bytes(..., 0) is enough for any).
  * At most 65535 sequences.

@@ -81,13 +81,14 @@
 // at a batch of 64), and kernels are instances by cap and bias because the
 // roles share the instruction caches.  Measured (nvkv_decode_attn_mod with
 // its merge): 3 x {330k, 420k, 470k} tokens, cap, 24/4 heads, head_dim 256:
-// 335 us, 0.64 of the measured copy rate; 64 windows of 4,096 tokens: 91.6 us,
-// 0.49; one sequence of 4,097 tokens, 8/2 heads, head_dim 128: 12.8 us, which
-// is two kernels' launches (each partly behind the kernel before), the set-up
-// (about 7,000 cycles before the first unit) and one drain.  What bounds it per unit is
-// the plain kernel's hand-off from the V^T writers to the value MMAs (about
-// 2,000 cycles a unit); a segment's end costs some 7,000 cycles more, which
-// many short windows feel.
+// 337 us, 0.64 of the measured copy rate (358 us, 0.60, under steady load); 64
+// windows of 4,096 tokens: 92 us, 0.48; one sequence of 4,097 tokens, 8/2
+// heads, head_dim 128: 12.6 us, which is two kernels' launches (each partly
+// behind the kernel before), the set-up (about 7,000 cycles before the first
+// unit) and one drain.  A unit takes about 2,555 cycles, of which the plain
+// kernel's hand-off from the V^T writers to the value MMAs accounts for 2,000
+// (its bytes for 1,633; the other 550 are not traced); a segment's end costs
+// some 7,000 cycles more, which many short windows feel.
 #include <cfloat>
 
 #include "score_mod.cuh"
@@ -641,8 +642,8 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // Two issuing warps: issuing a batch of tcgen05.mma blocks the thread
     // until the batch has nearly executed, so a single one would leave the
     // tensor pipe idle while it waits for the next step's inputs.  Each walks
-    // its loop converged and one lane issues (see mma_f16_ts_warp: 2 % of the
-    // plain step, 3 % of the masked one, 12 % of one of many windows).  One
+    // its loop converged and one lane issues (see mma_f16_ts_warp: 0.2 to 2 %
+    // of the plain step, 3 % of the masked one, 12 % of one of many windows).  One
     // issues the scores of each unit as soon as its tiles, scale
     // factors, query terms and S^T slot are ready; the other issues the
     // value MMAs of each unit once its V^T and P are ready.  Each commits

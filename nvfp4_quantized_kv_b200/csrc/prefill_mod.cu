@@ -55,15 +55,15 @@
 // timeout sets NVKV_DEVERR_TIMEOUT and drains.
 //
 // Measured, 24/4 heads, head_dim 256: the long prefill (65,536 + 2,048
-// tokens, cap 50) 3.80 ms = 881 TFLOP/s, 0.53 of the measured matrix rate,
-// bound by the softmax. A CTA of few tiles is bound by its way in and out,
+// tokens, cap 50) 3.86 ms = 867 TFLOP/s, 0.52 of the measured matrix rate (3.95
+// ms, 0.51, under steady load), bound by the softmax. A CTA of few tiles is bound by its way in and out,
 // some 19,000 cycles for one tile: 3,100 to the tile's key range and the
 // barriers, 2,800 to the first page block and Q, 4,000 for K and its scores,
 // 2,400 for the first softmax, 3,600 for the output, 2,900 from its end to
 // the next CTA's start on the SM. Packed documents of 1,500 tokens (8,192 +
-// 2,048): 82.3 us = 494 TFLOP/s; windows of 1,024 in chunks of 512, 301, 777
-// and 65 tokens: 77.6 us, 2.16 waves of such CTAs. A verify step of 24 rows
-// over 2 x 32,768 tokens, 18 CTAs a pair: 45 us; its K and V^T warps are busy
+// 2,048): 86.5 us = 470 TFLOP/s; windows of 1,024 in chunks of 512, 301, 777
+// and 65 tokens: 80.5 us, 2.16 waves of such CTAs. A verify step of 24 rows
+// over 2 x 32,768 tokens, 18 CTAs a pair: 46 us; its K and V^T warps are busy
 // 2,000 of the 2,130 cycles a tile. (Reading a tile's bytes while the tile
 // before is converted gained nothing there and cost the long prefill 11 %.)
 #include <type_traits>
@@ -1126,7 +1126,14 @@ cudaError_t launch_rows(const nvkv_cache &c, const nvkv_seqs &s, const void *q,
 // tiles' time before its first and after its last tile; n CTAs a split run in
 // ceil(n S / SMs) waves; the merge of S fp32 planes of `values` outputs takes
 // kMergeBytes a tile's time. Keys from documents (key_starts) are not known
-// here: the splits of a chunk then only fill the first wave.
+// here: the splits of a chunk then only fill the first wave. The constants put
+// the estimate within 1 % of the best count of each case that was swept (us):
+//   65,536 + 2,048 tokens, 24/4 x 256, cap  1: 4233  3: 3842  4: 3975  5: 3825 (3)
+//   65,536 + 100, the same heads            1: 1363  4: 356   7: 215   8: 352 (7)
+//   20,000 + 300 and 9,000 + 150, the same  1: 539   4: 308   6: 303   8: 315 (6)
+//   30,000 + 2,048, 16/4 x 128              1: 950   3: 973   4: 883   5: 917 (4)
+//   731 of a prefix, 8/2 x 128              1: 26.7  2: 22.7  3: 22.5  4: 28.7 (3)
+// (the count taken in brackets; chunks of few tiles, 2.2 to 2.6 waves, take 1).
 static int estimate_splits(int64_t n, int64_t keys, int64_t values, bool first_wave, int most,
                            int sms) {
   constexpr double kSetup = 6.0, kMergeBytes = 6.0e6;
