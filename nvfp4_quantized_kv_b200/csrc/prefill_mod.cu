@@ -20,10 +20,8 @@
 // no size of q overflows. sm_scale * log2(e) and the power of two come back as
 // one fp32 factor of the row's scores. (sm_scale in Q itself took 11 bits of
 // the product, fewer than the plain verify step's two f16 terms, and ended at
-// |q * sm_scale| = 45,000.) The factor's 16 packed products a tile and thread
-// and the rows' maxima cost 1 to 2 % (long chunk 3.82 -> 3.86 ms, documents
-// 84.2 -> 86.1 us); pairs of scores, not single ones, have the running maximum
-// subtracted to make up for half of it.
+// |q * sm_scale| = 45,000.) The rows' maxima and the factor cost 0.4 to 2.6 %:
+// long chunk 3.85 -> 3.86 ms, windows 80.2 -> 81.1 us, verify step 46.1 -> 47.3.
 //
 // Roles, and what set the pace before each of them (clock64 traces, cycles a
 // tile at head_dim 256 with a cap):
@@ -61,11 +59,12 @@
 // barriers, 2,800 to the first page block and Q, 4,000 for K and its scores,
 // 2,400 for the first softmax, 3,600 for the output, 2,900 from its end to
 // the next CTA's start on the SM. Packed documents of 1,500 tokens (8,192 +
-// 2,048): 86.5 us = 470 TFLOP/s; windows of 1,024 in chunks of 512, 301, 777
-// and 65 tokens: 80.5 us, 2.16 waves of such CTAs. A verify step of 24 rows
+// 2,048): 84.5 us = 481 TFLOP/s; windows of 1,024 in chunks of 512, 301, 777
+// and 65 tokens: 81 us, 2.16 waves of such CTAs. A verify step of 24 rows
 // over 2 x 32,768 tokens, 18 CTAs a pair: 46 us; its K and V^T warps are busy
 // 2,000 of the 2,130 cycles a tile. (Reading a tile's bytes while the tile
 // before is converted gained nothing there and cost the long prefill 11 %.)
+#include <cfloat>
 #include <type_traits>
 
 #include "score_mod.cuh"
@@ -390,9 +389,11 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     named_barrier(10, 16 * 32);
     // (below 2^-100 a row's scores are below 2^-80 whatever the keys)
     const uint32_t eb = max(27u, max(max(top_s[0], top_s[128]), max(top_s[256], top_s[384])) >> 7);
-    // 2^(14 - e), e = eb - 127; a row that is not finite is NaN throughout
-    const float up = __uint_as_float(eb < 255u ? (268u - eb) << 23 : 0x7fc00000u);
-    qfac = a.qscale * __uint_as_float((eb - 14u) << 23);  // 2^(e - 14)
+    // 2^(14 - e), e = eb - 127, with the scale's sign, so that the factor is
+    // positive; a row that is not finite is NaN throughout
+    float up = a.qscale == 0.f ? 0.f : copysignf(__uint_as_float((268u - eb) << 23), a.qscale);
+    if (eb == 255u) up = NAN;
+    qfac = fmaxf(fabsf(a.qscale) * __uint_as_float((eb - 14u) << 23), FLT_MIN);  // 2^(e - 14)
 #pragma unroll
     for (int c16 = 0; c16 < D / 128; ++c16) {
       uint32_t w[16];
@@ -676,6 +677,14 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     // (a row that is none has scores of 0 and a maximum of 0: it never asks
     // for a new one)
     float m = valid ? -INFINITY : 0.f, l = 0.f;
+    // Scores that are neither capped nor biased stay products: one multiply-add
+    // brings in the factor and subtracts the maximum. (Documents 86.0 -> 84.5
+    // us.) The maximum is a rounded product, so all of a row's weights are off
+    // by the same power of two, up to half of the maximum's last place: past
+    // kRawMost, where that could leave f16, the tile's products become scores
+    // first.
+    constexpr bool kRaw = !Mod::kCap && !Mod::kBias;
+    constexpr float kRawMost = 67108864.f;  // 2^26
     for (int j = 0; j < ntiles; ++j) {
       const int slot = j & 1;
       wait_bar(&sready[slot], (j >> 1) & 1, flags, a.err);
@@ -683,6 +692,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       tc_fence_after();
       const uint32_t scol = tl + kColS + slot * 64;
       float x[kKeys];
+      auto to_scores = [&]() {
+#pragma unroll
+        for (int e = 0; e < kKeys; e += 2) {
+          const float2 v = mul_f32x2(make_float2(x[e], x[e + 1]), make_float2(qfac, qfac));
+          x[e] = v.x, x[e + 1] = v.y;
+        }
+      };
       auto load_scores = [&]() {
         uint32_t(&xr)[kKeys] = reinterpret_cast<uint32_t(&)[kKeys]>(x);
         if constexpr (kKeys == 8) {
@@ -693,11 +709,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
             tmem_ld16(scol + koff + e, reinterpret_cast<uint32_t(&)[16]>(xr[e]));
         }
         tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < kKeys; e += 2) {
-          const float2 v = mul_f32x2(make_float2(x[e], x[e + 1]), make_float2(qfac, qfac));
-          x[e] = v.x, x[e + 1] = v.y;
-        }
+        if constexpr (!kRaw) to_scores();
       };
       auto top_score = [&]() {
         float t0 = max3(x[0], x[1], x[2]), t1 = max3(x[3], x[4], x[5]);
@@ -706,7 +718,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
           t0 = max3(t0, x[e], x[e + 1]);
           t1 = max3(t1, x[e + 2], x[e + 3]);
         }
-        return max3(t0, t1, fmaxf(x[kKeys - 2], x[kKeys - 1]));
+        const float top = max3(t0, t1, fmaxf(x[kKeys - 2], x[kKeys - 1]));
+        return kRaw ? top * qfac : top;
       };
       load_scores();
       const int key0 = tile_key(j) + koff;
@@ -802,11 +815,17 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       // visible key yet keeps m = -inf: it subtracts 0 instead). The
       // denominator sums the weights before their rounding, in fp32.
       const float ms = m == -INFINITY ? 0.f : m;
+      float fac = kRaw ? qfac : 1.f;
+      if (kRaw && rare(__any_sync(0xffffffffu, fabsf(ms) > kRawMost))) {
+        to_scores();
+        fac = 1.f;
+      }
       uint32_t pw[kKeys / 2];
       float2 lv0 = make_float2(0.f, 0.f), lv1 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < kKeys / 2; ++e) {
-        const float2 d = add_f32x2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(-ms, -ms));
+        const float2 two = make_float2(x[2 * e], x[2 * e + 1]), neg = make_float2(-ms, -ms);
+        const float2 d = kRaw ? fma_f32x2(two, make_float2(fac, fac), neg) : add_f32x2(two, neg);
         float2 w;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.x) : "f"(d.x));
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.y) : "f"(d.y));
