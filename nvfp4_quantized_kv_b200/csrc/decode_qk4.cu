@@ -1238,7 +1238,9 @@ decode_qk4_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                 for (int w = 0; w < 4; ++w) tmax = fmaxf(tmax, sh.red[w * kNP + stid]);
                 const float m_old = sh.m_s[stid];
-                if (tmax > m_old + kLazyRescale) {
+                // (masked: as the weights ask for it; m + 8 is rounded, and
+                // past 2^27 let a weight of 2^16 pass)
+                if (Mod::kOn ? tmax - m_old > kLazyRescale : tmax > m_old + kLazyRescale) {
                   alpha = exp2f(m_old - tmax);  // 0 when nothing was seen before
                   sh.m_s[stid] = tmax;
                 }

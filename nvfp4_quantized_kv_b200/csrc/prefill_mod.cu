@@ -681,10 +681,10 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
     // brings in the factor and subtracts the maximum. (Documents 86.0 -> 84.5
     // us.) The maximum is a rounded product, so all of a row's weights are off
     // by the same power of two, up to half of the maximum's last place: past
-    // kRawMost, where that could leave f16, the tile's products become scores
-    // first.
+    // kRawMost, where that could leave f16 (2^8 by the lag, 2^4 by the roundings
+    // at most), the tile's products become scores first.
     constexpr bool kRaw = !Mod::kCap && !Mod::kBias;
-    constexpr float kRawMost = 67108864.f;  // 2^26
+    constexpr float kRawMost = 33554432.f;  // 2^25
     for (int j = 0; j < ntiles; ++j) {
       const int slot = j & 1;
       wait_bar(&sready[slot], (j >> 1) & 1, flags, a.err);
@@ -774,14 +774,15 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tmap, const Args a, const
       }
       // One barrier of the two warps that share these rows: may any score
       // pass its row's running maximum by 2^8? (Every score of the tile has
-      // been read once it is passed.)
-      if (rare(named_barrier_or(2 + lq, 64, above > m + kLazyRescale))) {
+      // been read once it is passed.) The difference is exact where it matters;
+      // m + 8 is not past 2^27, where its rounding let a weight of 2^16 pass.
+      if (rare(named_barrier_or(2 + lq, 64, above - m > kLazyRescale))) {
         // The exact maximum of the row's visible scores decides; both threads
         // of the row come to the same result.
         red_s[128 * hf + r] = top_score();
         named_barrier(2 + lq, 64);
         const float tmax = fmaxf(red_s[r], red_s[128 + r]);
-        const bool raise = tmax > -INFINITY && (m == -INFINITY || tmax > m + kLazyRescale);
+        const bool raise = tmax > -INFINITY && (m == -INFINITY || tmax - m > kLazyRescale);
         const float alpha = raise ? exp2f(m - tmax) : 1.f;  // 0 when m = -inf
         // The Tensor Memory loads and stores of O are warp-collective: if any
         // row of the warp moves, the whole warp rescales its half of the
