@@ -152,8 +152,8 @@ nvkv_status nvkv_split_plan(const int32_t *kv_lens_host, int32_t batch, int32_t 
  *     block-scaled tensor-core MMA straight from the cached K codes and
  *     scales; q * sm_scale * log2(e) (fp32) enters as 8 stacked NVFP4
  *     terms after a power-of-two prescale of each row, leaving a remainder
- *     below about 1e-6 of each 16-element group's maximum, for any finite
- *     q; the products are exact and accumulate in fp32.  Weights
+ *     below about 1e-6 of each 16-element group's maximum, or 2e-6 of the
+ *     row's where that is more, for any finite q; the products are exact and accumulate in fp32.  Weights
  *     p = 2^(x - m) from an fp32 exp2, rounded to f16 (relative error
  *     <= 2^-11; below 2^-14 f16 subnormals, absolute error <= 2^-25); the
  *     value sum is an f16 x f16 MMA with fp32 accumulation.

@@ -24,7 +24,8 @@
 // group amax / 6, codes = E2M1 nearest, after a power-of-two prescale 2^k_l
 // that puts the row maximum in [256, 512)); every term shrinks the residual
 // by at least 5.6x (at most one E2M1 half-gap, scale/1, per element), so
-// the dropped remainder is below 0.177^8 = 1e-6 of each group's maximum.
+// the dropped remainder is below 0.177^8 = 1e-6 of each group's maximum (or
+// 2^-19 of the row's, where the smallest scale, 2^-9, comes before that).
 // The terms are the N side of the MMA (row r, term l -> column r*L + l), and
 // the softmax recombines each row's L columns with their 2^-k_l factors in
 // fp32.  The products of E2M1 codes and E4M3 scales are exact; the MMA
