@@ -70,9 +70,9 @@ DECODE_CAPTURE = {
                 "nvfp4_quantized_kv_b200/csrc/sm100.cuh",
                 "nvfp4_quantized_kv_b200/csrc/nvkv_common.cuh",
                 "include/nvkv.h"],
-    "sha256": "aa1322261fcec58cfdba31efd17c38f0f08d60fcc42b763bd73746fd5d9ef0db",
-    "dram_bytes_read": 207592704,
-    "dram_bytes_write": 3468032,
+    "sha256": "404770e941157bf1b39023acf8e873c014eff13a326132c21d668cc3a858f536",
+    "dram_bytes_read": 207640576,
+    "dram_bytes_write": 3360512,
     "kv_bytes": 207363456,
 }
 
